@@ -305,6 +305,96 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
                    int N, int K, int H, int dk, int dv, kda_stream_t stream);
 
 /*
+ * The gated delta rule with ONE decay per head (kda_gdn_*).  Per value head
+ *
+ *     S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+ *     o_t = scale * S_t^T q_t
+ *
+ * with a scalar log-decay g_t per token and head in the place of KDA's one
+ * per channel, and no lower bound on it (-inf resets the state; values below
+ * -104, whose exp is zero in fp32, act as -104).  Conventions shared by the
+ * kda_gdn_* calls, beside those at the top:
+ *   - HV value heads (v, g, beta, o, states) of which HV / HK consecutive
+ *     ones share a query/key head: HV must be a multiple of HK.
+ *   - q, k: bf16, [HK][d_k] per token; v: bf16, [HV][d_v] per token.  A
+ *     token's heads are dense; q_stride, k_stride, v_stride are the elements
+ *     from one token to the next (multiples of 8, at least HK * d_k or
+ *     HV * d_v), so the three may be slices of one projection's output.
+ *     q, k and v are read only.
+ *   - g, beta: [HV] per token, dense; fp32 if gate_f32 is not 0, else bf16.
+ *   - states: fp32 [rows][HV][d_k][d_v], the layout of the kda_* states.
+ *   - slots (optional, device int32 [N]): the state row of each sequence or
+ *     request in a pool of n_slots rows; rows of a call must be distinct (two
+ *     requests on one row leave it with an unspecified mix, without a fault).
+ *     A value outside [0, n_slots) is a padded entry: it has no state.
+ *     slots NULL: row n, and n_slots is not read.
+ */
+
+/*
+ * kda_gdn_chunk_fwd -- chunked forward (prefill, training) over N sequences.
+ *
+ *   cu_seqlens NULL: N sequences of T tokens each, q .. o [N][T] tokens;
+ *   cu_seqlens (device int32 [N + 1]): T tokens in all, sequence n has the
+ *     tokens [cu_seqlens[n], cu_seqlens[n + 1]).  Sequences may be empty.
+ *     Tokens before the first and behind the last are not touched: their o
+ *     rows keep what they held.  Ends outside [0, T] are cut to it and a
+ *     range that does not increase is empty (no fault, whatever the array
+ *     holds); ranges must not overlap.
+ *   o  : bf16 [tokens][HV][d_v], dense
+ *   h0 : state rows to start from, or NULL for zero
+ *   hT : state rows to write the last states to, or NULL; may equal h0
+ *   slots name the rows of both h0 and hT.  A padded sequence starts from
+ *   zero and keeps no state; an empty one copies its h0 row (or zeros).
+ * Tokens behind a sequence's end inside its last 64-token chunk count as zero
+ * whatever they hold.  Two launches: every chunk's state-free part for all
+ * chunks at once, then one CTA per sequence and value head along the chunks.
+ * K and Q enter the products as bf16, the state and what is computed as pairs
+ * of bf16 with fp32 sums: hT is accurate to about 1e-5 of its norm.
+ * Supported: d_k == d_v == 128.  Stream-ordered workspace of 25,600 bytes per
+ * value head and 64-token chunk (at most tokens / 64 + N chunks);
+ * KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in the prefill
+ * (kda_device_status).
+ */
+int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                      const float* h0, void* o, float* hT, const int32_t* cu_seqlens, const int32_t* slots,
+                      int n_slots, float scale, int N, int T, int HK, int HV, int d_k, int d_v,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                      kda_stream_t stream);
+
+/*
+ * kda_gdn_decode_step -- one token for each of N requests, state rows updated
+ * in place; o: bf16 [N][HV][d_v], dense.  A padded request's o is zeroed.
+ * Supported: d_k, d_v in {32, 64, 128}.
+ */
+int kda_gdn_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                        float* state, void* o, const int32_t* slots, int n_slots, float scale,
+                        int N, int HK, int HV, int d_k, int d_v,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                        kda_stream_t stream);
+
+/*
+ * kda_act_pack8 / kda_act_unpack8 -- activation checkpoints in 8 bits: bf16
+ * rows into e4m3 with one power-of-two scale per 32 channels, and back.
+ * `count` (1 to KDA_ACT8_MAX_TENSORS) tensors go in one launch; tensor i has
+ * rows[i] rows of cols[i] channels (cols a multiple of 32), the bf16 rows
+ * strides[i] elements apart when packed (a multiple of 8, at least cols[i])
+ * and dense when unpacked.
+ *   data   : e4m3  [rows][cols], dense
+ *   scales : uint8 [rows][cols / 32]: the biased exponent s of 2^(s - 127)
+ * A block's scale is the smallest power of two with which its largest
+ * magnitude does not pass 448 (at least 2^-127); values are rounded to
+ * nearest, ties to even (those that would become 2^128, which bf16 does not
+ * have, to 240 * 2^120).  Unpacking is exact (bf16 holds every value of the
+ * 8-bit form).  A block that holds an infinity or a NaN gets s = 255 and
+ * unpacks as NaN.  The pointer and size arrays are host arrays.
+ */
+#define KDA_ACT8_MAX_TENSORS 4
+int kda_act_pack8(int count, const void* const* x, void* const* data, void* const* scales,
+                  const int64_t* rows, const int64_t* cols, const int64_t* strides, kda_stream_t stream);
+int kda_act_unpack8(int count, const void* const* data, const void* const* scales, void* const* x,
+                    const int64_t* rows, const int64_t* cols, kda_stream_t stream);
+
+/*
  * kda_device_status -- KDA_OK, or KDA_ERR_TIMEOUT if a kernel of this
  * library gave up on a bounded device-side wait since the last call (every
  * wait between the roles of a prefill kernel, and the backward's waits for

@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libkda.so")
@@ -36,6 +37,7 @@ KDA_ERR_NO_MEMORY = -5
 EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_states", "kda_chunk_fwd_f32",
             "kda_chunk_transition", "kda_state_chain", "kda_chunk_fwd_raw", "kda_decode_step",
             "kda_decode_step_raw", "kda_verify_fwd", "kda_chunk_bwd", "kda_chunk_bwd_raw",
+            "kda_gdn_chunk_fwd", "kda_gdn_decode_step", "kda_act_pack8", "kda_act_unpack8",
             "kda_device_status", "kda_selftest_bounded_wait",
             "kda_status_string", "kda_launch_count", "kda_prefill_path", "kda_version")
 
@@ -92,6 +94,15 @@ def load_library(path: str = LIB_PATH):
     lib.kda_chunk_bwd_raw.restype = i
     lib.kda_verify_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, fp, i, i, i, i, i, vp]
     lib.kda_verify_fwd.restype = i
+    i64, f = ctypes.c_int64, ctypes.c_float
+    lib.kda_gdn_decode_step.argtypes = [vp, vp, vp, vp, vp, fp, vp, vp, i, f, i, i, i, i, i, i64, i64, i64, i, vp]
+    lib.kda_gdn_decode_step.restype = i
+    lib.kda_gdn_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, fp, vp, vp, i, f, i, i, i, i, i, i, i64, i64, i64, i, vp]
+    lib.kda_gdn_chunk_fwd.restype = i
+    lib.kda_act_pack8.argtypes = [i, vp, vp, vp, vp, vp, vp, vp]
+    lib.kda_act_pack8.restype = i
+    lib.kda_act_unpack8.argtypes = [i, vp, vp, vp, vp, vp, vp]
+    lib.kda_act_unpack8.restype = i
     lib.kda_device_status.argtypes = [vp]
     lib.kda_device_status.restype = i
     lib.kda_selftest_bounded_wait.argtypes = [ctypes.c_uint64, vp]
@@ -419,3 +430,227 @@ def chunk_bwd_raw(q_raw, k_raw, v, z, beta, h0, dO, dhT=None, *, want_dh0=True):
     """Gradients of chunk_fwd_raw (kda_chunk_bwd_raw): (dq_raw, dk_raw, dv,
     dz, dbeta, dh0), the prologue and its chain rule inside the kernels."""
     return _bwd("kda_chunk_bwd_raw", q_raw, k_raw, v, z, beta, h0, dO, dhT, want_dh0)
+
+
+# ------------------------------------- one decay per head (gated delta rule) --
+
+def _check_tokens(t, name, lead, heads, d, device):
+    """A bf16 tensor [*lead, heads, d] whose heads are dense and whose tokens
+    are a constant number of elements apart; returns that number."""
+    import torch
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
+    if tuple(t.shape) != tuple(lead) + (heads, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(lead) + (heads, d), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if t.numel() == 0:
+        return heads * d
+    st = t.stride()
+    # the stride of the last token axis with more than one entry
+    step = next((s for s, n in zip(reversed(st[:-2]), reversed(t.shape[:-2])) if n > 1), heads * d)
+    n = 1
+    for s, size in zip(reversed(st[:-2]), reversed(t.shape[:-2])):
+        if size > 1 and s != step * n:
+            raise ValueError("%s: the tokens must be equally spaced, got strides %s" % (name, st))
+        n *= size
+    if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
+        raise ValueError("%s: a token's heads must be dense, got strides %s" % (name, st))
+    if step % 8 != 0 or step < heads * d:
+        raise ValueError("%s: the token stride must be a multiple of 8 and at least %d, got %d" % (name, heads * d, step))
+    return step
+
+
+def _check_gates(g, beta, lead, hv, device):
+    import torch
+    if g.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("g must be torch.float32 or torch.bfloat16, got %s" % g.dtype)
+    _check(g, "g", g.dtype, tuple(lead) + (hv,), device)
+    _check(beta, "beta", g.dtype, tuple(lead) + (hv,), device)
+    return int(g.dtype == torch.float32)
+
+
+def _check_index(t, name, n, device):
+    import torch
+    if t is not None:
+        _check(t, name, torch.int32, (n,), device)
+
+
+def _gdn_sequences(q, cu_seqlens, dev):
+    """(N, T of the C call, number of sequences) of q [B, T, HK, dk] with or without cu_seqlens."""
+    B, T = q.shape[:2]
+    if cu_seqlens is None:
+        return B, T
+    import torch
+    if B != 1:
+        raise ValueError("with cu_seqlens the tokens are packed: the first axis must be 1, got %d" % B)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must have shape (N + 1,), got %s" % (tuple(cu_seqlens.shape),))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, tuple(cu_seqlens.shape), dev)
+    return cu_seqlens.shape[0] - 1, T
+
+
+def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slots=None, o=None, hT=None,
+                  output_final_state=True):
+    """Chunked forward of the gated delta rule with one decay per head
+    (kda_gdn_chunk_fwd), bf16 in and out, fp32 state.
+
+    q, k: [B, T, HK, 128]; v: [B, T, HV, 128] (bf16; slices of one wider tensor
+    are taken as they are); g, beta: [B, T, HV], fp32 or bf16.  With cu_seqlens
+    (int32 [N + 1], on the device) B is 1 and sequence n has the tokens
+    [cu_seqlens[n], cu_seqlens[n + 1]); else N = B.
+
+    h0: [N, HV, 128, 128] fp32 or None; hT may be passed as h0.  With slots
+    (int32 [N], on the device) h0 is a pool [rows, HV, 128, 128]: sequence n
+    starts from row slots[n] and its last state is written there; a slot
+    outside the pool starts from zero and keeps none.  Rows of o that belong to
+    no sequence are not written.  Returns (o, hT), hT the pool with slots."""
+    import torch
+    B, T, HK, dk = q.shape
+    HV, dv = v.shape[-2:]
+    dev = _require_cuda(q)
+    qs = _check_tokens(q, "q", (B, T), HK, dk, dev)
+    ks = _check_tokens(k, "k", (B, T), HK, dk, dev)
+    vs = _check_tokens(v, "v", (B, T), HV, dv, dev)
+    gf = _check_gates(g, beta, (B, T), HV, dev)
+    N, Tc = _gdn_sequences(q, cu_seqlens, dev)
+    _check_index(slots, "slots", N, dev)
+    rows = N
+    if slots is not None:
+        if h0 is None:
+            raise ValueError("slots name rows of a pool of states: h0 must be given")
+        if hT is not None and hT is not h0:
+            raise ValueError("with slots the last states are written to the pool: hT must not be another tensor")
+        rows = h0.shape[0]
+        hT = h0 if output_final_state else None
+    if h0 is not None:
+        _check(h0, "h0", torch.float32, (rows, HV, dk, dv), dev)
+    if o is None:
+        o = torch.empty((B, T, HV, dv), dtype=torch.bfloat16, device=dev)
+    _check(o, "o", torch.bfloat16, (B, T, HV, dv), dev)
+    if hT is None and output_final_state:
+        hT = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=dev)
+    if hT is not None:
+        _check(hT, "hT", torch.float32, (rows, HV, dk, dv), dev)
+    with torch.cuda.device(dev):
+        st = load_library().kda_gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
+                                              _ptr(cu_seqlens), _ptr(slots), rows, float(scale), N, Tc, HK, HV, dk, dv,
+                                              qs, ks, vs, gf, _stream(dev))
+    if st != KDA_OK:
+        raise KdaError("kda_gdn_chunk_fwd", st)
+    return o, hT
+
+
+def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):
+    """One token per request of the gated delta rule with one decay per head
+    (kda_gdn_decode_step); `state` is updated in place.
+
+    q, k: [N, HK, dk]; v: [N, HV, dv] (bf16; slices of one wider tensor are
+    taken as they are); g, beta: [N, HV], fp32 or bf16; state: fp32
+    [N, HV, dk, dv], or a pool [rows, HV, dk, dv] with slots [N] (int32, on the
+    device) naming each request's row; a slot outside the pool marks a padded
+    request (o = 0, no state).  Returns o [N, HV, dv] bf16."""
+    import torch
+    N, HK, dk = q.shape
+    HV, dv = v.shape[-2:]
+    dev = _require_cuda(q)
+    qs = _check_tokens(q, "q", (N,), HK, dk, dev)
+    ks = _check_tokens(k, "k", (N,), HK, dk, dev)
+    vs = _check_tokens(v, "v", (N,), HV, dv, dev)
+    gf = _check_gates(g, beta, (N,), HV, dev)
+    rows = N if slots is None else state.shape[0]
+    _check(state, "state", torch.float32, (rows, HV, dk, dv), dev)
+    _check_index(slots, "slots", N, dev)
+    if o is None:
+        o = torch.empty((N, HV, dv), dtype=torch.bfloat16, device=dev)
+    _check(o, "o", torch.bfloat16, (N, HV, dv), dev)
+    with torch.cuda.device(dev):
+        st = load_library().kda_gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(o),
+                                                _ptr(slots), rows, float(scale), N, HK, HV, dk, dv, qs, ks, vs, gf,
+                                                _stream(dev))
+    if st != KDA_OK:
+        raise KdaError("kda_gdn_decode_step", st)
+    return o
+
+
+# ------------------------------------------- activation checkpoints in 8 bits --
+
+class Packed8(NamedTuple):
+    """A bf16 tensor's 8-bit form: data (torch.float8_e4m3fn, the tensor's
+    shape) and scales (uint8, one per 32 channels of the last axis, the biased
+    exponent of a power of two)."""
+    data: "torch.Tensor"
+    scales: "torch.Tensor"
+
+    @property
+    def shape(self):
+        return self.data.shape
+
+
+ACT8_MAX_TENSORS = 4
+
+
+def _host_array(kind, values):
+    return (kind * len(values))(*values)
+
+
+def act_pack8(*tensors):
+    """The 8-bit form (Packed8) of each of up to four bf16 tensors, in one
+    launch (kda_act_pack8).  The last axis must be a multiple of 32; the
+    tensors may be slices of wider ones as long as their rows are equally
+    spaced.  One tensor gives a Packed8, several a tuple of them."""
+    import torch
+    if not 1 <= len(tensors) <= ACT8_MAX_TENSORS:
+        raise ValueError("act_pack8 takes 1 to %d tensors, got %d" % (ACT8_MAX_TENSORS, len(tensors)))
+    dev = _require_cuda(tensors[0])
+    rows, cols, strides, out = [], [], [], []
+    for n, t in enumerate(tensors):
+        name = "tensor %d" % n
+        if t.dim() < 1 or t.shape[-1] % 32 != 0:
+            raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(t.shape)))
+        rows_of = t if t.dim() >= 3 else t.unsqueeze(-2)        # [..., heads, channels]
+        strides.append(_check_tokens(rows_of, name, rows_of.shape[:-2], *rows_of.shape[-2:], dev))
+        cols.append(rows_of.shape[-2] * rows_of.shape[-1])
+        rows.append(t.numel() // cols[-1] if cols[-1] else 0)
+        out.append(Packed8(torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=dev),
+                           torch.empty(t.shape[:-1] + (t.shape[-1] // 32,), dtype=torch.uint8, device=dev)))
+    n = len(tensors)
+    with torch.cuda.device(dev):
+        st = load_library().kda_act_pack8(
+            n, _host_array(ctypes.c_void_p, [t.data_ptr() for t in tensors]),
+            _host_array(ctypes.c_void_p, [p.data.data_ptr() for p in out]),
+            _host_array(ctypes.c_void_p, [p.scales.data_ptr() for p in out]),
+            _host_array(ctypes.c_int64, rows), _host_array(ctypes.c_int64, cols), _host_array(ctypes.c_int64, strides),
+            _stream(dev))
+    if st != KDA_OK:
+        raise KdaError("kda_act_pack8", st)
+    return out[0] if n == 1 else tuple(out)
+
+
+def _check_packed8(p, name, device):
+    import torch
+    if p.data.dim() < 1 or p.data.shape[-1] % 32 != 0:
+        raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(p.data.shape)))
+    _check(p.data, name + ".data", torch.float8_e4m3fn, p.data.shape, device)
+    _check(p.scales, name + ".scales", torch.uint8, p.data.shape[:-1] + (p.data.shape[-1] // 32,), device)
+
+
+def act_unpack8(packed, *, out=None):
+    """The bf16 values that a Packed8 stands for, exactly (kda_act_unpack8)."""
+    import torch
+    dev = _require_cuda(packed.data)
+    _check_packed8(packed, "packed", dev)
+    if out is None:
+        out = torch.empty(packed.data.shape, dtype=torch.bfloat16, device=dev)
+    _check(out, "out", torch.bfloat16, packed.data.shape, dev)
+    last = packed.data.shape[-1]
+    with torch.cuda.device(dev):
+        st = load_library().kda_act_unpack8(
+            1, _host_array(ctypes.c_void_p, [packed.data.data_ptr()]),
+            _host_array(ctypes.c_void_p, [packed.scales.data_ptr()]),
+            _host_array(ctypes.c_void_p, [out.data_ptr()]),
+            _host_array(ctypes.c_int64, [packed.data.numel() // last if last else 0]),
+            _host_array(ctypes.c_int64, [last]), _stream(dev))
+    if st != KDA_OK:
+        raise KdaError("kda_act_unpack8", st)
+    return out

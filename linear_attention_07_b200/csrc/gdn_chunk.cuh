@@ -1,0 +1,137 @@
+// Chunked form of the gated delta rule with one decay per head (d_k = d_v =
+// 128): what the forward and the backward share.
+//
+// A chunk is C = 64 tokens.  With G_r the running sum of g inside the chunk,
+// gam = exp(G), eta_r = exp(G_last - G_r), D_ri = exp(G_r - G_i):
+//     A  = strict_lower(beta_r D_ri k_r . k_i),   X = (I + A)^-1
+//     R  = beta (V - gam K S0),   U = X R
+//     O  = scale gam Q S0 + P U,  P = scale lower(D_ri q_r . k_i)
+//     S1 = gam_last S0 + K^T (eta U)
+// One decay per head is one factor per token pair or token: K and Q enter
+// every product as they are in memory, exact in bf16.  Everything else (the
+// state, X, R, U) is fp32 and enters as the sum of two bf16 numbers (16
+// significant bits; the products hi hi, hi lo and lo hi are kept), so the
+// state carries about fp32 accuracy through bf16 tensor-core products.
+//
+// Sequences are cut into chunks at their own begins.  Chunk c of sequence n,
+// which begins at token a, has the workspace slot a / 64 + n + c: a sequence
+// of L tokens from a needs ceil(L / 64) <= (a + L) / 64 - a / 64 + 1 of them,
+// so slots never collide, and no prefix sum over the lengths is needed.
+#pragma once
+#include <cuda.h>
+
+#include "gdn_common.cuh"
+#include "kda_tc.cuh"
+
+namespace kda {
+namespace gdn {
+
+constexpr int C = 64;
+constexpr int D = 128;
+
+// What the prep kernel leaves per (slot, value head), in bytes.  X and P are
+// stored as the no-swizzle operand layout wants them: element (r, i) at
+// (r / 8) * 1024 + (i / 8) * 128 + (r % 8) * 16 + (i % 8) * 2.
+constexpr uint32_t REC_XH = 0;                       // X, upper 8 bits   [64 x 64] bf16
+constexpr uint32_t REC_XL = REC_XH + C * C * 2;      // X, the rest
+constexpr uint32_t REC_P = REC_XL + C * C * 2;       // P, one rounding   [64 x 64] bf16
+constexpr uint32_t REC_GAM = REC_P + C * C * 2;      // gam_r   [64] fp32
+constexpr uint32_t REC_ETA = REC_GAM + C * 4;        // eta_r
+constexpr uint32_t REC_BETA = REC_ETA + C * 4;       // beta_r (0 behind the sequence)
+constexpr uint32_t REC_LAST = REC_BETA + C * 4;      // gam_last
+constexpr uint32_t REC_BYTES = 25600;
+static_assert(REC_LAST + 4 <= REC_BYTES && REC_BYTES % 128 == 0, "record");
+
+__host__ __device__ inline int64_t slot_count(const Seqs& s) { return s.tokens / C + s.n_seq; }
+
+__device__ __forceinline__ int64_t first_slot(const Seqs& s, int n)
+{
+    int a, b;
+    seq_range(s, n, a, b);
+    return (int64_t)(a / C) + n;
+}
+
+// Sequence and chunk of a slot; false if the slot belongs to none.
+__device__ __forceinline__ bool slot_chunk(const Seqs& s, int64_t slot, int& n, int& chunk, int& begin, int& end)
+{
+    int lo = 0, hi = s.n_seq - 1;                    // the last n with first_slot(n) <= slot
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_slot(s, mid) <= slot) lo = mid; else hi = mid - 1;
+    }
+    n = lo;
+    seq_range(s, n, begin, end);
+    const int64_t c = slot - ((int64_t)(begin / C) + n);
+    if (c < 0 || c * C >= end - begin) return false;
+    chunk = (int)c;
+    return true;
+}
+
+// Descriptor of a 128-byte-swizzled tile of 128-byte rows (as a TMA box of 64
+// bf16 columns leaves it, 1024-byte aligned): groups of 8 rows are 1024 bytes
+// apart.  K-major (the row is a vector along K): 16 elements of K further are
+// 32 bytes further.  MN-major (the row is a vector along M or N): 16 rows
+// further along K are 2048 bytes further.
+__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr)
+{
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(1024 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor, kind::f16 with bf16 A and B and fp32 sums.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = false, bool b_mn = false)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(mbar) : "memory");
+}
+
+// Two fp32 values as packed bf16 pairs hi and lo with x ~ hi + lo (each
+// rounded to nearest: 16 significant bits together).
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void split_bf16(float a, float b, float& hi, float& lo)
+{
+    const uint32_t h = pack_bf16(a, b);
+    hi = __uint_as_float(h);
+    lo = __uint_as_float(pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u)));
+}
+
+// A bounded wait of one role.  Once any wait of the CTA has expired, every
+// later one returns at once: the roles run to their ends without issuing.
+struct Waits {
+    volatile int* abort;
+    int* status;
+    uint64_t ns;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
+    {
+        if (*abort) return false;
+        if (tc::mbar_wait(bar, parity, ns)) return true;
+        *abort = 1;
+        atomicExch(status, (int)KDA_ERR_TIMEOUT);
+        return false;
+    }
+};
+constexpr uint64_t DRAIN_NS = 20000000ull;           // after an expired wait: 20 ms for what is in flight
+
+// Host: bf16 [tokens][cols] with a row stride in elements, boxes of 64 rows by
+// box_cols (128-byte swizzle for boxes of 64 columns).
+bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, int box_cols);
+
+cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
+                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, cudaStream_t stream);
+
+}  // namespace gdn
+}  // namespace kda

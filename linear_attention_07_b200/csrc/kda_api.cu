@@ -69,6 +69,18 @@ cudaError_t prefill_serial_launch(const void* q, const void* k, const void* v,
                                   void* o, float* hT, int B, int T, int H,
                                   int dk, int dv, cudaStream_t stream);
 
+cudaError_t gdn_step_launch(const void* q, const void* k, const void* v, const void* g, const void* beta, float* state,
+                            void* o, const int* slots, int n_slots, float scale, int N, int HK, int HV, int dk, int dv,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32, cudaStream_t stream);
+cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                               const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
+                               float scale, int N, int T, int HK, int HV, int64_t q_stride, int64_t k_stride,
+                               int64_t v_stride, bool gate_f32, cudaStream_t stream);
+int gdn_prep_status(cudaStream_t stream);
+int gdn_forward_status(cudaStream_t stream);
+cudaError_t act8_launch(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
+                        const int64_t* cols, const int64_t* strides, bool pack, cudaStream_t stream);
+
 static bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 static bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
@@ -104,6 +116,34 @@ static int check_prefill(const void* q, const void* k, const void* v, const void
         if (beta == nullptr) return KDA_ERR_INVALID_ARG;
     }
     return KDA_OK;
+}
+
+// Common checks of the kda_gdn_* entry points.
+static int check_gdn_heads(int HK, int HV, int dk, int dv, int64_t qs, int64_t ks, int64_t vs)
+{
+    if (HK < 0 || HV < 0 || dk <= 0 || dv <= 0) return KDA_ERR_INVALID_ARG;
+    if (HK > 65535 || HV > 65535 || dk > 4096 || dv > 4096) return KDA_ERR_UNSUPPORTED;
+    if (HK == 0 || HV == 0) return HK == HV ? KDA_OK : KDA_ERR_INVALID_ARG;
+    if (HV % HK != 0) return KDA_ERR_INVALID_ARG;
+    if (qs % 8 != 0 || ks % 8 != 0 || vs % 8 != 0) return KDA_ERR_INVALID_ARG;
+    if (qs < (int64_t)HK * dk || ks < (int64_t)HK * dk || vs < (int64_t)HV * dv) return KDA_ERR_INVALID_ARG;
+    const int64_t lim = (int64_t)1 << 30;
+    if (qs > lim || ks > lim || vs > lim) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+// Sequences and tokens of the chunked calls.
+static int check_gdn_tokens(const void* cu, const void* slots, int n_slots, int N, int T, int HV)
+{
+    if (N < 0 || T < 0 || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    const int64_t tokens = cu ? T : (int64_t)N * T;
+    if (tokens > 0x7fffff00ll || (int64_t)N * HV > 0x7fffffffll) return KDA_ERR_UNSUPPORTED;
+    if ((tokens / 64 + N) * HV > 0x7fffffffll) return KDA_ERR_UNSUPPORTED;
+    if (((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(slots)) & 3u) != 0) return KDA_ERR_INVALID_ARG;
+    return KDA_OK;
+}
+static bool elem_ok(const void* p, unsigned bytes)
+{
+    return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
 }  // namespace kda
@@ -285,6 +325,77 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
                                    (cudaStream_t)stream));
 }
 
+int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                      const float* h0, void* o, float* hT, const int32_t* cu_seqlens, const int32_t* slots,
+                      int n_slots, float scale, int N, int T, int HK, int HV, int d_k, int d_v,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                      kda_stream_t stream)
+{
+    int st = check_gdn_heads(HK, HV, d_k, d_v, q_stride, k_stride, v_stride);
+    if (st == KDA_OK) st = check_gdn_tokens(cu_seqlens, slots, n_slots, N, T, HV);
+    if (st != KDA_OK) return st;
+    if (!(d_k == 128 && d_v == 128)) return KDA_ERR_UNSUPPORTED;
+    if (!opt_ptr_ok(h0) || !opt_ptr_ok(hT)) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)N * HV == 0) return KDA_OK;
+    if (T == 0 && hT == nullptr) return KDA_OK;
+    if (T > 0) {
+        if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(o)) return KDA_ERR_INVALID_ARG;
+        const unsigned ge = gate_f32 ? 4 : 2;
+        if (!elem_ok(g, ge) || !elem_ok(beta, ge)) return KDA_ERR_INVALID_ARG;
+    }
+    return status_of(gdn_forward_launch(q, k, v, g, beta, h0, o, hT, cu_seqlens, slots, n_slots, scale, N, T, HK, HV,
+                                        q_stride, k_stride, v_stride, gate_f32 != 0, (cudaStream_t)stream));
+}
+
+int kda_gdn_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                        float* state, void* o, const int32_t* slots, int n_slots, float scale,
+                        int N, int HK, int HV, int d_k, int d_v,
+                        int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                        kda_stream_t stream)
+{
+    if (N < 0 || n_slots < 0) return KDA_ERR_INVALID_ARG;
+    if (d_k <= 0 || d_v <= 0) return KDA_ERR_INVALID_ARG;
+    if (!dim_ok(d_k) || !dim_ok(d_v)) return KDA_ERR_UNSUPPORTED;
+    const int st = check_gdn_heads(HK, HV, d_k, d_v, q_stride, k_stride, v_stride);
+    if (st != KDA_OK) return st;
+    if ((int64_t)N * HV == 0) return KDA_OK;
+    if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(state) || !ptr_ok(o)) return KDA_ERR_INVALID_ARG;
+    const unsigned ge = gate_f32 ? 4 : 2;
+    if (!elem_ok(g, ge) || !elem_ok(beta, ge) || (slots && !elem_ok(slots, 4))) return KDA_ERR_INVALID_ARG;
+    return status_of(gdn_step_launch(q, k, v, g, beta, state, o, slots, slots ? n_slots : N, scale, N, HK, HV, d_k, d_v,
+                                     q_stride, k_stride, v_stride, gate_f32 != 0, (cudaStream_t)stream));
+}
+
+static int act8_any(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
+                    const int64_t* cols, const int64_t* strides, bool pack, kda_stream_t stream)
+{
+    if (count < 1 || count > KDA_ACT8_MAX_TENSORS) return KDA_ERR_INVALID_ARG;
+    if (!src || !dst || !scales || !rows || !cols) return KDA_ERR_INVALID_ARG;
+    for (int i = 0; i < count; ++i) {
+        if (rows[i] < 0 || cols[i] < 0 || cols[i] % 32 != 0) return KDA_ERR_INVALID_ARG;
+        if (cols[i] >= (int64_t)1 << 31 || rows[i] >= (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+        if (rows[i] * (cols[i] / 16) > (int64_t)0x7fffffff * 256) return KDA_ERR_UNSUPPORTED;   // the grid's x
+        if (rows[i] * cols[i] == 0) continue;
+        if (strides && (strides[i] % 8 != 0 || strides[i] < cols[i] || strides[i] >= (int64_t)1 << 40))
+            return KDA_ERR_INVALID_ARG;
+        if (!ptr_ok(src[i]) || !ptr_ok(dst[i]) || scales[i] == nullptr) return KDA_ERR_INVALID_ARG;
+    }
+    return status_of(act8_launch(count, src, dst, scales, rows, cols, strides, pack, (cudaStream_t)stream));
+}
+
+int kda_act_pack8(int count, const void* const* x, void* const* data, void* const* scales,
+                  const int64_t* rows, const int64_t* cols, const int64_t* strides, kda_stream_t stream)
+{
+    if (!strides) return KDA_ERR_INVALID_ARG;
+    return act8_any(count, x, data, scales, rows, cols, strides, true, stream);
+}
+
+int kda_act_unpack8(int count, const void* const* data, const void* const* scales, void* const* x,
+                    const int64_t* rows, const int64_t* cols, kda_stream_t stream)
+{
+    return act8_any(count, data, x, const_cast<void* const*>(scales), rows, cols, nullptr, false, stream);
+}
+
 const char* kda_status_string(int status)
 {
     switch (status) {
@@ -300,10 +411,13 @@ const char* kda_status_string(int status)
 
 int kda_device_status(kda_stream_t stream)
 {
-    const int a = prefill_device_status((cudaStream_t)stream);
-    const int b = bwd_device_status((cudaStream_t)stream);
-    if (a == KDA_ERR_CUDA || b == KDA_ERR_CUDA) return KDA_ERR_CUDA;
-    return a != KDA_OK ? a : b;
+    int st = KDA_OK;
+    for (auto* part : {prefill_device_status, bwd_device_status, gdn_prep_status, gdn_forward_status}) {
+        const int s = part((cudaStream_t)stream);     // each reads and clears its own word
+        if (s == KDA_ERR_CUDA) return s;
+        if (s != KDA_OK) st = s;
+    }
+    return st;
 }
 
 int kda_selftest_bounded_wait(uint64_t limit_ns, kda_stream_t stream)
