@@ -4,12 +4,12 @@
 // A chunk is C = 64 tokens.  With G_r the running sum of g inside the chunk,
 // gam = exp(G), eta_r = exp(G_last - G_r), D_ri = exp(G_r - G_i):
 //     A  = strict_lower(beta_r D_ri k_r . k_i),   X = (I + A)^-1
-//     R  = beta (V - gam K S0),   U = X R
+//     T  = X diag(beta),   U = T (V - gam K S0)
 //     O  = scale gam Q S0 + P U,  P = scale lower(D_ri q_r . k_i)
 //     S1 = gam_last S0 + K^T (eta U)
 // One decay per head is one factor per token pair or token: K and Q enter
 // every product as they are in memory, exact in bf16.  Everything else (the
-// state, X, R, U) is fp32 and enters as the sum of two bf16 numbers (16
+// state, T, gam K S0, U) is fp32 and enters as the sum of two bf16 numbers (16
 // significant bits; the products hi hi, hi lo and lo hi are kept), so the
 // state carries about fp32 accuracy through bf16 tensor-core products.
 //
@@ -29,18 +29,20 @@ namespace gdn {
 constexpr int C = 64;
 constexpr int D = 128;
 
-// What the prep kernel leaves per (slot, value head), in bytes.  X and P are
+// What the prep kernel leaves per (slot, value head), in bytes.  T and P are
 // stored as the no-swizzle operand layout wants them: element (r, i) at
 // (r / 8) * 1024 + (i / 8) * 128 + (r % 8) * 16 + (i % 8) * 2.
-constexpr uint32_t REC_XH = 0;                       // X, upper 8 bits   [64 x 64] bf16
-constexpr uint32_t REC_XL = REC_XH + C * C * 2;      // X, the rest
-constexpr uint32_t REC_P = REC_XL + C * C * 2;       // P, one rounding   [64 x 64] bf16
-constexpr uint32_t REC_GAM = REC_P + C * C * 2;      // gam_r   [64] fp32
-constexpr uint32_t REC_ETA = REC_GAM + C * 4;        // eta_r
-constexpr uint32_t REC_BETA = REC_ETA + C * 4;       // beta_r (0 behind the sequence)
-constexpr uint32_t REC_LAST = REC_BETA + C * 4;      // gam_last
-constexpr uint32_t REC_BYTES = 25600;
-static_assert(REC_LAST + 4 <= REC_BYTES && REC_BYTES % 128 == 0, "record");
+constexpr uint32_t REC_TH = 0;                       // T = X diag(beta), upper 8 bits   [64 x 64] bf16
+constexpr uint32_t REC_TL = REC_TH + C * C * 2;      // T, the rest
+constexpr uint32_t REC_NGAM = REC_TL + C * C * 2;    // -gam_r   [64] fp32
+constexpr uint32_t REC_ETA = REC_NGAM + C * 4;       // eta_r
+constexpr uint32_t REC_GQ = REC_ETA + C * 4;         // scale gam_r
+constexpr uint32_t REC_BETA = REC_GQ + C * 4;        // beta_r (0 behind the sequence)
+constexpr uint32_t REC_PH = REC_BETA + C * 4;        // P, likewise
+constexpr uint32_t REC_PL = REC_PH + C * C * 2;
+constexpr uint32_t REC_BYTES = REC_PL + C * C * 2;
+constexpr uint32_t REC_T_BYTES = REC_PH;             // T and the gates; P comes later in a chunk
+static_assert(REC_BYTES == 33792 && REC_T_BYTES % 1024 == 0, "record");
 
 __host__ __device__ inline int64_t slot_count(const Seqs& s) { return s.tokens / C + s.n_seq; }
 
@@ -84,6 +86,38 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// Four K steps of one product by a converged warp (one elected lane issues;
+// inlined, so that the descriptors stay warp-uniform).  A from tensor memory (8
+// columns per step) or shared memory, B from shared memory; the steps are in
+// descriptor units (16 bytes).
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+        "add.u64 b1, %2, %3;\n\tadd.u64 b2, b1, %3;\n\tadd.u64 b3, b2, %3;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n\t}\n"
+        :: "r"(d), "r"(a), "l"(b), "l"(b_step), "r"(idesc), "r"(more) : "memory");
+}
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t a_step, uint64_t b, uint64_t b_step, uint32_t idesc,
+                                     uint32_t more)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "add.u64 a1, %1, %2;\n\tadd.u64 a2, a1, %2;\n\tadd.u64 a3, a2, %2;\n\t"
+        "add.u64 b1, %3, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %3, %5, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n\t}\n"
+        :: "r"(d), "l"(a), "l"(a_step), "l"(b), "l"(b_step), "r"(idesc), "r"(more) : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t mbar)
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -93,6 +127,24 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  :: "r"(dst), "l"(src), "r"(bytes), "r"(mbar) : "memory");
+}
+
+// Packed fp32 pairs: one instruction for two values.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 // Two fp32 values as packed bf16 pairs hi and lo with x ~ hi + lo (each
@@ -106,7 +158,9 @@ __device__ __forceinline__ void split_bf16(float a, float b, float& hi, float& l
 {
     const uint32_t h = pack_bf16(a, b);
     hi = __uint_as_float(h);
-    lo = __uint_as_float(pack_bf16(a - __uint_as_float(h << 16), b - __uint_as_float(h & 0xffff0000u)));
+    const float2 r = fma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), make_float2(-1.f, -1.f),
+                          make_float2(a, b));         // exact
+    lo = __uint_as_float(pack_bf16(r.x, r.y));
 }
 
 // A bounded wait of one role.  Once any wait of the CTA has expired, every
@@ -117,8 +171,19 @@ struct Waits {
     uint64_t ns;
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const
     {
-        if (*abort) return false;
-        if (tc::mbar_wait(bar, parity, ns)) return true;
+        if (ns != 0 && tc::mbar_try_wait(bar, parity)) return true;
+        return slow(bar, parity);
+    }
+    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
+    {
+        if (ns == 0 && tc::mbar_test_wait(bar, parity)) return true;
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (ns != 0 && !*abort) {
+#pragma unroll 1
+            for (int i = 0; i < 64; ++i)              // each try may itself block for a while
+                if (tc::mbar_try_wait(bar, parity)) return true;
+            if (tc::globaltimer_ns() - t0 > ns) break;
+        }
         *abort = 1;
         atomicExch(status, (int)KDA_ERR_TIMEOUT);
         return false;
@@ -127,8 +192,8 @@ struct Waits {
 constexpr uint64_t DRAIN_NS = 20000000ull;           // after an expired wait: 20 ms for what is in flight
 
 // Host: bf16 [tokens][cols] with a row stride in elements, boxes of 64 rows by
-// box_cols (128-byte swizzle for boxes of 64 columns).
-bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, int box_cols);
+// 64 columns with the 128-byte swizzle.
+bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride);
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
                         uint8_t* rec, float scale, int HK, int HV, bool gate_f32, cudaStream_t stream);

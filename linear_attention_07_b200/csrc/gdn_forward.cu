@@ -1,29 +1,35 @@
 // Gated delta rule, one decay per head: chunked forward, after the prep kernel
 // (gdn_prep.cu).  One CTA per sequence and value head carries the state
 // through the chunks; per chunk (gdn_chunk.cuh)
-//     X_K = K S,  X_Q = Q S,  R = beta (V - gam X_K),  U = X R,
+//     X_K = K S,  X_Q = Q S,  U = T V - T (gam X_K),
 //     O = scale gam X_Q + P U,  S <- gam_last S + K^T (eta U).
 // Every product is computed transposed, with d_v as the M = 128 of the MMA:
-//     X^T = S^T K^T,  U^T = R^T X^T,  O^T = U^T P^T,  S^T += (eta U)^T K,
-// so the left operands (S, R, U: fp32 values as two bf16) go from registers
-// to tensor memory, the right ones (K, Q, X, P: bf16 in memory) stay as TMA
-// left them, and thread j owns column j of S, R, U and O throughout: nothing
-// the chain computes passes through shared memory.  Sums are fp32; the state
-// is updated in fp32 registers (never accumulated in tensor memory, whose
-// additions need not round to nearest).
+//     X^T = S^T K^T,  U^T = V^T T^T - (gam X)^T T^T,  O^T = U^T P^T,
+//     S^T += (eta U)^T K,
+// so the left operands that are computed here (S, gam X_K, U: fp32 values as
+// two bf16) go from registers to tensor memory, everything that is in memory
+// (K, Q, V, T, P: bf16) is read by the MMA as TMA left it, and thread j owns
+// column j of S, X, U and O throughout: nothing the chain computes passes
+// through shared memory.  Sums are fp32; the state is updated in fp32
+// registers (never accumulated in tensor memory, whose additions need not
+// round to nearest).
 //
-// Roles (14 warps):
-//   warps 0-7   chain: thread (j, half) holds S[dk][j] for 32 + 32 values of
-//               dk; R, U, the state update, and their split into bf16 pairs
-//   warps 8-11  output: thread j takes O^T's row j, 64 tokens, through
-//               shared memory to 16-byte stores, off the chain's path
-//   warp 12     issues every MMA
-//   warp 13     loads: K, Q (128-byte swizzle), V, the chunk's record, two
-//               stages
-// The chain is what bounds it (per chunk three products that wait for one
-// another, with the conversions between them).  To shorten it the state is
-// updated in two halves of d_k: while the second half of K^T U is computed
-// the first half is updated and split, and X_K starts on it.
+// Roles (22 warps):
+//   warps 0-15  chain: thread (j, part) holds S[dk][j] for 16 + 16 values of
+//               dk and takes 16 of the chunk's tokens; gam X_K, U, the state
+//               update, and their split into bf16 pairs
+//   warps 16-19 output: thread j takes O^T's row j, 64 tokens, through
+//               shared memory (where V was) to 16-byte stores, off the
+//               chain's path
+//   warp 20     issues every MMA
+//   warp 21     loads: K, Q, V (128-byte swizzle), T and the gates into three
+//               stages, P into one buffer
+// Per chunk the MMAs take 2,900 cycles (84 of 32 to 48 cycles) and the chain
+// waits for three of them in turn (X_K, U, K^T U), with the conversions
+// between; what the chain does not wait for (T V, X_Q, O) is issued behind
+// those, to run while it converts.  The state is updated in two halves of
+// d_k: while the second half of K^T U is computed the first half is updated
+// and split, and X_K starts on it.
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -33,29 +39,32 @@ __device__ int g_fwd_status;
 
 namespace fw {
 
-constexpr int N_CHAIN = 8, N_OUT = 4;                // warps
+constexpr int N_CHAIN = 16, N_OUT = 4;               // warps
 constexpr int W_MMA = N_CHAIN + N_OUT, W_LOAD = W_MMA + 1;
 constexpr int NT = 32 * (W_LOAD + 1);
 
-// a stage: K0 Q0 K1 Q1 (boxes of 64 tokens x 64 channels), V rows, record
-constexpr uint32_t S_V = 4 * 8192;
-constexpr uint32_t S_REC = S_V + C * D * 2;
-constexpr uint32_t STAGE = S_REC + REC_BYTES;
+// a stage: K0 Q0 K1 Q1 V0 V1 (boxes of 64 tokens x 64 channels), T and gates
+constexpr int STAGES = 3;
+constexpr uint32_t BOX = C * 64 * 2;
+constexpr uint32_t S_V = 4 * BOX;
+constexpr uint32_t S_REC = 6 * BOX;
+constexpr uint32_t STAGE = S_REC + REC_T_BYTES;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
-constexpr uint32_t OST = 2 * STAGE;                  // o staging [64][128] bf16
-constexpr uint32_t SMEM = OST + C * D * 2 + 1024;
+constexpr uint32_t S_P = STAGES * STAGE;             // P, one buffer
+constexpr uint32_t P_BYTES = REC_BYTES - REC_PH;
+constexpr uint32_t SMEM = S_P + P_BYTES + 1024;
 
 // barriers
-enum { B_FULL = 0, B_READY = 2, B_EMPTY = 4, B_MX = 6, B_MU, B_MD0, B_MD1, B_MO, B_S0, B_S1, B_R, B_U, B_OFREE, B_DRAIN, N_BAR };
+enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MX, B_MU, B_MD0, B_MD1, B_MO, B_S0, B_S1, B_R, B_U, B_UO, B_OFREE, B_DRAIN, N_BAR };
 
 // tensor memory columns
 constexpr uint32_t T_SH = 0, T_SL = 64;              // S^T, upper and lower half: two d_k per column
 constexpr uint32_t T_XK = 128, T_U = 192;            // X_K^T, U^T
 constexpr uint32_t T_D = 128;                        // (K^T U)^T, when X_K and U are done with
 constexpr uint32_t T_XQ = 256;
-constexpr uint32_t T_RH = 320, T_RL = 352;           // R^T, then (eta U)^T
-constexpr uint32_t T_UB = 384;                       // U^T rounded once, for O
-constexpr uint32_t T_O = 416;
+constexpr uint32_t T_RH = 320, T_RL = 352;           // -(gam X_K)^T, then (eta U)^T
+constexpr uint32_t T_UH = 384, T_UL = 416;           // U^T, for O
+constexpr uint32_t T_O = 448;
 
 struct Args {
     Seqs seqs;
@@ -93,8 +102,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b >= B_EMPTY && b < B_EMPTY + 2 ? N_CHAIN + N_OUT
-                            : b == B_S0 || b == B_S1 || b == B_R || b == B_U ? N_CHAIN : b == B_OFREE ? N_OUT : 1;
+            const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
+                            : b == B_S0 || b == B_S1 || b == B_R || b == B_U || b == B_UO ? N_CHAIN : b == B_OFREE ? N_OUT : 1;
             mbar_init(bar(b), count);
         }
         fence_mbar_init();
@@ -111,118 +120,113 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const Waits wait = {&s_abort, &g_fwd_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
-        const int sp = warp & 3, half = warp >> 2, j = 32 * sp + lane;
+        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        float S[2][32];                              // S[b][i]: d_k = 64 b + 32 half + i
+        float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
         const float* h = p.h0 && row >= 0 ? p.h0 + ((int64_t)row * p.HV + hv) * D * D + j : nullptr;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 32 * half + i) * D] : 0.f;
-        auto put = [&](uint32_t hi_col, uint32_t lo_col, const float (&x)[32]) {
-            float hi[16], lo[16];
+            for (int i = 0; i < 16; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 16 * part + i) * D] : 0.f;
+        // 16 values into the operand columns of this part, two per column
+        auto put = [&](uint32_t hi_col, uint32_t lo_col, const float (&x)[16]) {
+            float hi[8], lo[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
-            tmem_st16(t + hi_col + 16 * half, hi);
-            tmem_st16(t + lo_col + 16 * half, lo);
+            for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+            tmem_st8(t + hi_col + 8 * part, hi);
+            tmem_st8(t + lo_col + 8 * part, lo);
         };
         auto arrive = [&](int b) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(b));
         };
-        auto give_state = [&](int b) {
-            put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
+        auto give = [&](int b) {                     // what this warp put is there
             wait_st();
             fence_before_sync();
-            arrive(B_S0 + b);
+            arrive(b);
         };
-        if (chunks > 0) {
-            give_state(0);
-            give_state(1);
-        }
+        if (chunks > 0)
+            for (int b = 0; b < 2; ++b) {
+                put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
+                give(B_S0 + b);
+            }
+        int s = 0, ph = 0;                           // stage and its phase
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
-            const uint8_t* st = sm + s * STAGE;
-            const float* gam = reinterpret_cast<const float*>(st + S_REC + REC_GAM) + 32 * half;
-            const float* eta = reinterpret_cast<const float*>(st + S_REC + REC_ETA) + 32 * half;
-            const float* bet = reinterpret_cast<const float*>(st + S_REC + REC_BETA) + 32 * half;
-            const __nv_bfloat16* V = reinterpret_cast<const __nv_bfloat16*>(st + S_V) + 32 * half * D + j;
-            wait(bar(B_FULL + s), (c >> 1) & 1);
-            wait(bar(B_READY + s), (c >> 1) & 1);
-            const float last = *reinterpret_cast<const float*>(st + S_REC + REC_LAST);
-            float x[32];
+            const float4* gates = reinterpret_cast<const float4*>(sm + s * STAGE + S_REC + REC_NGAM) + 4 * part;
+            float x[16];
+            wait(bar(B_FULL + s), ph);
+            const float last = -reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM)[C - 1];
+            // x times one gate per token (NGAM or ETA: 16 float4 apart)
+            auto scale_by = [&](int which) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = gates[16 * which + i];
+                    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
+                    const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
+                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+                }
+            };
             wait(bar(B_MX), c & 1);
             fence_after_sync();
-            tmem_ld32(t + T_XK + 32 * half, x);
+            tmem_ld16(t + T_XK + 16 * part, x);
             wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(gam + i), b4 = *reinterpret_cast<const float4*>(bet + i);
-                x[i] = b4.x * fmaf(-g4.x, x[i], to_f32(V[(i + 0) * D]));
-                x[i + 1] = b4.y * fmaf(-g4.y, x[i + 1], to_f32(V[(i + 1) * D]));
-                x[i + 2] = b4.z * fmaf(-g4.z, x[i + 2], to_f32(V[(i + 2) * D]));
-                x[i + 3] = b4.w * fmaf(-g4.w, x[i + 3], to_f32(V[(i + 3) * D]));
-            }
+            scale_by(0);
             put(T_RH, T_RL, x);
-            wait_st();
-            fence_before_sync();
-            arrive(B_R);
+            give(B_R);
 
             wait(bar(B_MU), c & 1);
             fence_after_sync();
-            tmem_ld32(t + T_U + 32 * half, x);
+            tmem_ld16(t + T_U + 16 * part, x);
             wait_ld();
-            {
-                float ub[16];
+            float u[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ub[i] = __uint_as_float(pack_bf16(x[2 * i], x[2 * i + 1]));
-                tmem_st16(t + T_UB + 16 * half, ub);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 e4 = *reinterpret_cast<const float4*>(eta + i);
-                x[i] *= e4.x; x[i + 1] *= e4.y; x[i + 2] *= e4.z; x[i + 3] *= e4.w;
-            }
+            for (int i = 0; i < 16; ++i) u[i] = x[i];
+            scale_by(1);
             put(T_RH, T_RL, x);
-            wait_st();
-            fence_before_sync();
-            arrive(B_U);
+            give(B_U);
             arrive(B_EMPTY + s);
+            put(T_UH, T_UL, u);                      // while K^T U is computed
+            give(B_UO);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 wait(bar(B_MD0 + b), c & 1);
                 fence_after_sync();
-                tmem_ld32(t + T_D + 64 * b + 32 * half, x);
+                tmem_ld16(t + T_D + 64 * b + 16 * part, x);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[b][i] = fmaf(last, S[b][i], x[i]);
-                if (c + 1 < chunks) give_state(b);
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 y = fma2(make_float2(last, last), make_float2(S[b][i], S[b][i + 1]), make_float2(x[i], x[i + 1]));
+                    S[b][i] = y.x;
+                    S[b][i + 1] = y.y;
+                }
+                if (c + 1 < chunks) {
+                    put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
+                    give(B_S0 + b);
+                }
             }
+            if (++s == STAGES) s = 0, ph ^= 1;
         }
         if (p.hT && row >= 0) {
             float* hT = p.hT + ((int64_t)row * p.HV + hv) * D * D + j;
-            const bool bad = s_abort != 0;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    hT[(int64_t)(64 * b + 32 * half + i) * D] = bad ? __int_as_float(0x7fc00000) : S[b][i];
+                for (int i = 0; i < 16; ++i) hT[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
         }
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + OST);
+        int s = 0, ph = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
-            const uint8_t* st = sm + s * STAGE;
-            const float* gam = reinterpret_cast<const float*>(st + S_REC + REC_GAM);
+            const float2* gq = reinterpret_cast<const float2*>(sm + s * STAGE + S_REC + REC_GQ);
+            __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + s * STAGE + S_V);    // V's products are done
             const int t0 = begin + c * C, nv = min(C, end - t0);
-            wait(bar(B_FULL + s), (c >> 1) & 1);
+            wait(bar(B_FULL + s), ph);
             wait(bar(B_MO), c & 1);
             fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 float x[32], y[32];
                 tmem_ld32(t + T_XQ + 32 * q, x);
@@ -234,11 +238,13 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (lane == 0) mbar_arrive(bar(B_OFREE));
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    so[(32 * q + i) * D + j] = __float2bfloat16_rn(fmaf(p.scale * gam[32 * q + i], x[i], y[i]));
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 v = fma2(gq[16 * q + i / 2], make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
+                    so[(32 * q + i) * D + j] = b2.x;
+                    so[(32 * q + i + 1) * D + j] = b2.y;
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
             asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
             for (int e = 0; e < C * D / 8 / 128; ++e) {
@@ -247,121 +253,123 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     *reinterpret_cast<uint4*>(p.o + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
                         *reinterpret_cast<const uint4*>(so + r * D + 8 * c8);
             }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            fence_smem_to_async();                   // the next load of this stage is the async proxy's write
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
+            if (++s == STAGES) s = 0, ph ^= 1;
         }
     } else if (warp == W_MMA) {
-        const uint32_t id_n64 = idesc_bf16(128, 64), id_d = idesc_bf16(128, 64, false, true);
-        uint32_t issued = 0;
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_d = idesc_bf16(128, 64, false, true), id_v = idesc_bf16(128, 64, true);
+        int s = 0, ph = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
             uint8_t* st = sm + s * STAGE;
-            const uint32_t base = smem_u32(st), rec = base + S_REC;
+            const uint32_t base = smem_u32(st);
             const int nv = min(C, end - (begin + c * C));
             auto ok = [&](int b, uint32_t parity) {   // every lane sees the same outcome
                 const bool w = wait(bar(b), parity);
                 return __all_sync(0xffffffffu, w) != 0;
             };
-            bool go = ok(B_FULL + s, (c >> 1) & 1);
+            if (!ok(B_FULL + s, ph)) break;
             if (nv < C) {      // rows behind the sequence count as zero, whatever they hold
-                for (int e = lane; e < (C - nv) * 4 * 8; e += 32) {
-                    const int piece = e & 7, box = (e >> 3) & 3, r = nv + (e >> 5);
-                    *reinterpret_cast<uint4*>(st + box * 8192 + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+                for (int e = lane; e < (C - nv) * 6 * 8; e += 32) {
+                    const int piece = e & 7, box = (e >> 3) % 6, r = nv + (e >> 3) / 6;
+                    *reinterpret_cast<uint4*>(st + box * BOX + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                for (int e = lane; e < (C - nv) * 16; e += 32)
-                    *reinterpret_cast<uint4*>(st + S_V + nv * D * 2 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 fence_smem_to_async();
+                __syncwarp();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_READY + s));
-            // (x S)^T for the K rows (box 0) or the Q rows (box 1): d_k steps [k0, k1)
-            auto state_product = [&](uint32_t d, uint32_t a, int box, int k0, int k1, bool first) {
-#pragma unroll
-                for (int ks = k0; ks < k1; ++ks)
-                    mma_f16_ts_w(tm + d, tm + a + 8 * ks,
-                                 sdesc_sw128(base + (2 * (ks / 4) + box) * 8192) + (uint64_t)(2 * (ks % 4)), id_n64,
-                                 first && ks == k0 ? 0u : 1u);
+            // (K S)^T or (Q S)^T: d_k steps [k0, k0 + 4), the box of K or Q that holds them
+            const uint64_t kq = sdesc_sw128(base);
+            auto state_product = [&](uint32_t d, uint32_t a, int box, int k0, uint32_t more) {
+                mma4_ts(tm + d, tm + a + 8 * k0, kq + (uint64_t)(box * (BOX >> 4)), 2, id_n64, more);
             };
-            go = go && ok(B_S0, c & 1);
-            fence_after_sync();
-            if (go) {
-                state_product(T_XK, T_SH, 0, 0, 4, true);
-                state_product(T_XK, T_SL, 0, 0, 4, false);
-            }
-            go = go && ok(B_S1, c & 1);
-            fence_after_sync();
-            if (go) {
-                state_product(T_XK, T_SH, 0, 4, 8, false);
-                state_product(T_XK, T_SL, 0, 4, 8, false);
-                mma_commit_w(bar(B_MX));
-            }
-            if (c > 0) go = go && ok(B_OFREE, (c - 1) & 1);
-            fence_after_sync();
-            if (go) state_product(T_XQ, T_SH, 1, 0, 8, true);
-            // U^T = R^T X^T (K = tokens): R_hi X_hi + R_lo X_hi + R_hi X_lo
-            auto token_product = [&](uint32_t d, uint32_t a, uint32_t b, bool first) {
-                const uint64_t bd = sdesc(b, 128, 1024);
-#pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
-                    mma_f16_ts_w(tm + d, tm + a + 8 * ks, bd + (uint64_t)(16 * ks), id_n64, first && ks == 0 ? 0u : 1u);
+            // (x)^T T^T or U^T P^T over the 64 tokens
+            auto token_product = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t more) {
+                mma4_ts(tm + d, tm + a, sdesc(b, 128, 1024), 16, id_n64, more);
             };
-            go = go && ok(B_R, c & 1);
+            if (!ok(B_S0, c & 1)) break;
             fence_after_sync();
-            if (go) {
-                token_product(T_U, T_RH, rec + REC_XH, true);
-                token_product(T_U, T_RL, rec + REC_XH, false);
-                token_product(T_U, T_RH, rec + REC_XL, false);
-                mma_commit_w(bar(B_MU));
-            }
-            go = go && ok(B_U, c & 1);
+            state_product(T_XK, T_SH, 0, 0, 0u);
+            state_product(T_XK, T_SL, 0, 0, 1u);
+            if (!ok(B_S1, c & 1)) break;
             fence_after_sync();
-            if (go) {
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {         // (K^T U)^T, 64 values of d_k each
-                    const uint64_t kd = sdesc_sw128(base + 2 * b * 8192);
-#pragma unroll
-                    for (int hl = 0; hl < 2; ++hl)
-#pragma unroll
-                        for (int ks = 0; ks < C / 16; ++ks)
-                            mma_f16_ts_w(tm + T_D + 64 * b, tm + (hl ? T_RL : T_RH) + 8 * ks, kd + (uint64_t)(128 * ks),
-                                         id_d, hl == 0 && ks == 0 ? 0u : 1u);
-                    mma_commit_w(bar(B_MD0 + b));
-                }
-                token_product(T_O, T_UB, rec + REC_P, true);
-                mma_commit_w(bar(B_MO));
+            state_product(T_XK, T_SH, 2, 4, 1u);
+            state_product(T_XK, T_SL, 2, 4, 1u);
+            mma_commit_w(bar(B_MX));
+            {   // U^T = V^T T^T, while the chain takes X_K
+                const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
+                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
+                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
             }
-            issued = c + 1;
-            if (!go) break;
+            if (!ok(B_R, c & 1)) break;
+            fence_after_sync();
+            token_product(T_U, T_RH, base + S_REC + REC_TH, 1u);
+            token_product(T_U, T_RL, base + S_REC + REC_TH, 1u);
+            token_product(T_U, T_RH, base + S_REC + REC_TL, 1u);
+            mma_commit_w(bar(B_MU));
+            if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
+            fence_after_sync();
+            state_product(T_XQ, T_SH, 1, 0, 0u);      // while the chain splits U
+            state_product(T_XQ, T_SH, 3, 4, 1u);
+            state_product(T_XQ, T_SL, 1, 0, 1u);
+            state_product(T_XQ, T_SL, 3, 4, 1u);
+            if (!ok(B_U, c & 1)) break;
+            fence_after_sync();
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {             // (K^T U)^T, 64 values of d_k each
+                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
+                mma4_ts(tm + T_D + 64 * b, tm + T_RH, kd, 128, id_d, 0u);
+                mma4_ts(tm + T_D + 64 * b, tm + T_RL, kd, 128, id_d, 1u);
+                mma_commit_w(bar(B_MD0 + b));
+            }
+            if (!ok(B_P, c & 1) || !ok(B_UO, c & 1)) break;
+            fence_after_sync();
+            token_product(T_O, T_UH, smem_u32(sm + S_P), 0u);     // while it updates the state
+            token_product(T_O, T_UL, smem_u32(sm + S_P), 1u);
+            token_product(T_O, T_UH, smem_u32(sm + S_P) + C * C * 2, 1u);
+            mma_commit_w(bar(B_MO));
+            if (++s == STAGES) s = 0, ph ^= 1;
         }
-        if (issued > 0) {                             // what was issued ends before its memory goes
+        if (chunks > 0) {                             // what was issued ends before its memory goes
             mma_commit_w(bar(B_DRAIN));
             mbar_wait(bar(B_DRAIN), 0, DRAIN_NS);
         }
-    } else {
-        const uint32_t bytes = 4 * 8192 + C * D * 2 + REC_BYTES;
-        int loaded = 0;
-        if (lane == 0) {
+    } else if (lane == 0) {
+        constexpr uint32_t bytes = 6 * BOX + REC_T_BYTES;
+        const uint8_t* rec = p.rec + (slot0 * p.HV + hv) * REC_BYTES;
+        int s = 0, ph = 0, loaded = 0, loaded_p = 0;
 #pragma unroll 1
-            for (int c = 0; c < chunks; ++c) {
-                const int s = c & 1;
-                if (c >= 2 && !wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1)) break;
+        for (int c = 0; c < chunks + 1; ++c) {
+            // the stage of chunk c is free once chunk c - STAGES is done with it, P's buffer after each chunk
+            if (c < chunks) {
+                if (c >= STAGES && !wait(bar(B_EMPTY + s), ph ^ 1)) break;
                 if (*(volatile int*)&s_abort) break;
                 const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
                 const int y = begin + c * C;
                 mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    tma_load_2d(base + 2 * b * 8192, &mk, hk * D + 64 * b, y, full);
-                    tma_load_2d(base + (2 * b + 1) * 8192, &mq, hk * D + 64 * b, y, full);
+                    tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
+                    tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
+                    tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
                 }
-                tma_load_2d(base + S_V, &mv, hv * D, y, full);
-                bulk_load(base + S_REC, p.rec + ((slot0 + c) * p.HV + hv) * REC_BYTES, REC_BYTES, full);
+                bulk_load(base + S_REC, rec + (int64_t)c * p.HV * REC_BYTES, REC_T_BYTES, full);
                 loaded = c + 1;
+                if (++s == STAGES) s = 0, ph ^= 1;
             }
-            for (int c = max(0, loaded - 2); c < loaded; ++c)          // everything loaded has landed before the end
-                mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
+            // P one chunk behind the stages: its buffer is read until the previous chunk's O is complete
+            if (c >= 1) {
+                if (c >= 2 && !wait(bar(B_MO), c & 1)) break;
+                mbar_arrive_expect_tx(bar(B_P), P_BYTES);
+                bulk_load(smem_u32(sm + S_P), rec + (int64_t)(c - 1) * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
+                loaded_p = c;
+            }
         }
-        __syncwarp();
+        // everything loaded has landed before the end
+        for (int c = max(0, loaded - STAGES); c < loaded; ++c)
+            mbar_wait(bar(B_FULL + c % STAGES), (c / STAGES) & 1, DRAIN_NS);
+        if (loaded_p > 0) mbar_wait(bar(B_P), (loaded_p - 1) & 1, DRAIN_NS);
     }
     fence_before_sync();
     __syncthreads();
@@ -410,9 +418,9 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
     uint8_t* rec = nullptr;
     const int64_t tokens = a.seqs.tokens;
     if (tokens > 0) {
-        if (!make_token_map(&mq, q, tokens, (int64_t)HK * D, q_stride, 64) ||
-            !make_token_map(&mk, k, tokens, (int64_t)HK * D, k_stride, 64) ||
-            !make_token_map(&mv, v, tokens, (int64_t)HV * D, v_stride, D))
+        if (!make_token_map(&mq, q, tokens, (int64_t)HK * D, q_stride) ||
+            !make_token_map(&mk, k, tokens, (int64_t)HK * D, k_stride) ||
+            !make_token_map(&mv, v, tokens, (int64_t)HV * D, v_stride))
             return cudaErrorInvalidValue;
         keep_pool_memory();
         e = cudaMallocAsync(reinterpret_cast<void**>(&rec), (size_t)slot_count(a.seqs) * HV * REC_BYTES, stream);

@@ -1,15 +1,15 @@
 // Gated delta rule, one decay per head: the part of a chunk that needs no
 // state, for every chunk at once (one CTA per value head and chunk slot):
-// X = (I + A)^-1, P and the gate factors (gdn_chunk.cuh).
+// T = (I + A)^-1 diag(beta), P and the gate factors (gdn_chunk.cuh).
 //
 // K K^T and Q K^T are one tensor-core product of M = 128 ([K; Q]), N = 64,
-// K = 128 from the TMA-staged rows.  The running sums of g and their
-// differences are taken in 64 bits: a sum over 64 tokens reaches thousands
+// K = 128 from the TMA-staged rows.  The running sums of g are taken in 64
+// bits and kept as two fp32 numbers: a sum over 64 tokens reaches thousands
 // when tokens reset the state, and fp32 would then lose the decay between
-// neighbours.  X comes from forward substitution in fp32: the four 16 x 16
-// diagonal blocks by columns, then X10 = -X11 A10 X00 for blocks of 16 and of
-// 32 (a row-by-row substitution of 64 rows would be one long chain, powers of
-// A would lose digits when keys repeat).
+// neighbours.  X comes from forward substitution in fp32 (powers of A would
+// lose digits when keys repeat): the two 32 x 32 diagonal blocks side by side,
+// one column per thread with its values in registers and the rows of A as
+// broadcast 16-byte reads, then X10 = -X11 (A10 X00) the same way.
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -18,20 +18,39 @@ namespace gdn {
 __device__ int g_prep_status;
 
 namespace prep {
-constexpr int NT = 256;
-constexpr int LD = C + 1;
-// K and Q rows (two boxes of 64 channels each: K0 Q0 K1 Q1), then A, X and
-// the product between the blocks in their place
+constexpr int NT = 128;
+constexpr int LD = C + 4;                            // rows stay 16-byte aligned
+// K and Q rows (two boxes of 64 channels each: K0 Q0 K1 Q1), then A and X in
+// their place
 constexpr uint32_t KQ_BYTES = 2 * C * D * 2;
 constexpr uint32_t A_OFF = 0;
 constexpr uint32_t X_OFF = A_OFF + C * LD * 4;
-constexpr uint32_t Y_OFF = X_OFF + C * LD * 4;
-constexpr uint32_t BODY = Y_OFF + 32 * 33 * 4;
+constexpr uint32_t BODY = X_OFF + C * LD * 4;
 static_assert(BODY >= KQ_BYTES, "one body for both");
 constexpr uint32_t SMEM = BODY + 1024;               // room to align the tiles to 1024 bytes
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 32 columns of row r as pairs of bf16, in the operand layout.
+__device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, int r, int col, const float (&x)[32])
+{
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_bf16(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], hi[e], lo[e]);
+        const uint32_t at = (r / 8) * 1024 + (col / 8 + p) * 128 + (r % 8) * 16;
+        *reinterpret_cast<float4*>(hi_dst + at) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<float4*>(lo_dst + at) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
 }  // namespace prep
 
-__global__ void __launch_bounds__(prep::NT, 4)
+__global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, uint8_t* __restrict__ rec_all, float scale, int HK, int HV,
             bool gate_f32, uint64_t wait_ns)
@@ -40,8 +59,9 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     using namespace tc;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[2];
-    __shared__ double sG[C];
-    __shared__ float sB[C];
+    // the running sum of g in units of log 2, as two fp32 numbers
+    __shared__ __align__(16) float sGh[C], sGl[C];
+    __shared__ __align__(16) float sB[C];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
@@ -77,15 +97,17 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             x[i] = r < nv ? (double)cut_decay(gate(g, at, gate_f32)) : 0.0;
             sB[r] = r < nv ? gate(beta, at, gate_f32) : 0.f;
         }
-        const double both = x[0] + x[1];
-        double sum = both;
+        double sum = x[0] + x[1];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const double y = __shfl_up_sync(0xffffffffu, sum, off);
             if (lane >= off) sum += y;
         }
-        sG[2 * lane] = sum - both + x[0];
-        sG[2 * lane + 1] = sum;
+        for (int i = 0; i < 2; ++i) {
+            const double G = (i == 0 ? sum - x[1] : sum) * 1.4426950408889634;
+            sGh[2 * lane + i] = (float)G;
+            sGl[2 * lane + i] = (float)(G - (double)(float)G);
+        }
     }
     fence_before_sync();
     __syncthreads();
@@ -117,42 +139,40 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     fence_after_sync();
     float* sA = reinterpret_cast<float*>(sm + A_OFF);
     float* sX = reinterpret_cast<float*>(sm + X_OFF);
-    float* sY = reinterpret_cast<float*>(sm + Y_OFF);
-    {   // thread: one row of [K K^T; Q K^T], 32 columns
-        float x[32];
-        const int sp = warp & 3, col = 32 * (warp >> 2), r = (sp & 1) * 32 + lane;
-        tmem_ld32(tm + ((uint32_t)(32 * sp) << 16) + col, x);
-        wait_ld();
-        const double Gr = sG[r];
-        if (sp < 2) {
-            const float b = sB[r];
+    {   // thread: one row of [K K^T; Q K^T]; warps 0-1 make A, warps 2-3 P
+        const int r = tid % C;
+        const float gh = sGh[r], gl = sGl[r], f = warp < 2 ? sB[r] : scale;
+        const int last = warp < 2 ? r - 1 : r;        // the row's last column
+#pragma unroll 1
+        for (int col = 0; col < C; col += 32) {
+            float x[32];
+            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + col, x);
+            wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int c = col + i;
-                sA[r * LD + c] = c < r ? b * expf((float)(Gr - sG[c])) * x[i] : 0.f;
-            }
-        } else {
-            uint8_t* dst = rec + REC_P + (r / 8) * 1024 + (r % 8) * 16;
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                uint32_t w[4];
+            for (int i = 0; i < 32; i += 4) {
+                const float4 ch = *reinterpret_cast<const float4*>(sGh + col + i), cl = *reinterpret_cast<const float4*>(sGl + col + i);
+                const float dh[4] = {ch.x, ch.y, ch.z, ch.w}, dl[4] = {cl.x, cl.y, cl.z, cl.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = 8 * p + 2 * e, c = col + i;
-                    const float lo = c <= r ? scale * expf((float)(Gr - sG[c])) * x[i] : 0.f;
-                    const float hi = c + 1 <= r ? scale * expf((float)(Gr - sG[c + 1])) * x[i + 1] : 0.f;
-                    w[e] = pack_bf16(lo, hi);
+                    const float d = exp2_fast((gh - dh[e]) + (gl - dl[e]));
+                    x[i + e] = col + i + e <= last ? f * d * x[i + e] : 0.f;
                 }
-                *reinterpret_cast<uint4*>(dst + (col / 8 + p) * 128) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (warp < 2) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(sA + r * LD + col + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            } else {
+                store_split(rec + REC_PH, rec + REC_PL, r, col, x);
             }
         }
     }
     if (tid < C) {
-        const double Gl = sG[C - 1], Gr = sG[tid];
-        reinterpret_cast<float*>(rec + REC_GAM)[tid] = expf((float)Gr);
-        reinterpret_cast<float*>(rec + REC_ETA)[tid] = expf((float)(Gl - Gr));
+        const float gh = sGh[tid], gl = sGl[tid], gam = exp2f(gh + gl);
+        reinterpret_cast<float*>(rec + REC_NGAM)[tid] = s_abort ? __int_as_float(0x7fc00000) : -gam;
+        reinterpret_cast<float*>(rec + REC_ETA)[tid] = exp2f((sGh[C - 1] - gh) + (sGl[C - 1] - gl));
+        reinterpret_cast<float*>(rec + REC_GQ)[tid] = scale * gam;
         reinterpret_cast<float*>(rec + REC_BETA)[tid] = sB[tid];
-        if (tid == 0) *reinterpret_cast<float*>(rec + REC_LAST) = expf((float)Gl);
     }
     fence_before_sync();
     __syncthreads();
@@ -160,82 +180,80 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         fence_after_sync();
         tmem_dealloc(tm, 64);
     }
-    // X: the 16 x 16 diagonal blocks, one column per thread
-    if (tid < C) {
-        const int b = tid / 16, j = tid % 16;
-        const float* a = sA + (16 * b) * LD + 16 * b;
-        float x[16];
+    // X00 (warp 0) and X11 (warp 1): 32 x 32 forward substitution, one column
+    // per thread; the rows of A are broadcast reads
+    constexpr int H = C / 2;
+    if (warp < 2) {
+        const float* a = sA + (H * warp) * LD + H * warp;
+        float x[H];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
+        for (int r = 0; r < H; ++r) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < r; ++i) s[i & 3] = fmaf(a[r * LD + i], x[i], s[i & 3]);
-            x[r] = r == j ? 1.f : r > j ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
+            for (int i = 0; i < r; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(a + r * LD + i);   // A is zero from the diagonal on
+                s[0] = fmaf(v.x, x[i], s[0]);
+                if (i + 1 < r) s[1] = fmaf(v.y, x[i + 1], s[1]);
+                if (i + 2 < r) s[2] = fmaf(v.z, x[i + 2], s[2]);
+                if (i + 3 < r) s[3] = fmaf(v.w, x[i + 3], s[3]);
+            }
+            x[r] = r == lane ? 1.f : r > lane ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
         }
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sX[(16 * b + r) * LD + 16 * b + j] = x[r];
+        for (int r = 0; r < H; ++r) sX[(H * warp + r) * LD + H * warp + lane] = x[r];
     }
     __syncthreads();
-    // blocks of S next to one another: X10 = -X11 (A10 X00), S = 16 then 32;
-    // the block of S x S results is spread over the threads of its pair
-    auto join = [&](auto size) {
-        constexpr int S = decltype(size)::value;
-        constexpr int PAIRS = C / (2 * S), TP = NT / PAIRS, PER = S * S / TP;      // results per thread
-        const int pair = tid / TP, t = tid % TP;
-        const int col = t % S, row0 = (t / S) * PER;
-        const int base = 2 * S * pair;
-        float acc[PER];
+    // X10 = -X11 (A10 X00): thread = one column, 8 rows
+    {
+        float x[H], acc[8];
+        const int r0 = 8 * warp;
+        auto eight_rows = [&](const float* m) {       // acc = rows [r0, r0 + 8) of m times the column x
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < S; ++k) {                 // Y = A10 X00
-            const float x = k >= col ? sX[(base + k) * LD + base + col] : 0.f;
+            for (int r = 0; r < 8; ++r) {
+                float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = fmaf(sA[(base + S + row0 + i) * LD + base + k], x, acc[i]);
-        }
-        float* y = sY + pair * (S * (S + 1));
-#pragma unroll
-        for (int i = 0; i < PER; ++i) y[(row0 + i) * (S + 1) + col] = acc[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll 8
-        for (int k = 0; k < S; ++k) {
-            const float v = y[k * (S + 1) + col];
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                acc[i] = fmaf(k <= row0 + i ? sX[(base + S + row0 + i) * LD + base + S + k] : 0.f, v, acc[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) sX[(base + S + row0 + i) * LD + base + col] = -acc[i];
-        __syncthreads();
-    };
-    join(std::integral_constant<int, 16>());
-    join(std::integral_constant<int, 32>());
-    {   // X as two bf16 numbers, in the operand layout: one row and 16 columns per thread
-        const int r = tid % C, c0 = (tid / C) * 16;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = c0 + 8 * p + 2 * e;
-                // above the diagonal blocks sX was never written
-                const float a = c <= r ? sX[r * LD + c] : 0.f, b = c + 1 <= r ? sX[r * LD + c + 1] : 0.f;
-                float h, l;
-                split_bf16(a, b, h, l);
-                hi[e] = __float_as_uint(h);
-                lo[e] = __float_as_uint(l);
+                for (int i = 0; i < H; i += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(m + (r0 + r) * LD + i);
+                    s[0] = fmaf(v.x, x[i], s[0]);
+                    s[1] = fmaf(v.y, x[i + 1], s[1]);
+                    s[2] = fmaf(v.z, x[i + 2], s[2]);
+                    s[3] = fmaf(v.w, x[i + 3], s[3]);
+                }
+                acc[r] = (s[0] + s[1]) + (s[2] + s[3]);
             }
-            const uint32_t at = (r / 8) * 1024 + (c0 / 8 + p) * 128 + (r % 8) * 16;
-            *reinterpret_cast<uint4*>(rec + REC_XH + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(rec + REC_XL + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
+        };
+        float* y = sA;                                // over A00, which is done with
+#pragma unroll
+        for (int i = 0; i < H; ++i) x[i] = sX[i * LD + lane];
+        eight_rows(sA + H * LD);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) y[(r0 + r) * LD + lane] = acc[r];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < H; ++i) x[i] = y[i * LD + lane];
+        eight_rows(sX + H * LD + H);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) sX[(H + r0 + r) * LD + lane] = -acc[r];
     }
-    if (s_abort && tid < C) reinterpret_cast<float*>(rec + REC_GAM)[tid] = __int_as_float(0x7fc00000);
+    __syncthreads();
+    {   // T = X diag(beta) as two bf16 numbers, in the operand layout: one row and 32 columns per thread
+        const int r = tid % C, col = 32 * (tid / C);
+        float x[32];
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(sX + r * LD + col + i), b = *reinterpret_cast<const float4*>(sB + col + i);
+            x[i] = v.x * b.x; x[i + 1] = v.y * b.y; x[i + 2] = v.z * b.z; x[i + 3] = v.w * b.w;
+        }
+        if (col > r) {                                // the block above the diagonal was never written
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        store_split(rec + REC_TH, rec + REC_TL, r, col, x);
+    }
 }
 
-bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, int box_cols)
+bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride)
 {
     typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -251,10 +269,10 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)tokens};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)C};
+    const cuuint32_t box[2] = {64, (cuuint32_t)C};
     const cuuint32_t estr[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
