@@ -350,7 +350,7 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * chunks at once, then one CTA per sequence and value head along the chunks.
  * K and Q enter the products as bf16, the state and what is computed as pairs
  * of bf16 with fp32 sums: hT is accurate to about 1e-5 of its norm.
- * Supported: d_k == d_v == 128.  Stream-ordered workspace of 25,600 bytes per
+ * Supported: d_k == d_v == 128.  Stream-ordered workspace of 33,792 bytes per
  * value head and 64-token chunk (at most tokens / 64 + N chunks);
  * KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in the prefill
  * (kda_device_status).
@@ -360,6 +360,39 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
                       int n_slots, float scale, int N, int T, int HK, int HV, int d_k, int d_v,
                       int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
                       kda_stream_t stream);
+
+/*
+ * kda_gdn_chunk_bwd -- gradients of a kda_gdn_chunk_fwd call: with L = sum(dO
+ * * o) + sum(dhT * hT), of L with respect to q, k, v, g, beta and h0.
+ *   q .. h0, cu_seqlens, scale, sizes, strides: the forward's (h0: [N] rows)
+ *   dO  : bf16 [tokens][HV][d_v], dense      dhT : fp32 [N][HV][d_k][d_v] or NULL
+ *   dq, dk : bf16 [tokens][HK][d_k], summed over the value heads of a group
+ *   dv : bf16 [tokens][HV][d_v]     dg, dbeta : bf16 [tokens][HV]
+ *   dh0 : fp32 [N][HV][d_k][d_v], or NULL
+ * Tokens before the first sequence and behind the last get zero gradients.  A
+ * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
+ * atomics: the same inputs give the same bits.  Three launches (one more with
+ * cu_seqlens); stream-ordered workspace of 164,864 bytes per value head and
+ * 64-token chunk and 768 bytes per token and value head (KDA_ERR_NO_MEMORY if
+ * it cannot be had).  Supported: d_k == d_v == 128.
+ *
+ * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits
+ * (kda_act_pack8, dense [tokens][HK or HV][128] and [..][4] scales): the
+ * gradients at the values that the 8-bit forms stand for.  They are expanded
+ * into the workspace (2 more bytes per value).
+ */
+int kda_gdn_chunk_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                      const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
+                      void* dg, void* dbeta, float* dh0, const int32_t* cu_seqlens, float scale,
+                      int N, int T, int HK, int HV, int d_k, int d_v,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                      kda_stream_t stream);
+int kda_gdn_chunk_bwd_packed8(const void* q8, const void* k8, const void* v8, const void* q_scales,
+                              const void* k_scales, const void* v_scales, const void* g, const void* beta,
+                              const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
+                              void* dg, void* dbeta, float* dh0, const int32_t* cu_seqlens, float scale,
+                              int N, int T, int HK, int HV, int d_k, int d_v, int gate_f32,
+                              kda_stream_t stream);
 
 /*
  * kda_gdn_decode_step -- one token for each of N requests, state rows updated

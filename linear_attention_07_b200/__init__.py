@@ -37,7 +37,7 @@ KDA_ERR_NO_MEMORY = -5
 EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_states", "kda_chunk_fwd_f32",
             "kda_chunk_transition", "kda_state_chain", "kda_chunk_fwd_raw", "kda_decode_step",
             "kda_decode_step_raw", "kda_verify_fwd", "kda_chunk_bwd", "kda_chunk_bwd_raw",
-            "kda_gdn_chunk_fwd", "kda_gdn_decode_step", "kda_act_pack8", "kda_act_unpack8",
+            "kda_gdn_chunk_fwd", "kda_gdn_chunk_bwd", "kda_gdn_chunk_bwd_packed8", "kda_gdn_decode_step", "kda_act_pack8", "kda_act_unpack8",
             "kda_device_status", "kda_selftest_bounded_wait",
             "kda_status_string", "kda_launch_count", "kda_prefill_path", "kda_version")
 
@@ -99,6 +99,10 @@ def load_library(path: str = LIB_PATH):
     lib.kda_gdn_decode_step.restype = i
     lib.kda_gdn_chunk_fwd.argtypes = [vp, vp, vp, vp, vp, fp, vp, fp, vp, vp, i, f, i, i, i, i, i, i, i64, i64, i64, i, vp]
     lib.kda_gdn_chunk_fwd.restype = i
+    lib.kda_gdn_chunk_bwd.argtypes = [vp] * 14 + [vp, f, i, i, i, i, i, i, i64, i64, i64, i, vp]
+    lib.kda_gdn_chunk_bwd.restype = i
+    lib.kda_gdn_chunk_bwd_packed8.argtypes = [vp] * 17 + [vp, f, i, i, i, i, i, i, i, vp]
+    lib.kda_gdn_chunk_bwd_packed8.restype = i
     lib.kda_act_pack8.argtypes = [i, vp, vp, vp, vp, vp, vp, vp]
     lib.kda_act_pack8.restype = i
     lib.kda_act_unpack8.argtypes = [i, vp, vp, vp, vp, vp, vp]
@@ -539,6 +543,56 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slot
     if st != KDA_OK:
         raise KdaError("kda_gdn_chunk_fwd", st)
     return o, hT
+
+
+def gdn_chunk_bwd(q, k, v, g, beta, h0, dO, dhT=None, *, scale=1.0, cu_seqlens=None, want_dh0=True):
+    """Gradients of gdn_chunk_fwd (kda_gdn_chunk_bwd): with L = sum(dO * o) +
+    sum(dhT * hT), returns (dq, dk, dv, dg, dbeta, dh0).
+
+    q, k and v are bf16 as in the forward, or all three a Packed8 (their
+    8-bit checkpoints; the gradients are those at the values that these stand
+    for).  dO: [B, T, HV, 128] bf16; dhT: [N, HV, 128, 128] fp32 or None.  dq,
+    dk (summed over the value heads of a group), dv, dg, dbeta are bf16, dh0 is
+    fp32 (None if want_dh0 is False).  Tokens that belong to no sequence get
+    zero gradients."""
+    import torch
+    eight = [isinstance(x, Packed8) for x in (q, k, v)]
+    if any(eight) and not all(eight):
+        raise TypeError("q, k and v must all be tensors or all be Packed8")
+    B, T, HK, dk = q.shape
+    HV, dv = v.shape[-2:]
+    dev = _require_cuda(q.data if eight[0] else q)
+    strides = []
+    for name, t, heads, d in (("q", q, HK, dk), ("k", k, HK, dk), ("v", v, HV, dv)):
+        if eight[0]:
+            _check_packed8(t, name, dev)
+            if tuple(t.shape) != (B, T, heads, d):
+                raise ValueError("%s must have shape %s, got %s" % (name, (B, T, heads, d), tuple(t.shape)))
+        else:
+            strides.append(_check_tokens(t, name, (B, T), heads, d, dev))
+    gf = _check_gates(g, beta, (B, T), HV, dev)
+    N, Tc = _gdn_sequences(q, cu_seqlens, dev)
+    _check(dO, "dO", torch.bfloat16, (B, T, HV, dv), dev)
+    for name, t in (("h0", h0), ("dhT", dhT)):
+        if t is not None:
+            _check(t, name, torch.float32, (N, HV, dk, dv), dev)
+    gq, gk = (torch.empty((B, T, HK, dk), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    gv = torch.empty((B, T, HV, dv), dtype=torch.bfloat16, device=dev)
+    gg, gb = (torch.empty((B, T, HV), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    gh = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
+    rest = [_ptr(x) for x in (g, beta, h0, dO, dhT, gq, gk, gv, gg, gb, gh, cu_seqlens)]
+    sizes = (float(scale), N, Tc, HK, HV, dk, dv)
+    with torch.cuda.device(dev):
+        if eight[0]:
+            fn = "kda_gdn_chunk_bwd_packed8"
+            st = load_library().kda_gdn_chunk_bwd_packed8(*(_ptr(x.data) for x in (q, k, v)), *(_ptr(x.scales) for x in (q, k, v)),
+                                                          *rest, *sizes, gf, _stream(dev))
+        else:
+            fn = "kda_gdn_chunk_bwd"
+            st = load_library().kda_gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), *rest, *sizes, *strides, gf, _stream(dev))
+    if st != KDA_OK:
+        raise KdaError(fn, st)
+    return gq, gk, gv, gg, gb, gh
 
 
 def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):

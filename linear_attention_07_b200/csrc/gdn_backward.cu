@@ -1,0 +1,960 @@
+// Gated delta rule, one decay per head: backward of the chunked forward, after
+// the prep kernel (gdn_prep.cu).  With dO~ = scale dO, dS1 = dL/dS1 and the
+// chunk's quantities of gdn_chunk.cuh:
+//     dU  = P^T dO + eta (K dS1)
+//     dV  = T^T dU                                  (T = X diag(beta))
+//     dS0 = gam_last dS1 + K^T (-gam dV) + Q^T (gam dO~)
+// and, with E = U / beta and Z = dV / beta (A enters U through (I + A) U =
+// beta (V - gam K S0), so dA = -Z U^T):
+//     dkk_ri = -D_ri dV_r . U_i  (i < r),    dqk_ri = scale D_ri dO_r . U_i  (i <= r)
+//     dQ  = gam dO~ S0^T + dqk K
+//     dK  = [-gam dV S0^T + dkk K]  +  [eta U dS1^T + dkk^T K + dqk^T Q]
+//     dbeta_r = Z_r . E_r = dV_r . U_r / beta_r^2
+// The gradient of a log-decay collects every path across its token, without
+// the cancellation of a sum over all tokens behind it:
+//     dg_t = gam_last <dS1, S0>  +  sum_{r >= t} a_r  +  sum_{i < t} b_i  +  sum_{i < t <= r} w_ri
+//     a_r  = gam_r (dO~_r . q_r S0 - dV_r . k_r S0)         read behind t what was there before the chunk
+//     b_i  = eta_i U_i . k_i dS1                            written before t and kept to the chunk's end
+//     w_ri = dqk_ri q_r . k_i + dkk_ri k_r . k_i            written before t, read behind it
+// A write strength of zero would make dbeta 0 / 0: the backward takes |beta|
+// as at least 2^-30 (below fp32's resolution of the state).
+//
+// Two launches after the prep:
+//   1. chains_kernel: per sequence and value head two CTAs side by side, the
+//      forward chain (states at the chunks' starts, U) and the reverse chain
+//      (state gradients at the chunks' ends, dV, dh0);
+//   2. local_kernel: per chunk and query/key head, dq, dk (summed over the
+//      value heads of the group), dg, dbeta.
+// All that passes between products is a pair of bf16, as in the forward: a
+// single rounding would show in dg and dbeta, which are few numbers each from
+// a long sum.
+#include "gdn_chunk.cuh"
+
+namespace kda {
+namespace gdn {
+
+__device__ int g_back_status;
+
+namespace bk {
+
+constexpr uint32_t BOX = C * 64 * 2;
+// a state as two bf16 planes, each as the local kernel's left operand (M =
+// d_k, K = d_v in two halves, MN-major without swizzle): element (i, j) at
+// (j / 64) * 16384 + (i / 8) * 1024 + (j % 64) * 16 + (i % 8) * 2
+constexpr uint32_t PLANE = D * D * 2, HALF = PLANE / 2;
+constexpr uint32_t ST_SBO = 1024, ST_LBO = 128;
+
+// ------------------------------------------------------------------ chains --
+
+constexpr int N_CHAIN = 16, N_OUT = 4;               // warps
+constexpr int W_MMA = N_CHAIN + N_OUT, W_LOAD = W_MMA + 1;
+constexpr int NT = 32 * (W_LOAD + 1);
+// a stage: K0 Q0 K1 Q1, V0 V1 (reverse: dO), the record
+constexpr int STAGES = 2;
+constexpr uint32_t S_V = 4 * BOX, S_REC = 6 * BOX;
+constexpr uint32_t STAGE = S_REC + REC_BYTES;
+static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+constexpr uint32_t S_OUT = STAGES * STAGE;           // U or dV staging, two planes [64][128] bf16
+constexpr uint32_t SMEM = S_OUT + 2 * C * D * 2 + 1024;
+
+enum { B_FULL = 0, B_EMPTY = STAGES, B_MX = 2 * STAGES, B_MU, B_MD0, B_MD1, B_S0, B_S1, B_R, B_U, B_DO, B_OUT, B_OUTFREE, B_DRAIN, N_BAR };
+
+constexpr uint32_t T_SH = 0, T_SL = 64;
+constexpr uint32_t T_X = 128;                        // (K S)^T
+constexpr uint32_t T_PO = 192;                       // forward: U^T; reverse: (P^T dO)^T
+constexpr uint32_t T_RH = 256, T_RL = 288;
+constexpr uint32_t T_OH = 320, T_OL = 352;           // reverse: (gam dO~)^T
+constexpr uint32_t T_D = 384;
+
+struct Args {
+    Seqs seqs;
+    const uint8_t* rec;
+    const float* h0;
+    const float* dhT;
+    float* dh0;
+    uint8_t* S0;            // per (slot, value head): the chunk's start state, two planes
+    uint8_t* dS1;           // and its end state's gradient
+    __nv_bfloat16* u[2];    // U and dV, two planes [tokens][HV][D] each; dV's first is the gradient
+    __nv_bfloat16* dv[2];
+    int HK, HV;
+    uint64_t wait_ns;
+};
+
+template <bool REV>
+__device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& p,
+                                      uint8_t* sm, uint64_t* bars, volatile int* s_abort, uint32_t tm, int n, int hv)
+{
+    using namespace tc;
+    constexpr uint32_t T_U = REV ? T_X : T_PO;       // reverse: dV^T, when K dS is done with
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int hk = hv / (p.HV / p.HK);
+    int begin, end;
+    seq_range(p.seqs, n, begin, end);
+    const int chunks = (end - begin + C - 1) / C;
+    const int64_t slot0 = (int64_t)(begin / C) + n;
+    auto bar = [&](int b) { return smem_u32(&bars[b]); };
+    auto chunk_at = [&](int c) { return REV ? chunks - 1 - c : c; };
+    const Waits wait = {s_abort, &g_back_status, p.wait_ns};
+
+    if (warp < N_CHAIN) {
+        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
+        const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
+        const float* init = REV ? p.dhT : p.h0;
+        const float* h = init ? init + ((int64_t)n * p.HV + hv) * D * D + j : nullptr;
+        float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 16 * part + i) * D] : 0.f;
+        auto arrive = [&](int b) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
+        auto give = [&](int b) {
+            wait_st();
+            fence_before_sync();
+            arrive(b);
+        };
+        auto put = [&](uint32_t hi_col, uint32_t lo_col, const float (&x)[16]) {
+            float hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+            tmem_st8(t + hi_col + 8 * part, hi);
+            tmem_st8(t + lo_col + 8 * part, lo);
+        };
+        // the state's half b: operand of the next chunk, and for the local kernel
+        auto give_state = [&](int b, int c) {
+            float hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) split_bf16(S[b][2 * i], S[b][2 * i + 1], hi[i], lo[i]);
+            tmem_st8(t + T_SH + 32 * b + 8 * part, hi);
+            tmem_st8(t + T_SL + 32 * b + 8 * part, lo);
+            give(B_S0 + b);
+            uint8_t* dst = (REV ? p.dS1 : p.S0) + ((slot0 + chunk_at(c)) * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF +
+                           (8 * b + 2 * part) * ST_SBO + (j % 64) * 16;
+            *reinterpret_cast<float4*>(dst) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<float4*>(dst + ST_SBO) = make_float4(hi[4], hi[5], hi[6], hi[7]);
+            *reinterpret_cast<float4*>(dst + PLANE) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<float4*>(dst + PLANE + ST_SBO) = make_float4(lo[4], lo[5], lo[6], lo[7]);
+        };
+        if (chunks > 0) {
+            give_state(0, 0);
+            give_state(1, 0);
+        }
+        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT) + 16 * part * D + j;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1;
+            const float4* gates = reinterpret_cast<const float4*>(sm + s * STAGE + S_REC + REC_NGAM) + 4 * part;
+            wait(bar(B_FULL + s), (c >> 1) & 1);
+            const float last = -reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM)[C - 1];
+            float x[16];
+            auto scale_by = [&](int which) {         // 0: -gam, 1: eta
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = gates[16 * which + i];
+                    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
+                    const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
+                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+                }
+            };
+            wait(bar(B_MX), c & 1);                  // K S, and in reverse P^T dO
+            fence_after_sync();
+            tmem_ld16(t + T_X + 16 * part, x);
+            if constexpr (REV) {
+                float y[16];
+                tmem_ld16(t + T_PO + 16 * part, y);
+                wait_ld();
+                scale_by(1);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] += y[i];
+            } else {
+                wait_ld();
+                scale_by(0);
+            }
+            put(T_RH, T_RL, x);
+            give(B_R);
+
+            wait(bar(B_MU), c & 1);
+            fence_after_sync();
+            tmem_ld16(t + T_U + 16 * part, x);
+            wait_ld();
+            float u[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) u[i] = x[i];
+            scale_by(REV ? 0 : 1);
+            put(T_RH, T_RL, x);
+            give(B_U);
+            arrive(B_EMPTY + s);
+            if (c > 0) wait(bar(B_OUTFREE), (c - 1) & 1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const __nv_bfloat16 hi = __float2bfloat16_rn(u[i]);
+                so[i * D] = hi;
+                so[C * D + i * D] = __float2bfloat16_rn(u[i] - __bfloat162float(hi));
+            }
+            arrive(B_OUT);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                wait(bar(B_MD0 + b), c & 1);
+                fence_after_sync();
+                tmem_ld16(t + T_D + 64 * b + 16 * part, x);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const float2 y = fma2(make_float2(last, last), make_float2(S[b][i], S[b][i + 1]), make_float2(x[i], x[i + 1]));
+                    S[b][i] = y.x;
+                    S[b][i + 1] = y.y;
+                }
+                if (c + 1 < chunks) give_state(b, c + 1);
+            }
+        }
+        if (REV && p.dh0) {
+            float* out = p.dh0 + ((int64_t)n * p.HV + hv) * D * D + j;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
+        }
+    } else if (warp < W_MMA) {
+        const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
+        const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
+        const __nv_bfloat16* so = reinterpret_cast<const __nv_bfloat16*>(sm + S_OUT);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1, t0 = begin + chunk_at(c) * C, nv = min(C, end - t0);
+            wait(bar(B_FULL + s), (c >> 1) & 1);
+            if constexpr (REV) {                     // gam dO~ as an operand; the previous one has been read
+                if (c > 0) wait(bar(B_MD1), (c - 1) & 1);
+                fence_after_sync();
+                const uint8_t* box = sm + s * STAGE + S_V + (j / 64) * BOX + (j % 8) * 2;
+                const float* gq = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_GQ);
+                const int piece = (j % 64) / 8;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    float hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float x[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = 16 * q + 2 * i + e;
+                            const float d = to_f32(*reinterpret_cast<const __nv_bfloat16*>(box + r * 128 + ((piece ^ (r & 7)) * 16)));
+                            x[e] = r < nv ? gq[r] * d : 0.f;
+                        }
+                        split_bf16(x[0], x[1], hi[i], lo[i]);
+                    }
+                    tmem_st8(t + T_OH + 8 * q, hi);
+                    tmem_st8(t + T_OL + 8 * q, lo);
+                }
+                wait_st();
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_DO));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
+            wait(bar(B_OUT), c & 1);
+#pragma unroll 4
+            for (int e = 0; e < 2 * C * D / 8 / 128; ++e) {
+                const int i = ot + 128 * e, plane = i / (C * D / 8), r = (i / (D / 8)) % C, c8 = i % (D / 8);
+                if (r < nv)
+                    *reinterpret_cast<uint4*>((REV ? p.dv : p.u)[plane] + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
+                        *reinterpret_cast<const uint4*>(so + plane * C * D + r * D + 8 * c8);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_OUTFREE));
+        }
+    } else if (warp == W_MMA) {
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_bmn = idesc_bf16(128, 64, false, true);
+        const uint32_t id_v = idesc_bf16(128, 64, true, REV);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1;
+            uint8_t* st = sm + s * STAGE;
+            const uint32_t base = smem_u32(st);
+            const int nv = min(C, end - (begin + chunk_at(c) * C));
+            auto ok = [&](int b, uint32_t parity) {
+                const bool w = wait(bar(b), parity);
+                return __all_sync(0xffffffffu, w) != 0;
+            };
+            if (!ok(B_FULL + s, (c >> 1) & 1)) break;
+            if (nv < C) {      // rows behind the sequence count as zero, whatever they hold
+                for (int e = lane; e < (C - nv) * 6 * 8; e += 32) {
+                    const int piece = e & 7, box = (e >> 3) % 6, r = nv + (e >> 3) / 6;
+                    *reinterpret_cast<uint4*>(st + box * BOX + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_smem_to_async();
+                __syncwarp();
+            }
+            const uint64_t kq = sdesc_sw128(base);
+            const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
+            // T and P as right operands: rows (forward) or columns (reverse) as N
+            auto tp = [&](uint32_t off) { return REV ? sdesc(base + S_REC + off, 1024, 128) : sdesc(base + S_REC + off, 128, 1024); };
+            constexpr uint64_t tp_step = REV ? 128 : 16;
+            auto state_product = [&](uint32_t a, int box, int k0, uint32_t more) {
+                mma4_ts(tm + T_X, tm + a + 8 * k0, kq + (uint64_t)(box * (BOX >> 4)), 2, id_n64, more);
+            };
+            if (!ok(B_S0, c & 1)) break;
+            fence_after_sync();
+            state_product(T_SH, 0, 0, 0u);
+            state_product(T_SL, 0, 0, 1u);
+            if (!ok(B_S1, c & 1)) break;
+            fence_after_sync();
+            state_product(T_SH, 2, 4, 1u);
+            state_product(T_SL, 2, 4, 1u);
+            if constexpr (REV) {
+                mma4_ss(tm + T_PO, vd, 128, tp(REC_PH), tp_step, id_v, 0u);
+                mma4_ss(tm + T_PO, vd, 128, tp(REC_PL), tp_step, id_v, 1u);
+                mma_commit_w(bar(B_MX));
+                if (!ok(B_DO, c & 1)) break;
+                fence_after_sync();
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {        // Q^T (gam dO~), while the chain computes dU
+                    const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
+                    mma4_ts(tm + T_D + 64 * b, tm + T_OH, qd, 128, id_bmn, 0u);
+                    mma4_ts(tm + T_D + 64 * b, tm + T_OL, qd, 128, id_bmn, 1u);
+                }
+            } else {
+                mma_commit_w(bar(B_MX));
+                mma4_ss(tm + T_PO, vd, 128, tp(REC_TH), tp_step, id_v, 0u);
+                mma4_ss(tm + T_PO, vd, 128, tp(REC_TL), tp_step, id_v, 1u);
+            }
+            if (!ok(B_R, c & 1)) break;
+            fence_after_sync();
+            mma4_ts(tm + T_U, tm + T_RH, tp(REC_TH), tp_step, REV ? id_bmn : id_n64, REV ? 0u : 1u);
+            mma4_ts(tm + T_U, tm + T_RL, tp(REC_TH), tp_step, REV ? id_bmn : id_n64, 1u);
+            mma4_ts(tm + T_U, tm + T_RH, tp(REC_TL), tp_step, REV ? id_bmn : id_n64, 1u);
+            mma_commit_w(bar(B_MU));
+            if (!ok(B_U, c & 1)) break;
+            fence_after_sync();
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
+                mma4_ts(tm + T_D + 64 * b, tm + T_RH, kd, 128, id_bmn, REV ? 1u : 0u);
+                mma4_ts(tm + T_D + 64 * b, tm + T_RL, kd, 128, id_bmn, 1u);
+                mma_commit_w(bar(B_MD0 + b));
+            }
+        }
+        if (chunks > 0) {                             // what was issued ends before its memory goes
+            mma_commit_w(bar(B_DRAIN));
+            mbar_wait(bar(B_DRAIN), 0, DRAIN_NS);
+        }
+    } else if (lane == 0) {
+        constexpr uint32_t bytes = REV ? 6 * BOX + REC_BYTES : 4 * BOX + REC_T_BYTES;
+        int loaded = 0;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1;
+            // the chain and output warps are done with chunk c - 2, and so are its last products
+            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1))) break;
+            if (c >= 2 && !wait(bar(B_MD1), c & 1)) break;
+            if (*s_abort) break;
+            const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
+            const int y = begin + chunk_at(c) * C;
+            mbar_arrive_expect_tx(full, bytes);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
+                if (REV) tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
+                tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
+            }
+            bulk_load(base + S_REC, p.rec + ((slot0 + chunk_at(c)) * p.HV + hv) * REC_BYTES, REV ? REC_BYTES : REC_T_BYTES, full);
+            loaded = c + 1;
+        }
+        for (int c = max(0, loaded - STAGES); c < loaded; ++c)
+            mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
+    }
+}
+
+__global__ void __launch_bounds__(NT, 1)
+chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo, const __grid_constant__ Args p)
+{
+    using namespace tc;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[N_BAR];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const bool rev = (blockIdx.x & 1) != 0;          // the two chains of a head next to one another: they share loads
+    const int hv = (blockIdx.x >> 1) % p.HV, n = (blockIdx.x >> 1) / p.HV;
+    if (tid == 0) {
+        for (int b = 0; b < N_BAR; ++b) {
+            const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
+                            : b == B_S0 || b == B_S1 || b == B_R || b == B_U || b == B_OUT ? N_CHAIN
+                            : b == B_DO || b == B_OUTFREE ? N_OUT : 1;
+            mbar_init(smem_u32(&bars[b]), count);
+        }
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == W_MMA) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = s_tmem;
+    if (rev) chain<true>(mq, mk, mdo, p, sm, bars, &s_abort, tm, n, hv);
+    else chain<false>(mq, mk, mv, p, sm, bars, &s_abort, tm, n, hv);
+    fence_before_sync();
+    __syncthreads();
+    if (warp == W_MMA) {
+        fence_after_sync();
+        tmem_dealloc(tm, 512);
+    }
+    if (*(volatile int*)&s_abort) {                  // a wait expired: no partial result passes for a real one
+        int begin, end;
+        seq_range(p.seqs, n, begin, end);
+        const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+        __nv_bfloat16* out = rev ? p.dv[0] : p.u[0]; // the local kernel reads both: its gradients become NaN
+        for (int64_t e = tid; e < (int64_t)(end - begin) * D; e += NT)
+            out[((int64_t)(begin + e / D) * p.HV + hv) * D + e % D] = nan;
+        if (rev && p.dh0)
+            for (int e = tid; e < D * D; e += NT) p.dh0[((int64_t)n * p.HV + hv) * D * D + e] = __int_as_float(0x7fc00000);
+    }
+}
+
+// ------------------------------------------------------------------- local --
+
+namespace lo {
+constexpr int LNT = 256;
+// boxes of 64 tokens x 64 channels, first and second 64 channels: dV0 dO0 dV1
+// dO1 (upper planes), then the lower plane of dV with U's upper plane between,
+// so that 128 rows from either are an operand, U's lower plane, K0 Q0 K1 Q1
+constexpr int X_V = 0, X_VL = 4, X_U = 5, X_UL = 8, X_K = 10, X_Q = 11, BOXES = 14;
+// halves (64 of d_v) of S0 and dS1, two planes each
+constexpr uint32_t O_ST = BOXES * BOX;
+// the pair gradients [dkk; dqk] (128 rows of 64, swizzled as a box), two planes; the gates
+constexpr uint32_t O_L = O_ST + 4 * HALF, O_G = O_L + 4 * BOX;
+constexpr uint32_t SMEM = O_G + 1024 + 1024;
+constexpr uint32_t O_OUT = 0;                        // dk and dq [64][128] bf16, at the end
+// tensor memory: S0 [dV; dO]^T, dS1 U^T, [dkk; dqk] with K and the rest of dk, [dV; dO] U^T in two parts, [K; Q] K^T
+constexpr uint32_t T_A = 0, T_B = 128, T_C = 192, T_G = 320, T_G2 = 384, T_KK = 448;
+
+// Sum over the warp's lanes of each of 32 values: lane l gets that of x[l].
+__device__ __forceinline__ float lane_sums(float (&x)[32], int lane)
+{
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) {
+        const bool up = (lane & w) != 0;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float give = up ? x[i] : x[i + w], keep = up ? x[i + w] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+    }
+    return x[0];
+}
+}  // namespace lo
+
+struct LocalArgs {
+    Seqs seqs;
+    const void* g;
+    const uint8_t* rec;
+    const uint8_t* S0;
+    const uint8_t* dS1;
+    __nv_bfloat16 *dq, *dk, *dg, *dbeta;
+    float scale;
+    int HK, HV;
+    bool gate_f32;
+    uint64_t wait_ns;
+};
+struct LocalMaps {
+    CUtensorMap q, k, dO, dv, dvl, u, ul;
+};
+
+__global__ void __launch_bounds__(lo::LNT, 1)
+local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ LocalArgs p)
+{
+    using namespace lo;
+    using namespace tc;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[5];
+    __shared__ __align__(16) float sGh[C], sGl[C];
+    __shared__ float sDB[C], sA[4][C], sB[4][C], sW[4][C], sTot[2 * C], sDot[8];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t slot = blockIdx.x / p.HK;
+    const int hk = (int)(blockIdx.x % p.HK), group = p.HV / p.HK;
+    int n, chunk, begin, end;
+    if (!slot_chunk(p.seqs, slot, n, chunk, begin, end)) return;
+    const int t0 = begin + chunk * C, nv = min(C, end - t0);
+    const uint32_t base = smem_u32(sm), full = smem_u32(&bars[0]), full2 = smem_u32(&bars[1]);
+    // products complete: pairs, the states' first half, the second half and the rest (a barrier each: two may
+    // complete before a thread looks)
+    const uint32_t done[3] = {smem_u32(&bars[2]), smem_u32(&bars[3]), smem_u32(&bars[4])};
+    if (tid == 0) {
+        for (int b = 0; b < 5; ++b) mbar_init(smem_u32(&bars[b]), 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&s_tmem), 512);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    const uint32_t tm = s_tmem;
+    const Waits wait = {&s_abort, &g_back_status, p.wait_ns};
+    // this thread in tensor memory: lane 32 sp + lane, and the first or second half of the columns
+    const int sp = warp & 3, half = warp >> 2, row = 32 * sp + lane;
+    const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
+    float ak[32], aq[32];                            // dk, dq at channel `row`, 32 tokens, over the group
+#pragma unroll
+    for (int i = 0; i < 32; ++i) ak[i] = aq[i] = 0.f;
+    auto xb = [&](int b) { return sdesc_sw128(base + b * BOX); };
+    auto xb_mn = [&](int b) {                        // 128 channels as M or N: the next 64 are two boxes on
+        return (sdesc_sw128(base + b * BOX) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(2 * BOX >> 4) << 16);
+    };
+    auto finish = [&](int which, int m) {            // every thread waits for the products
+        if (!wait(done[which], m & 1) && warp == 0) mbar_wait(done[which], m & 1, DRAIN_NS);
+        fence_after_sync();
+    };
+    auto land = [&](uint32_t b, uint32_t parity) {
+        if (!wait(b, parity)) mbar_wait(b, parity, DRAIN_NS);
+    };
+    // the states' half h: S0 and dS1, upper and lower plane
+    auto load_states = [&](int64_t unit, int h, uint32_t b) {
+        for (int x = 0; x < 2; ++x)
+            for (int pl = 0; pl < 2; ++pl)
+                bulk_load(base + O_ST + (2 * x + pl) * HALF, (x ? p.dS1 : p.S0) + unit * (2 * (int64_t)PLANE) + pl * PLANE + h * HALF, HALF, b);
+    };
+    // products with the states' half in shared memory: S0 [dV; dO]^T and dS1 U^T (d_k as M)
+    auto state_products = [&](int h) {
+        const uint32_t id128 = idesc_bf16(128, 128, true, false), id64 = idesc_bf16(128, 64, true, false);
+        const uint64_t s0 = sdesc(base + O_ST, ST_LBO, ST_SBO), s0l = sdesc(base + O_ST + HALF, ST_LBO, ST_SBO);
+        const uint64_t ds = sdesc(base + O_ST + 2 * HALF, ST_LBO, ST_SBO), dsl = sdesc(base + O_ST + 3 * HALF, ST_LBO, ST_SBO);
+        const uint32_t more = h > 0 ? 1u : 0u;
+        mma4_ss(tm + T_A, s0, 16, xb(X_V + 2 * h), 2, id128, more);
+        mma4_ss(tm + T_A, s0l, 16, xb(X_V + 2 * h), 2, id128, 1u);
+        mma4_ss(tm + T_A, s0, 16, xb(X_VL + 2 * h), 2, id64, 1u);
+        mma4_ss(tm + T_B, ds, 16, xb(X_U + 2 * h), 2, id64, more);
+        mma4_ss(tm + T_B, dsl, 16, xb(X_U + 2 * h), 2, id64, 1u);
+        mma4_ss(tm + T_B, ds, 16, xb(X_UL + h), 2, id64, 1u);
+        mma_commit_w(done[1 + h]);
+    };
+    // <dS1, S0> over the half in shared memory
+    auto state_dot = [&]() {
+        float dot = 0.f;
+#pragma unroll 2
+        for (int e = tid; e < (int)(HALF / 16); e += LNT) {
+            uint4 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = *reinterpret_cast<const uint4*>(sm + O_ST + x * HALF + 16 * e);
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a0 = __uint_as_float(u[i] << 16) + __uint_as_float(u[4 + i] << 16);
+                const float a1 = __uint_as_float(u[i] & 0xffff0000u) + __uint_as_float(u[4 + i] & 0xffff0000u);
+                const float b0 = __uint_as_float(u[8 + i] << 16) + __uint_as_float(u[12 + i] << 16);
+                const float b1 = __uint_as_float(u[8 + i] & 0xffff0000u) + __uint_as_float(u[12 + i] & 0xffff0000u);
+                dot = fmaf(a0, b0, fmaf(a1, b1, dot));
+            }
+        }
+        return dot;
+    };
+
+#pragma unroll 1
+    for (int m = 0; m < group; ++m) {
+        const int hv = hk * group + m;
+        const int64_t unit = slot * p.HV + hv;
+        if (tid == 0) {
+            mbar_arrive_expect_tx(full, (m == 0 ? 14 : 10) * BOX + 4 * HALF + 1024);
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                const int x = hv * D + 64 * b, y = hk * D + 64 * b;
+                tma_load_2d(base + (X_V + 2 * b) * BOX, &maps.dv, x, t0, full);
+                tma_load_2d(base + (X_V + 1 + 2 * b) * BOX, &maps.dO, x, t0, full);
+                tma_load_2d(base + (X_VL + 2 * b) * BOX, &maps.dvl, x, t0, full);
+                tma_load_2d(base + (X_U + 2 * b) * BOX, &maps.u, x, t0, full);
+                tma_load_2d(base + (X_UL + b) * BOX, &maps.ul, x, t0, full);
+                if (m == 0) {
+                    tma_load_2d(base + (X_K + 2 * b) * BOX, &maps.k, y, t0, full);
+                    tma_load_2d(base + (X_Q + 2 * b) * BOX, &maps.q, y, t0, full);
+                }
+            }
+            load_states(unit, 0, full);
+            bulk_load(base + O_G, p.rec + unit * REC_BYTES + REC_NGAM, 1024, full);
+        }
+        if (warp == 2) {                              // the running sum of g in units of log 2
+            double x[2];
+            for (int i = 0; i < 2; ++i) {
+                const int rr = 2 * lane + i;
+                x[i] = rr < nv ? (double)cut_decay(gate(p.g, (int64_t)(t0 + rr) * p.HV + hv, p.gate_f32)) : 0.0;
+            }
+            double sum = x[0] + x[1];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, sum, off);
+                if (lane >= off) sum += y;
+            }
+            for (int i = 0; i < 2; ++i) {
+                const double G = (i == 0 ? sum - x[1] : sum) * 1.4426950408889634;
+                sGh[2 * lane + i] = (float)G;
+                sGl[2 * lane + i] = (float)(G - (double)(float)G);
+            }
+        }
+        land(full, m & 1);
+        if (nv < C) {                                 // rows behind the sequence
+            for (int e = tid; e < (C - nv) * BOXES * 8; e += LNT) {
+                const int piece = e & 7, box = (e >> 3) % BOXES, rr = nv + (e >> 3) / BOXES;
+                *reinterpret_cast<uint4*>(sm + box * BOX + rr * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_smem_to_async();
+        }
+        __syncthreads();
+        bool issued = false;
+        if (warp == 0 && (issued = !__any_sync(0xffffffffu, *(volatile int*)&s_abort != 0))) {
+            const uint32_t id = idesc_bf16(128, 64);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t more = h > 0 ? 1u : 0u;
+                if (m == 0) mma4_ss(tm + T_KK, xb(X_K + 2 * h), 2, xb(X_K + 2 * h), 2, id, more);
+                mma4_ss(tm + T_G, xb(X_V + 2 * h), 2, xb(X_U + 2 * h), 2, id, more);
+                mma4_ss(tm + T_G, xb(X_V + 2 * h), 2, xb(X_UL + h), 2, id, 1u);
+                mma4_ss(tm + T_G2, xb(X_VL + 2 * h), 2, xb(X_U + 2 * h), 2, id, more);
+            }
+            mma_commit_w(done[0]);
+            state_products(0);
+        }
+        float dot = state_dot();
+        finish(0, m);
+        {   // pair gradients: dkk_ri = -D_ri dV_r . U_i (i < r), dqk_ri = scale D_ri dO_r . U_i (i <= r)
+            float x[32], y[32];
+            const int r = row % C;
+            const bool is_q = row >= C;
+            tmem_ld32(t + T_G + 32 * half, x);
+            if (!is_q) tmem_ld32(t + T_G2 + 32 * half, y);      // warp-uniform
+            wait_ld();
+            if (!is_q) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] += y[i];
+            }
+            tmem_ld32(t + T_KK + 32 * half, y);
+            wait_ld();
+            const float gh = sGh[r], gl = sGl[r], f = is_q ? p.scale : -1.f;
+            const int last = is_q ? r : r - 1;
+            float pre = 0.f;                          // of w over the columns before
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 ch = *reinterpret_cast<const float4*>(sGh + 32 * half + i), cl = *reinterpret_cast<const float4*>(sGl + 32 * half + i);
+                const float dh[4] = {ch.x, ch.y, ch.z, ch.w}, dl[4] = {cl.x, cl.y, cl.z, cl.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 32 * half + i + e;
+                    if (!is_q && c == r) sDB[r] = x[i + e];
+                    x[i + e] = c <= last ? f * exp2f((gh - dh[e]) + (gl - dl[e])) * x[i + e] : 0.f;
+                    pre = fmaf(x[i + e], c < r ? y[i + e] : 0.f, pre);
+                    y[i + e] = c + 1 <= r ? pre : 0.f;           // token t = c + 1: this row's part of sum_{i < t <= r} w_ri
+                }
+            }
+            if (half == 0) sTot[row] = pre;
+            const float ws = lane_sums(y, lane);
+            sW[sp][32 * half + lane] = ws;            // for token 32 half + lane + 1, columns of this half only
+#pragma unroll
+            for (int pc = 0; pc < 4; ++pc) {
+                float hi[4], lw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split_bf16(x[8 * pc + 2 * e], x[8 * pc + 2 * e + 1], hi[e], lw[e]);
+                uint8_t* dst = sm + O_L + row * 128 + (((4 * half + pc) ^ (row & 7)) * 16);
+                *reinterpret_cast<float4*>(dst) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<float4*>(dst + 2 * BOX) = make_float4(lw[0], lw[1], lw[2], lw[3]);
+            }
+        }
+        finish(1, m);                                 // the states' first half has been read
+        fence_smem_to_async();
+        fence_before_sync();
+        __syncthreads();
+        fence_after_sync();
+        if (tid == 0) {
+            mbar_arrive_expect_tx(full2, 4 * HALF);
+            load_states(unit, 1, full2);
+        }
+        if (warp == 0 && issued) {
+            __syncwarp();
+            const uint32_t id128 = idesc_bf16(128, 128, true, false), idmn = idesc_bf16(128, 64, true, true);
+            const uint64_t l = sdesc_sw128(base + O_L), k = xb_mn(X_K), q = xb_mn(X_Q);
+            constexpr uint64_t LO = 2 * BOX >> 4, Q_ROWS = BOX >> 4;
+            // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk
+            mma4_ss(tm + T_C, k, 128, l, 2, id128, 0u);
+            mma4_ss(tm + T_C, k, 128, l + LO, 2, id128, 1u);
+            mma4_ss(tm + T_C, k, 128, l, 128, idmn, 1u);
+            mma4_ss(tm + T_C, k, 128, l + LO, 128, idmn, 1u);
+            mma4_ss(tm + T_C, q, 128, l + Q_ROWS, 128, idmn, 1u);
+            mma4_ss(tm + T_C, q, 128, l + LO + Q_ROWS, 128, idmn, 1u);
+        }
+        land(full2, m & 1);
+        if (warp == 0 && issued) {
+            __syncwarp();
+            state_products(1);
+        }
+        dot += state_dot();
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (lane == 0) sDot[warp] = dot;
+        finish(2, m);
+        const float* gates = reinterpret_cast<const float*>(sm + O_G);       // -gam, eta, scale gam, beta: 64 each
+        {   // channel `row`, tokens 32 half .. + 31
+            float a[32], b[32], pa[32];
+            const uint8_t* kp = sm + (X_K + 2 * (row / 64)) * BOX + (row % 8) * 2;
+            const int piece = (row % 64) / 8;
+            auto at = [&](const uint8_t* x, int tok) {
+                return to_f32(*reinterpret_cast<const __nv_bfloat16*>(x + tok * 128 + ((piece ^ (tok & 7)) * 16)));
+            };
+            tmem_ld32(t + T_A + 32 * half, a);        // dV S0^T
+            tmem_ld32(t + T_C + 32 * half, b);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float z = gates[32 * half + i] * a[i];
+                pa[i] = z * at(kp, 32 * half + i);
+                ak[i] += z + b[i];
+            }
+            tmem_ld32(t + T_A + 64 + 32 * half, a);   // dO S0^T
+            tmem_ld32(t + T_C + 64 + 32 * half, b);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float z = gates[2 * C + 32 * half + i] * a[i];
+                pa[i] = fmaf(z, at(kp + BOX, 32 * half + i), pa[i]);
+                aq[i] += z + b[i];
+            }
+            sA[sp][32 * half + lane] = lane_sums(pa, lane);
+            tmem_ld32(t + T_B + 32 * half, a);        // U dS1^T
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float z = gates[C + 32 * half + i] * a[i];
+                b[i] = z * at(kp, 32 * half + i);
+                ak[i] += z;
+            }
+            sB[sp][32 * half + lane] = lane_sums(b, lane);
+        }
+        fence_smem_to_async();                        // the next loads write where these threads did
+        fence_before_sync();
+        __syncthreads();                              // everything of this value head has been read
+        fence_after_sync();
+        if (warp == 0) {                              // dg and dbeta, two tokens per lane
+            float a[2], b[2], w[2], tot[2], dd = lane < 8 ? sDot[lane] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * lane + i;
+                a[i] = (sA[0][r] + sA[1][r]) + (sA[2][r] + sA[3][r]);
+                b[i] = (sB[0][r] + sB[1][r]) + (sB[2][r] + sB[3][r]);
+                w[i] = r > 0 ? (sW[0][r - 1] + sW[1][r - 1]) + (sW[2][r - 1] + sW[3][r - 1]) : 0.f;
+                tot[i] = sTot[r] + sTot[C + r];       // row r's first 32 columns
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
+            float sa = a[0] + a[1], sb = b[0] + b[1], st = tot[0] + tot[1];
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float x = __shfl_down_sync(0xffffffffu, sa, off), y = __shfl_up_sync(0xffffffffu, sb, off);
+                const float z = __shfl_down_sync(0xffffffffu, st, off);
+                if (lane + off < 32) sa += x, st += z;
+                if (lane >= off) sb += y;
+            }
+            // sa, st: from token 2 lane on; sb: up to token 2 lane + 1
+            const float before = __shfl_up_sync(0xffffffffu, sb, 1);
+            const float from0[2] = {sa, sa - a[0]}, tot0[2] = {st, st - tot[0]};
+            const float b0 = lane > 0 ? before : 0.f, upto[2] = {b0, b0 + b[0]};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 2 * lane + i;
+                if (r < nv) {
+                    const int64_t o = (int64_t)(t0 + r) * p.HV + hv;
+                    const float beta = gates[3 * C + r];
+                    const float pairs = w[i] + (r > 32 ? tot0[i] : 0.f);
+                    p.dg[o] = __float2bfloat16_rn(fmaf(-gates[C - 1], dd, from0[i] + upto[i] + pairs));
+                    p.dbeta[o] = __float2bfloat16_rn(sDB[r] / beta / beta);
+                }
+            }
+        }
+        __syncthreads();
+    }
+    {   // dk, dq: channel-major in registers, token-major in memory
+        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + O_OUT);
+        const bool bad = *(volatile int*)&s_abort != 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int tok = 32 * half + i;
+            so[tok * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : ak[i]);
+            so[(C + tok) * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : aq[i]);
+        }
+        __syncthreads();
+#pragma unroll 4
+        for (int e = tid; e < 2 * C * D / 8; e += LNT) {
+            const int r = (e / (D / 8)) % C, c8 = e % (D / 8);
+            if (r < nv)
+                *reinterpret_cast<uint4*>((e >= C * D / 8 ? p.dq : p.dk) + ((int64_t)(t0 + r) * p.HK + hk) * D + 8 * c8) =
+                    *reinterpret_cast<const uint4*>(so + 8 * e);
+        }
+    }
+    fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_sync();
+        tmem_dealloc(tm, 512);
+    }
+    if (*(volatile int*)&s_abort) {
+        const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+        for (int e = tid; e < nv * group; e += LNT) {
+            const int64_t at = (int64_t)(t0 + e / group) * p.HV + hk * group + e % group;
+            p.dg[at] = nan;
+            p.dbeta[at] = nan;
+        }
+    }
+}
+
+// Tokens before the first sequence and behind the last belong to none: their
+// gradients are zero.
+struct Outside {
+    __nv_bfloat16* p[5];
+    int64_t row[5];
+};
+__global__ void outside_kernel(const Outside z, const int* __restrict__ cu, int n_seq, int64_t tokens)
+{
+    const int64_t a = min((int64_t)max(cu[0], 0), tokens), b = min(max((int64_t)cu[n_seq], a), tokens);
+    const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    for (int i = 0; i < 5; ++i) {
+        for (int64_t e = at; e < a * z.row[i]; e += step) z.p[i][e] = __float2bfloat16_rn(0.f);
+        for (int64_t e = b * z.row[i] + at; e < tokens * z.row[i]; e += step) z.p[i][e] = __float2bfloat16_rn(0.f);
+    }
+}
+
+}  // namespace bk
+
+static DeviceFlags g_back_attr_done;
+
+}  // namespace gdn
+
+cudaError_t act8_launch(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
+                        const int64_t* cols, const int64_t* strides, bool pack, cudaStream_t stream);
+
+// scales: null (q, k, v bf16 with the given strides) or the scales of q, k, v
+// in 8 bits (dense), which are expanded into the workspace first.
+cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
+                                const void* beta, const float* h0, const void* dO, const float* dhT, void* dq, void* dk,
+                                void* dv, void* dg, void* dbeta, float* dh0, const int* cu, float scale, int N, int T,
+                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32,
+                                cudaStream_t stream)
+{
+    using namespace gdn;
+    using namespace bk;
+    Args a = {};
+    a.seqs.cu = cu;
+    a.seqs.n_seq = N;
+    a.seqs.n_slots = N;
+    a.seqs.len = T;
+    a.seqs.tokens = cu ? T : (int64_t)N * T;
+    const int64_t tokens = a.seqs.tokens;
+    const size_t state = (size_t)N * HV * D * D * sizeof(float);
+    if (tokens == 0) {       // no token: the start states' gradient is the last states'
+        if (!dh0) return cudaSuccess;
+        return dhT ? cudaMemcpyAsync(dh0, dhT, state, cudaMemcpyDeviceToDevice, stream) : cudaMemsetAsync(dh0, 0, state, stream);
+    }
+    cudaError_t e = once_per_device(g_back_attr_done, [](int) {
+        const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        const cudaError_t r = cudaFuncSetAttribute(chains_kernel, at, (int)SMEM);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(local_kernel, at, (int)lo::SMEM);
+    });
+    if (e != cudaSuccess) return e;
+    const size_t units = (size_t)slot_count(a.seqs) * HV;
+    const size_t u_bytes = (size_t)tokens * HV * D * 2, qk_bytes = (size_t)tokens * HK * D * 2;
+    size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE) + 3 * u_bytes;
+    if (scales) bytes += 2 * qk_bytes + u_bytes;
+    uint8_t* ws = nullptr;
+    keep_pool_memory();
+    e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
+    if (e != cudaSuccess) return e;
+    uint8_t* at = ws;
+    auto take = [&](size_t b) { uint8_t* r = at; at += b; return r; };
+    a.rec = take(units * REC_BYTES);
+    a.S0 = take(units * 2 * PLANE);
+    a.dS1 = take(units * 2 * PLANE);
+    a.u[0] = (__nv_bfloat16*)take(u_bytes);
+    a.u[1] = (__nv_bfloat16*)take(u_bytes);
+    a.dv[0] = (__nv_bfloat16*)dv;
+    a.dv[1] = (__nv_bfloat16*)take(u_bytes);
+    if (scales) {
+        void* out[3] = {take(qk_bytes), take(qk_bytes), take(u_bytes)};
+        const void* src[3] = {q, k, v};
+        void* sc[3] = {const_cast<void*>(scales[0]), const_cast<void*>(scales[1]), const_cast<void*>(scales[2])};
+        const int64_t rows[3] = {tokens, tokens, tokens}, cols[3] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D};
+        e = act8_launch(3, src, out, sc, rows, cols, nullptr, false, stream);
+        q = out[0], k = out[1], v = out[2];
+        q_stride = k_stride = (int64_t)HK * D;
+        v_stride = (int64_t)HV * D;
+    }
+    a.h0 = h0;
+    a.dhT = dhT;
+    a.dh0 = dh0;
+    a.HK = HK;
+    a.HV = HV;
+    a.wait_ns = bounded_wait_limit_ns();
+    LocalArgs l = {};
+    l.seqs = a.seqs;
+    l.g = g;
+    l.rec = a.rec;
+    l.S0 = a.S0;
+    l.dS1 = a.dS1;
+    l.dq = (__nv_bfloat16*)dq;
+    l.dk = (__nv_bfloat16*)dk;
+    l.dg = (__nv_bfloat16*)dg;
+    l.dbeta = (__nv_bfloat16*)dbeta;
+    l.scale = scale;
+    l.HK = HK;
+    l.HV = HV;
+    l.gate_f32 = gate_f32;
+    l.wait_ns = a.wait_ns;
+    LocalMaps maps;
+    CUtensorMap mv;
+    const int64_t row = (int64_t)HV * D;
+    if (e == cudaSuccess &&
+        (!make_token_map(&maps.q, q, tokens, (int64_t)HK * D, q_stride) || !make_token_map(&maps.k, k, tokens, (int64_t)HK * D, k_stride) ||
+         !make_token_map(&mv, v, tokens, row, v_stride) || !make_token_map(&maps.dO, dO, tokens, row, row) ||
+         !make_token_map(&maps.dv, a.dv[0], tokens, row, row) || !make_token_map(&maps.dvl, a.dv[1], tokens, row, row) ||
+         !make_token_map(&maps.u, a.u[0], tokens, row, row) || !make_token_map(&maps.ul, a.u[1], tokens, row, row)))
+        e = cudaErrorInvalidValue;
+    if (e == cudaSuccess && cu) {
+        const int64_t rows[5] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D, HV, HV};
+        Outside z = {};
+        void* out[5] = {dq, dk, dv, dg, dbeta};
+        for (int i = 0; i < 5; ++i) z.p[i] = (__nv_bfloat16*)out[i], z.row[i] = rows[i];
+        outside_kernel<<<64, 256, 0, stream>>>(z, cu, N, tokens);
+        note_launches(1);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && N > 0)
+        e = prep_launch(maps.q, maps.k, g, beta, a.seqs, const_cast<uint8_t*>(a.rec), scale, HK, HV, gate_f32, 9.313225746154785e-10f, stream);
+    if (e == cudaSuccess && N > 0) {
+        chains_kernel<<<(unsigned)(2 * (int64_t)N * HV), NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess && N > 0) {
+        local_kernel<<<(unsigned)(slot_count(a.seqs) * HK), lo::LNT, lo::SMEM, stream>>>(maps, l);
+        e = cudaGetLastError();
+    }
+    if (N > 0) note_launches(2);
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    return e == cudaSuccess ? ef : e;
+}
+
+int gdn_backward_status(cudaStream_t stream)
+{
+    int st = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&st, gdn::g_back_status, sizeof(int), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaMemcpyToSymbolAsync(gdn::g_back_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    return st;
+}
+
+}  // namespace kda

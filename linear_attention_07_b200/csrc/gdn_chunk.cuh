@@ -196,7 +196,7 @@ constexpr uint64_t DRAIN_NS = 20000000ull;           // after an expired wait: 2
 bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride);
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, cudaStream_t stream);
+                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, float beta_floor, cudaStream_t stream);
 
 }  // namespace gdn
 }  // namespace kda

@@ -425,7 +425,7 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         keep_pool_memory();
         e = cudaMallocAsync(reinterpret_cast<void**>(&rec), (size_t)slot_count(a.seqs) * HV * REC_BYTES, stream);
         if (e != cudaSuccess) return e;
-        e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, stream);
+        e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, 0.f, stream);
     }
     a.rec = rec;
     if (e == cudaSuccess) {

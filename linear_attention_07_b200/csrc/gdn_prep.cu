@@ -53,7 +53,7 @@ __device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, in
 __global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, uint8_t* __restrict__ rec_all, float scale, int HK, int HV,
-            bool gate_f32, uint64_t wait_ns)
+            bool gate_f32, float beta_floor, uint64_t wait_ns)
 {
     using namespace prep;
     using namespace tc;
@@ -95,7 +95,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             const int r = 2 * lane + i;
             const int64_t at = (int64_t)(t0 + r) * HV + hv;
             x[i] = r < nv ? (double)cut_decay(gate(g, at, gate_f32)) : 0.0;
-            sB[r] = r < nv ? gate(beta, at, gate_f32) : 0.f;
+            const float b = r < nv ? gate(beta, at, gate_f32) : 0.f;
+            sB[r] = r < nv && fabsf(b) < beta_floor ? copysignf(beta_floor, b) : b;
         }
         double sum = x[0] + x[1];
 #pragma unroll
@@ -279,14 +280,14 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
 static DeviceFlags g_prep_attr_done;
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, cudaStream_t stream)
+                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, float beta_floor, cudaStream_t stream)
 {
     const cudaError_t e = once_per_device(g_prep_attr_done, [](int) {
         return cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep::SMEM);
     });
     if (e != cudaSuccess) return e;
     prep_kernel<<<(unsigned)(slot_count(seqs) * HV), prep::NT, prep::SMEM, stream>>>(
-        mq, mk, g, beta, seqs, rec, scale, HK, HV, gate_f32, bounded_wait_limit_ns());
+        mq, mk, g, beta, seqs, rec, scale, HK, HV, gate_f32, beta_floor, bounded_wait_limit_ns());
     note_launches(1);
     return cudaGetLastError();
 }

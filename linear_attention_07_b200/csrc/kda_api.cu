@@ -76,7 +76,13 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
                                const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
                                float scale, int N, int T, int HK, int HV, int64_t q_stride, int64_t k_stride,
                                int64_t v_stride, bool gate_f32, cudaStream_t stream);
+cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
+                                const void* beta, const float* h0, const void* dO, const float* dhT, void* dq, void* dk,
+                                void* dv, void* dg, void* dbeta, float* dh0, const int* cu, float scale, int N, int T,
+                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32,
+                                cudaStream_t stream);
 int gdn_prep_status(cudaStream_t stream);
+int gdn_backward_status(cudaStream_t stream);
 int gdn_forward_status(cudaStream_t stream);
 cudaError_t act8_launch(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
                         const int64_t* cols, const int64_t* strides, bool pack, cudaStream_t stream);
@@ -347,6 +353,56 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
                                         q_stride, k_stride, v_stride, gate_f32 != 0, (cudaStream_t)stream));
 }
 
+static int gdn_chunk_bwd_any(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
+                             const void* beta, const float* h0, const void* dO, const float* dhT, void* dq, void* dk,
+                             void* dv, void* dg, void* dbeta, float* dh0, const int32_t* cu_seqlens, float scale, int N,
+                             int T, int HK, int HV, int d_k, int d_v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, int gate_f32, kda_stream_t stream)
+{
+    int st = check_gdn_heads(HK, HV, d_k, d_v, q_stride, k_stride, v_stride);
+    if (st == KDA_OK) st = check_gdn_tokens(cu_seqlens, nullptr, 0, N, T, HV);
+    if (st != KDA_OK) return st;
+    if (!(d_k == 128 && d_v == 128)) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)N * HV > 0x3fffffffll) return KDA_ERR_UNSUPPORTED;      // two CTAs each
+    if (!opt_ptr_ok(h0) || !opt_ptr_ok(dhT) || !opt_ptr_ok(dh0)) return KDA_ERR_INVALID_ARG;
+    if (HV == 0 || (N == 0 && (T == 0 || !cu_seqlens))) return KDA_OK;
+    if (T == 0 && dh0 == nullptr) return KDA_OK;
+    if (T > 0) {
+        if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(dO) || !ptr_ok(dq) || !ptr_ok(dk) || !ptr_ok(dv))
+            return KDA_ERR_INVALID_ARG;
+        const unsigned ge = gate_f32 ? 4 : 2;
+        if (!elem_ok(g, ge) || !elem_ok(beta, ge) || !elem_ok(dg, 2) || !elem_ok(dbeta, 2)) return KDA_ERR_INVALID_ARG;
+        if (scales && (!scales[0] || !scales[1] || !scales[2])) return KDA_ERR_INVALID_ARG;
+    }
+    return status_of(gdn_backward_launch(q, k, v, scales, g, beta, h0, dO, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens,
+                                         scale, N, T, HK, HV, q_stride, k_stride, v_stride, gate_f32 != 0,
+                                         (cudaStream_t)stream));
+}
+
+int kda_gdn_chunk_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
+                      const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
+                      void* dg, void* dbeta, float* dh0, const int32_t* cu_seqlens, float scale,
+                      int N, int T, int HK, int HV, int d_k, int d_v,
+                      int64_t q_stride, int64_t k_stride, int64_t v_stride, int gate_f32,
+                      kda_stream_t stream)
+{
+    return gdn_chunk_bwd_any(q, k, v, nullptr, g, beta, h0, dO, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens, scale, N, T,
+                             HK, HV, d_k, d_v, q_stride, k_stride, v_stride, gate_f32, stream);
+}
+
+int kda_gdn_chunk_bwd_packed8(const void* q8, const void* k8, const void* v8, const void* q_scales,
+                              const void* k_scales, const void* v_scales, const void* g, const void* beta,
+                              const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
+                              void* dg, void* dbeta, float* dh0, const int32_t* cu_seqlens, float scale,
+                              int N, int T, int HK, int HV, int d_k, int d_v, int gate_f32,
+                              kda_stream_t stream)
+{
+    const void* scales[3] = {q_scales, k_scales, v_scales};
+    if (HK < 0 || HV < 0 || d_k <= 0 || d_v <= 0 || d_k > 4096 || d_v > 4096) return KDA_ERR_INVALID_ARG;
+    return gdn_chunk_bwd_any(q8, k8, v8, scales, g, beta, h0, dO, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens, scale, N, T,
+                             HK, HV, d_k, d_v, (int64_t)HK * d_k, (int64_t)HK * d_k, (int64_t)HV * d_v, gate_f32, stream);
+}
+
 int kda_gdn_decode_step(const void* q, const void* k, const void* v, const void* g, const void* beta,
                         float* state, void* o, const int32_t* slots, int n_slots, float scale,
                         int N, int HK, int HV, int d_k, int d_v,
@@ -412,7 +468,8 @@ const char* kda_status_string(int status)
 int kda_device_status(kda_stream_t stream)
 {
     int st = KDA_OK;
-    for (auto* part : {prefill_device_status, bwd_device_status, gdn_prep_status, gdn_forward_status}) {
+    for (auto* part : {prefill_device_status, bwd_device_status, gdn_prep_status, gdn_forward_status,
+                       gdn_backward_status}) {
         const int s = part((cudaStream_t)stream);     // each reads and clears its own word
         if (s == KDA_ERR_CUDA) return s;
         if (s != KDA_OK) st = s;
