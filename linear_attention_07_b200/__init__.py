@@ -437,60 +437,89 @@ def chunk_bwd_raw(q_raw, k_raw, v, z, beta, h0, dO, dhT=None, *, want_dh0=True):
 
 
 # ------------------------------------- one decay per head (gated delta rule) --
+# These calls are made once per layer and token, so their checks are written to
+# cost little: one comparison of type, shape and device per tensor, the reason
+# looked for only when it fails.
 
-def _check_tokens(t, name, lead, heads, d, device):
+_BF16 = _F32 = _I32 = _torch = None
+
+
+def _types():
+    """torch, with the dtypes the calls compare against at hand."""
+    global _BF16, _F32, _I32, _torch
+    if _torch is None:
+        import torch
+        _BF16, _F32, _I32, _torch = torch.bfloat16, torch.float32, torch.int32, torch
+    return _torch
+
+
+def _call(fn_name, dev, *args):
+    """The library function on the current stream of `dev`, made the current device."""
+    torch = _torch
+    fn = getattr(_lib or load_library(), fn_name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != KDA_OK:
+        raise KdaError(fn_name, st)
+
+
+def _dense(t, name, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape (None: None)."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _check_tokens(t, name, lead, heads, d, dev):
     """A bf16 tensor [*lead, heads, d] whose heads are dense and whose tokens
     are a constant number of elements apart; returns that number."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError("%s must be %s, got %s" % (name, torch.bfloat16, t.dtype))
-    if tuple(t.shape) != tuple(lead) + (heads, d):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(lead) + (heads, d), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if t.numel() == 0:
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be %s, got %s" % (name, _BF16, t.dtype))
+    if t.shape != (*lead, heads, d):
+        raise ValueError("%s must have shape %s, got %s" % (name, (*lead, heads, d), tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("%s must be on %s, got %s" % (name, dev, t.device))
+    if t.is_contiguous():
         return heads * d
     st = t.stride()
-    # the stride of the last token axis with more than one entry
-    step = next((s for s, n in zip(reversed(st[:-2]), reversed(t.shape[:-2])) if n > 1), heads * d)
-    n = 1
-    for s, size in zip(reversed(st[:-2]), reversed(t.shape[:-2])):
-        if size > 1 and s != step * n:
-            raise ValueError("%s: the tokens must be equally spaced, got strides %s" % (name, st))
-        n *= size
+    if t.numel() == 0:
+        return heads * d
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError("%s: a token's heads must be dense, got strides %s" % (name, st))
+    step, n = 0, 1                                   # from the last token axis with more than one entry
+    for size, s in zip(t.shape[-3::-1], st[-3::-1]):
+        if size > 1:
+            if step and s != step * n:
+                raise ValueError("%s: the tokens must be equally spaced, got strides %s" % (name, st))
+            if not step:
+                step = s
+            n *= size
+    step = step or heads * d
     if step % 8 != 0 or step < heads * d:
         raise ValueError("%s: the token stride must be a multiple of 8 and at least %d, got %d" % (name, heads * d, step))
     return step
 
 
-def _check_gates(g, beta, lead, hv, device):
-    import torch
-    if g.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError("g must be torch.float32 or torch.bfloat16, got %s" % g.dtype)
-    _check(g, "g", g.dtype, tuple(lead) + (hv,), device)
-    _check(beta, "beta", g.dtype, tuple(lead) + (hv,), device)
-    return int(g.dtype == torch.float32)
+def _check_gates(g, beta, shape, dev):
+    """Addresses of g and beta and whether they are fp32."""
+    kind = g.dtype
+    if kind is not _F32 and kind is not _BF16:
+        raise TypeError("g must be torch.float32 or torch.bfloat16, got %s" % kind)
+    return _dense(g, "g", kind, shape, dev), _dense(beta, "beta", kind, shape, dev), 1 if kind is _F32 else 0
 
 
-def _check_index(t, name, n, device):
-    import torch
-    if t is not None:
-        _check(t, name, torch.int32, (n,), device)
-
-
-def _gdn_sequences(q, cu_seqlens, dev):
-    """(N, T of the C call, number of sequences) of q [B, T, HK, dk] with or without cu_seqlens."""
-    B, T = q.shape[:2]
+def _gdn_sequences(B, T, cu_seqlens, dev):
+    """(N, T of the C call) with or without cu_seqlens."""
     if cu_seqlens is None:
         return B, T
-    import torch
     if B != 1:
         raise ValueError("with cu_seqlens the tokens are packed: the first axis must be 1, got %d" % B)
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must have shape (N + 1,), got %s" % (tuple(cu_seqlens.shape),))
-    _check(cu_seqlens, "cu_seqlens", torch.int32, tuple(cu_seqlens.shape), dev)
+    _dense(cu_seqlens, "cu_seqlens", _I32, cu_seqlens.shape, dev)
     return cu_seqlens.shape[0] - 1, T
 
 
@@ -509,39 +538,33 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slot
     starts from row slots[n] and its last state is written there; a slot
     outside the pool starts from zero and keeps none.  Rows of o that belong to
     no sequence are not written.  Returns (o, hT), hT the pool with slots."""
-    import torch
+    torch = _types()
     B, T, HK, dk = q.shape
     HV, dv = v.shape[-2:]
     dev = _require_cuda(q)
     qs = _check_tokens(q, "q", (B, T), HK, dk, dev)
     ks = _check_tokens(k, "k", (B, T), HK, dk, dev)
     vs = _check_tokens(v, "v", (B, T), HV, dv, dev)
-    gf = _check_gates(g, beta, (B, T), HV, dev)
-    N, Tc = _gdn_sequences(q, cu_seqlens, dev)
-    _check_index(slots, "slots", N, dev)
-    rows = N
+    gp, bp, gf = _check_gates(g, beta, (B, T, HV), dev)
+    N, Tc = _gdn_sequences(B, T, cu_seqlens, dev)
+    rows, sp = N, None
     if slots is not None:
         if h0 is None:
             raise ValueError("slots name rows of a pool of states: h0 must be given")
         if hT is not None and hT is not h0:
             raise ValueError("with slots the last states are written to the pool: hT must not be another tensor")
+        sp = _dense(slots, "slots", _I32, (N,), dev)
         rows = h0.shape[0]
         hT = h0 if output_final_state else None
-    if h0 is not None:
-        _check(h0, "h0", torch.float32, (rows, HV, dk, dv), dev)
+    state = (rows, HV, dk, dv)
+    hp = None if h0 is None else _dense(h0, "h0", _F32, state, dev)
     if o is None:
-        o = torch.empty((B, T, HV, dv), dtype=torch.bfloat16, device=dev)
-    _check(o, "o", torch.bfloat16, (B, T, HV, dv), dev)
+        o = torch.empty((B, T, HV, dv), dtype=_BF16, device=dev)
     if hT is None and output_final_state:
-        hT = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=dev)
-    if hT is not None:
-        _check(hT, "hT", torch.float32, (rows, HV, dk, dv), dev)
-    with torch.cuda.device(dev):
-        st = load_library().kda_gdn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(h0), _ptr(o), _ptr(hT),
-                                              _ptr(cu_seqlens), _ptr(slots), rows, float(scale), N, Tc, HK, HV, dk, dv,
-                                              qs, ks, vs, gf, _stream(dev))
-    if st != KDA_OK:
-        raise KdaError("kda_gdn_chunk_fwd", st)
+        hT = torch.empty(state, dtype=_F32, device=dev)
+    _call("kda_gdn_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, hp,
+          _dense(o, "o", _BF16, (B, T, HV, dv), dev), None if hT is None else _dense(hT, "hT", _F32, state, dev),
+          None if cu_seqlens is None else cu_seqlens.data_ptr(), sp, rows, scale, N, Tc, HK, HV, dk, dv, qs, ks, vs, gf)
     return o, hT
 
 
@@ -555,43 +578,35 @@ def gdn_chunk_bwd(q, k, v, g, beta, h0, dO, dhT=None, *, scale=1.0, cu_seqlens=N
     dk (summed over the value heads of a group), dv, dg, dbeta are bf16, dh0 is
     fp32 (None if want_dh0 is False).  Tokens that belong to no sequence get
     zero gradients."""
-    import torch
-    eight = [isinstance(x, Packed8) for x in (q, k, v)]
-    if any(eight) and not all(eight):
+    torch = _types()
+    eight = isinstance(q, Packed8)
+    if isinstance(k, Packed8) != eight or isinstance(v, Packed8) != eight:
         raise TypeError("q, k and v must all be tensors or all be Packed8")
     B, T, HK, dk = q.shape
     HV, dv = v.shape[-2:]
-    dev = _require_cuda(q.data if eight[0] else q)
-    strides = []
-    for name, t, heads, d in (("q", q, HK, dk), ("k", k, HK, dk), ("v", v, HV, dv)):
-        if eight[0]:
-            _check_packed8(t, name, dev)
-            if tuple(t.shape) != (B, T, heads, d):
-                raise ValueError("%s must have shape %s, got %s" % (name, (B, T, heads, d), tuple(t.shape)))
-        else:
-            strides.append(_check_tokens(t, name, (B, T), heads, d, dev))
-    gf = _check_gates(g, beta, (B, T), HV, dev)
-    N, Tc = _gdn_sequences(q, cu_seqlens, dev)
-    _check(dO, "dO", torch.bfloat16, (B, T, HV, dv), dev)
-    for name, t in (("h0", h0), ("dhT", dhT)):
-        if t is not None:
-            _check(t, name, torch.float32, (N, HV, dk, dv), dev)
-    gq, gk = (torch.empty((B, T, HK, dk), dtype=torch.bfloat16, device=dev) for _ in range(2))
-    gv = torch.empty((B, T, HV, dv), dtype=torch.bfloat16, device=dev)
-    gg, gb = (torch.empty((B, T, HV), dtype=torch.bfloat16, device=dev) for _ in range(2))
-    gh = torch.empty((N, HV, dk, dv), dtype=torch.float32, device=dev) if want_dh0 else None
-    rest = [_ptr(x) for x in (g, beta, h0, dO, dhT, gq, gk, gv, gg, gb, gh, cu_seqlens)]
-    sizes = (float(scale), N, Tc, HK, HV, dk, dv)
-    with torch.cuda.device(dev):
-        if eight[0]:
-            fn = "kda_gdn_chunk_bwd_packed8"
-            st = load_library().kda_gdn_chunk_bwd_packed8(*(_ptr(x.data) for x in (q, k, v)), *(_ptr(x.scales) for x in (q, k, v)),
-                                                          *rest, *sizes, gf, _stream(dev))
-        else:
-            fn = "kda_gdn_chunk_bwd"
-            st = load_library().kda_gdn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), *rest, *sizes, *strides, gf, _stream(dev))
-    if st != KDA_OK:
-        raise KdaError(fn, st)
+    dev = _require_cuda(q.data if eight else q)
+    if eight:
+        ins, scales, strides = zip(*((*_packed8(t, name, (B, T, heads, d), dev), heads * d) for name, t, heads, d in
+                                     (("q", q, HK, dk), ("k", k, HK, dk), ("v", v, HV, dv))))
+    else:
+        strides = (_check_tokens(q, "q", (B, T), HK, dk, dev), _check_tokens(k, "k", (B, T), HK, dk, dev),
+                   _check_tokens(v, "v", (B, T), HV, dv, dev))
+        ins = (q.data_ptr(), k.data_ptr(), v.data_ptr())
+    gp, bp, gf = _check_gates(g, beta, (B, T, HV), dev)
+    N, Tc = _gdn_sequences(B, T, cu_seqlens, dev)
+    state = (N, HV, dk, dv)
+    bf = dict(dtype=_BF16, device=dev)
+    gq, gk = torch.empty((B, T, HK, dk), **bf), torch.empty((B, T, HK, dk), **bf)
+    gv, gg, gb = torch.empty((B, T, HV, dv), **bf), torch.empty((B, T, HV), **bf), torch.empty((B, T, HV), **bf)
+    gh = torch.empty(state, dtype=_F32, device=dev) if want_dh0 else None
+    rest = (gp, bp, None if h0 is None else _dense(h0, "h0", _F32, state, dev), _dense(dO, "dO", _BF16, (B, T, HV, dv), dev),
+            None if dhT is None else _dense(dhT, "dhT", _F32, state, dev), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
+            gg.data_ptr(), gb.data_ptr(), None if gh is None else gh.data_ptr(),
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), scale, N, Tc, HK, HV, dk, dv)
+    if eight:
+        _call("kda_gdn_chunk_bwd_packed8", dev, *ins, *scales, *rest, gf)
+    else:
+        _call("kda_gdn_chunk_bwd", dev, *ins, *rest, *strides, gf)
     return gq, gk, gv, gg, gb, gh
 
 
@@ -604,26 +619,20 @@ def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):
     [N, HV, dk, dv], or a pool [rows, HV, dk, dv] with slots [N] (int32, on the
     device) naming each request's row; a slot outside the pool marks a padded
     request (o = 0, no state).  Returns o [N, HV, dv] bf16."""
-    import torch
+    torch = _types()
     N, HK, dk = q.shape
     HV, dv = v.shape[-2:]
     dev = _require_cuda(q)
     qs = _check_tokens(q, "q", (N,), HK, dk, dev)
     ks = _check_tokens(k, "k", (N,), HK, dk, dev)
     vs = _check_tokens(v, "v", (N,), HV, dv, dev)
-    gf = _check_gates(g, beta, (N,), HV, dev)
-    rows = N if slots is None else state.shape[0]
-    _check(state, "state", torch.float32, (rows, HV, dk, dv), dev)
-    _check_index(slots, "slots", N, dev)
+    gp, bp, gf = _check_gates(g, beta, (N, HV), dev)
+    rows, sp = (N, None) if slots is None else (state.shape[0], _dense(slots, "slots", _I32, (N,), dev))
     if o is None:
-        o = torch.empty((N, HV, dv), dtype=torch.bfloat16, device=dev)
-    _check(o, "o", torch.bfloat16, (N, HV, dv), dev)
-    with torch.cuda.device(dev):
-        st = load_library().kda_gdn_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state), _ptr(o),
-                                                _ptr(slots), rows, float(scale), N, HK, HV, dk, dv, qs, ks, vs, gf,
-                                                _stream(dev))
-    if st != KDA_OK:
-        raise KdaError("kda_gdn_decode_step", st)
+        o = torch.empty((N, HV, dv), dtype=_BF16, device=dev)
+    _call("kda_gdn_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp,
+          _dense(state, "state", _F32, (rows, HV, dk, dv), dev), _dense(o, "o", _BF16, (N, HV, dv), dev), sp, rows,
+          scale, N, HK, HV, dk, dv, qs, ks, vs, gf)
     return o
 
 
@@ -642,10 +651,8 @@ class Packed8(NamedTuple):
 
 
 ACT8_MAX_TENSORS = 4
-
-
-def _host_array(kind, values):
-    return (kind * len(values))(*values)
+_PTRS = [ctypes.c_void_p * n for n in range(ACT8_MAX_TENSORS + 1)]
+_SIZES = [ctypes.c_int64 * n for n in range(ACT8_MAX_TENSORS + 1)]
 
 
 def act_pack8(*tensors):
@@ -653,58 +660,45 @@ def act_pack8(*tensors):
     launch (kda_act_pack8).  The last axis must be a multiple of 32; the
     tensors may be slices of wider ones as long as their rows are equally
     spaced.  One tensor gives a Packed8, several a tuple of them."""
-    import torch
-    if not 1 <= len(tensors) <= ACT8_MAX_TENSORS:
-        raise ValueError("act_pack8 takes 1 to %d tensors, got %d" % (ACT8_MAX_TENSORS, len(tensors)))
+    torch = _types()
+    n = len(tensors)
+    if not 1 <= n <= ACT8_MAX_TENSORS:
+        raise ValueError("act_pack8 takes 1 to %d tensors, got %d" % (ACT8_MAX_TENSORS, n))
     dev = _require_cuda(tensors[0])
     rows, cols, strides, out = [], [], [], []
-    for n, t in enumerate(tensors):
-        name = "tensor %d" % n
-        if t.dim() < 1 or t.shape[-1] % 32 != 0:
-            raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(t.shape)))
-        rows_of = t if t.dim() >= 3 else t.unsqueeze(-2)        # [..., heads, channels]
-        strides.append(_check_tokens(rows_of, name, rows_of.shape[:-2], *rows_of.shape[-2:], dev))
-        cols.append(rows_of.shape[-2] * rows_of.shape[-1])
-        rows.append(t.numel() // cols[-1] if cols[-1] else 0)
-        out.append(Packed8(torch.empty(t.shape, dtype=torch.float8_e4m3fn, device=dev),
-                           torch.empty(t.shape[:-1] + (t.shape[-1] // 32,), dtype=torch.uint8, device=dev)))
-    n = len(tensors)
-    with torch.cuda.device(dev):
-        st = load_library().kda_act_pack8(
-            n, _host_array(ctypes.c_void_p, [t.data_ptr() for t in tensors]),
-            _host_array(ctypes.c_void_p, [p.data.data_ptr() for p in out]),
-            _host_array(ctypes.c_void_p, [p.scales.data_ptr() for p in out]),
-            _host_array(ctypes.c_int64, rows), _host_array(ctypes.c_int64, cols), _host_array(ctypes.c_int64, strides),
-            _stream(dev))
-    if st != KDA_OK:
-        raise KdaError("kda_act_pack8", st)
+    for i, t in enumerate(tensors):
+        shape = t.shape
+        if len(shape) < 1 or shape[-1] % 32 != 0:
+            raise ValueError("tensor %d: the last axis must be a multiple of 32, got shape %s" % (i, tuple(shape)))
+        x = t if len(shape) >= 3 else t.unsqueeze(-2)            # [..., heads, channels]
+        heads, d = x.shape[-2:]
+        strides.append(_check_tokens(x, "tensor %d" % i, x.shape[:-2], heads, d, dev))
+        cols.append(heads * d)
+        rows.append(t.numel() // (heads * d) if heads * d else 0)
+        out.append(Packed8(torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
+                           torch.empty((*shape[:-1], shape[-1] // 32), dtype=torch.uint8, device=dev)))
+    _call("kda_act_pack8", dev, n, _PTRS[n](*[t.data_ptr() for t in tensors]), _PTRS[n](*[p.data.data_ptr() for p in out]),
+          _PTRS[n](*[p.scales.data_ptr() for p in out]), _SIZES[n](*rows), _SIZES[n](*cols), _SIZES[n](*strides))
     return out[0] if n == 1 else tuple(out)
 
 
-def _check_packed8(p, name, device):
-    import torch
-    if p.data.dim() < 1 or p.data.shape[-1] % 32 != 0:
-        raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(p.data.shape)))
-    _check(p.data, name + ".data", torch.float8_e4m3fn, p.data.shape, device)
-    _check(p.scales, name + ".scales", torch.uint8, p.data.shape[:-1] + (p.data.shape[-1] // 32,), device)
+def _packed8(p, name, shape, dev):
+    """Addresses of a Packed8's data and scales, checked against the tensor's shape."""
+    if len(shape) < 1 or shape[-1] % 32 != 0:
+        raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(shape)))
+    return (_dense(p.data, name + ".data", _torch.float8_e4m3fn, shape, dev),
+            _dense(p.scales, name + ".scales", _torch.uint8, (*shape[:-1], shape[-1] // 32), dev))
 
 
 def act_unpack8(packed, *, out=None):
     """The bf16 values that a Packed8 stands for, exactly (kda_act_unpack8)."""
-    import torch
+    torch = _types()
     dev = _require_cuda(packed.data)
-    _check_packed8(packed, "packed", dev)
+    shape = packed.data.shape
+    data, scales = _packed8(packed, "packed", shape, dev)
     if out is None:
-        out = torch.empty(packed.data.shape, dtype=torch.bfloat16, device=dev)
-    _check(out, "out", torch.bfloat16, packed.data.shape, dev)
-    last = packed.data.shape[-1]
-    with torch.cuda.device(dev):
-        st = load_library().kda_act_unpack8(
-            1, _host_array(ctypes.c_void_p, [packed.data.data_ptr()]),
-            _host_array(ctypes.c_void_p, [packed.scales.data_ptr()]),
-            _host_array(ctypes.c_void_p, [out.data_ptr()]),
-            _host_array(ctypes.c_int64, [packed.data.numel() // last if last else 0]),
-            _host_array(ctypes.c_int64, [last]), _stream(dev))
-    if st != KDA_OK:
-        raise KdaError("kda_act_unpack8", st)
+        out = torch.empty(shape, dtype=_BF16, device=dev)
+    last = shape[-1]
+    _call("kda_act_unpack8", dev, 1, _PTRS[1](data), _PTRS[1](scales), _PTRS[1](_dense(out, "out", _BF16, shape, dev)),
+          _SIZES[1](packed.data.numel() // last if last else 0), _SIZES[1](last))
     return out
