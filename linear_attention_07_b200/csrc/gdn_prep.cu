@@ -6,10 +6,11 @@
 // K = 128 from the TMA-staged rows.  The running sums of g are taken in 64
 // bits and kept as two fp32 numbers: a sum over 64 tokens reaches thousands
 // when tokens reset the state, and fp32 would then lose the decay between
-// neighbours.  X comes from forward substitution in fp32 (powers of A would
-// lose digits when keys repeat): the two 32 x 32 diagonal blocks side by side,
-// one column per thread with its values in registers and the rows of A as
-// broadcast 16-byte reads, then X10 = -X11 (A10 X00) the same way.
+// neighbours.  X comes from forward substitution (powers of A would lose
+// digits when keys repeat): the 16 x 16 diagonal blocks in fp32, then X10 =
+// -X11 (A10 X00) for blocks of 16 and of 32 as small tensor-core products of
+// fp32 accuracy (three tf32 products each): with fp32 FMAs those read shared
+// memory once per multiply, which bound the kernel.
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -47,6 +48,73 @@ __device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, in
         *reinterpret_cast<float4*>(hi_dst + at) = make_float4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<float4*>(lo_dst + at) = make_float4(lo[0], lo[1], lo[2], lo[3]);
     }
+}
+
+// fp32 products on the tensor cores: x = hi + lo with 11 significant bits in
+// hi, and hi hi + hi lo + lo hi.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
+{
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2])
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// (16 MT x 16 MT at m) times (16 MT x 8 at x), both of row stride LD.
+template <int MT>
+__device__ __forceinline__ void block_product(const float* m, const float* x, int lane, float (&d)[MT][4])
+{
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[i][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2 * MT; ++k) {
+        uint32_t bh[2], bl[2];
+        split_tf32(x[(8 * k + t) * LD + g], bh[0], bl[0]);
+        split_tf32(x[(8 * k + t + 4) * LD + g], bh[1], bl[1]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const float* a = m + (16 * i + g) * LD + 8 * k + t;
+            uint32_t ah[4], al[4];
+            split_tf32(a[0], ah[0], al[0]);
+            split_tf32(a[8 * LD], ah[1], al[1]);
+            split_tf32(a[4], ah[2], al[2]);
+            split_tf32(a[8 * LD + 4], ah[3], al[3]);
+            mma_tf32(d[i], al, bh);
+            mma_tf32(d[i], ah, bl);
+            mma_tf32(d[i], ah, bh);
+        }
+    }
+}
+// Columns [col, col + 8) of X10 = -X11 (A10 X00) for the blocks of 16 MT rows at `base`.
+template <int MT>
+__device__ __forceinline__ void join(const float* sA, float* sX, int base, int col, int lane)
+{
+    constexpr int S = 16 * MT;
+    const int g = lane >> 2, t = lane & 3;
+    float d[MT][4];
+    float* x10 = sX + (base + S) * LD + col;
+    auto put = [&](float sign) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float* y = x10 + (16 * i + g) * LD + 2 * t;
+            y[0] = sign * d[i][0];
+            y[1] = sign * d[i][1];
+            y[8 * LD] = sign * d[i][2];
+            y[8 * LD + 1] = sign * d[i][3];
+        }
+    };
+    block_product<MT>(sA + (base + S) * LD + base, sX + base * LD + col, lane, d);
+    put(1.f);
+    __syncwarp();
+    block_product<MT>(sX + (base + S) * LD + base + S, x10, lane, d);
+    __syncwarp();
+    put(-1.f);
 }
 }  // namespace prep
 
@@ -147,6 +215,14 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
 #pragma unroll 1
         for (int col = 0; col < C; col += 32) {
             float x[32];
+            if (col > (r | 31)) {                     // a block above the diagonal (warp-uniform): A's is never read
+                if (warp >= 2) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    store_split(rec + REC_PH, rec + REC_PL, r, col, x);
+                }
+                continue;
+            }
             tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + col, x);
             wait_ld();
 #pragma unroll
@@ -181,62 +257,40 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         fence_after_sync();
         tmem_dealloc(tm, 64);
     }
-    // X00 (warp 0) and X11 (warp 1): 32 x 32 forward substitution, one column
-    // per thread; the rows of A are broadcast reads
-    constexpr int H = C / 2;
-    if (warp < 2) {
-        const float* a = sA + (H * warp) * LD + H * warp;
-        float x[H];
+    {   // the 16 x 16 diagonal blocks, one per warp: forward substitution, one column per thread (lanes 16-31 repeat
+        // lanes 0-15), its values in registers and the rows of A as broadcast reads
+        const float* a = sA + 16 * warp * (LD + 1);
+        const int j = lane & 15;
+        float x[16];
 #pragma unroll
-        for (int r = 0; r < H; ++r) {
+        for (int r = 0; r < 16; ++r) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < r; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(a + r * LD + i);   // A is zero from the diagonal on
+                const float4 v = *reinterpret_cast<const float4*>(a + r * LD + i);
                 s[0] = fmaf(v.x, x[i], s[0]);
                 if (i + 1 < r) s[1] = fmaf(v.y, x[i + 1], s[1]);
                 if (i + 2 < r) s[2] = fmaf(v.z, x[i + 2], s[2]);
                 if (i + 3 < r) s[3] = fmaf(v.w, x[i + 3], s[3]);
             }
-            x[r] = r == lane ? 1.f : r > lane ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
+            x[r] = r == j ? 1.f : r > j ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
         }
+        if (lane < 16)
 #pragma unroll
-        for (int r = 0; r < H; ++r) sX[(H * warp + r) * LD + H * warp + lane] = x[r];
+            for (int r = 0; r < 16; ++r) sX[(16 * warp + r) * LD + 16 * warp + j] = x[r];
+        else if ((warp & 1) == 0)                     // the joined blocks of 32 have zeros above their diagonal
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sX[(16 * warp + r) * LD + 16 * warp + 16 + j] = 0.f;
     }
     __syncthreads();
-    // X10 = -X11 (A10 X00): thread = one column, 8 rows
+    // blocks next to one another: X10 = -X11 (A10 X00), of 16 and then of 32; every warp takes 8 columns, its own
+    // part of A10 X00 passing through X10's place
     {
-        float x[H], acc[8];
-        const int r0 = 8 * warp;
-        auto eight_rows = [&](const float* m) {       // acc = rows [r0, r0 + 8) of m times the column x
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < H; i += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(m + (r0 + r) * LD + i);
-                    s[0] = fmaf(v.x, x[i], s[0]);
-                    s[1] = fmaf(v.y, x[i + 1], s[1]);
-                    s[2] = fmaf(v.z, x[i + 2], s[2]);
-                    s[3] = fmaf(v.w, x[i + 3], s[3]);
-                }
-                acc[r] = (s[0] + s[1]) + (s[2] + s[3]);
-            }
-        };
-        float* y = sA;                                // over A00, which is done with
-#pragma unroll
-        for (int i = 0; i < H; ++i) x[i] = sX[i * LD + lane];
-        eight_rows(sA + H * LD);
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < 8; ++r) y[(r0 + r) * LD + lane] = acc[r];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < H; ++i) x[i] = y[i * LD + lane];
-        eight_rows(sX + H * LD + H);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) sX[(H + r0 + r) * LD + lane] = -acc[r];
+        const int base = 32 * (warp >> 1), col = base + 8 * (warp & 1);
+        join<1>(sA, sX, base, col, lane);
     }
+    __syncthreads();
+    join<2>(sA, sX, 0, 8 * warp, lane);
     __syncthreads();
     {   // T = X diag(beta) as two bf16 numbers, in the operand layout: one row and 32 columns per thread
         const int r = tid % C, col = 32 * (tid / C);
@@ -246,10 +300,13 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             const float4 v = *reinterpret_cast<const float4*>(sX + r * LD + col + i), b = *reinterpret_cast<const float4*>(sB + col + i);
             x[i] = v.x * b.x; x[i + 1] = v.y * b.y; x[i + 2] = v.z * b.z; x[i + 3] = v.w * b.w;
         }
-        if (col > r) {                                // the block above the diagonal was never written
+        const int d = r / 16 * 16 + 16;               // from here on row r was never written
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        }
+        for (int i = 0; i < 32; i += 16)
+            if (col + i >= d) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[i + e] = 0.f;
+            }
         store_split(rec + REC_TH, rec + REC_TL, r, col, x);
     }
 }
