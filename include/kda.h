@@ -350,7 +350,7 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * chunks at once, then one CTA per sequence and value head along the chunks.
  * K and Q enter the products as bf16, the state and what is computed as pairs
  * of bf16 with fp32 sums: hT is accurate to about 1e-5 of its norm.
- * Supported: d_k == d_v == 128.  Stream-ordered workspace of 33,792 bytes per
+ * Supported: d_k == d_v == 128.  Stream-ordered workspace of 66,560 bytes per
  * value head and 64-token chunk (at most tokens / 64 + N chunks);
  * KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in the prefill
  * (kda_device_status).
@@ -372,7 +372,7 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * Tokens before the first sequence and behind the last get zero gradients.  A
  * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
  * atomics: the same inputs give the same bits.  Three launches (one more with
- * cu_seqlens); stream-ordered workspace of 164,864 bytes per value head and
+ * cu_seqlens); stream-ordered workspace of 197,632 bytes per value head and
  * 64-token chunk and 768 bytes per token and value head (KDA_ERR_NO_MEMORY if
  * it cannot be had).  Supported: d_k == d_v == 128.
  *

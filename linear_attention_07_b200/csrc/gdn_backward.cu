@@ -2,8 +2,8 @@
 // the prep kernel (gdn_prep.cu).  With dO~ = scale dO, dS1 = dL/dS1 and the
 // chunk's quantities of gdn_chunk.cuh:
 //     dU  = P^T dO + eta (K dS1)
-//     dV  = T^T dU                                  (T = X diag(beta))
-//     dS0 = gam_last dS1 + K^T (-gam dV) + Q^T (gam dO~)
+//     dV  = T^T dU
+//     dS0 = gam_last dS1 - W^T dU + Q^T (gam dO~)
 // and, with E = U / beta and Z = dV / beta (A enters U through (I + A) U =
 // beta (V - gam K S0), so dA = -Z U^T):
 //     dkk_ri = -D_ri dV_r . U_i  (i < r),    dqk_ri = scale D_ri dO_r . U_i  (i <= r)
@@ -37,7 +37,6 @@ __device__ int g_back_status;
 
 namespace bk {
 
-constexpr uint32_t BOX = C * 64 * 2;
 // a state as two bf16 planes, each as the local kernel's left operand (M =
 // d_k, K = d_v in two halves, MN-major without swizzle): element (i, j) at
 // (j / 64) * 16384 + (i / 8) * 1024 + (j % 64) * 16 + (i % 8) * 2
@@ -49,20 +48,22 @@ constexpr uint32_t ST_SBO = 1024, ST_LBO = 128;
 constexpr int N_CHAIN = 16, N_OUT = 4;               // warps
 constexpr int W_MMA = N_CHAIN + N_OUT, W_LOAD = W_MMA + 1;
 constexpr int NT = 32 * (W_LOAD + 1);
-// a stage: K0 Q0 K1 Q1, V0 V1 (reverse: dO), the record
+// a stage: K0 Q0 K1 Q1, V0 V1 (reverse: dO), W, T and the gates
 constexpr int STAGES = 2;
 constexpr uint32_t S_V = 4 * BOX, S_REC = 6 * BOX;
-constexpr uint32_t STAGE = S_REC + REC_BYTES;
+constexpr uint32_t STAGE = S_REC + REC_W_BYTES;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
-constexpr uint32_t S_OUT = STAGES * STAGE;           // U or dV staging, two planes [64][128] bf16
-constexpr uint32_t SMEM = S_OUT + 2 * C * D * 2 + 1024;
+constexpr uint32_t S_P = STAGES * STAGE;             // reverse: P, one buffer
+constexpr uint32_t S_OUT = S_P + P_BYTES;            // U or dV staging [32][128] bf16
+constexpr uint32_t SMEM = S_OUT + 32 * D * 2 + 1024;
 
-enum { B_FULL = 0, B_EMPTY = STAGES, B_MX = 2 * STAGES, B_MU, B_MD0, B_MD1, B_S0, B_S1, B_R, B_U, B_DO, B_OUT, B_OUTFREE, B_DRAIN, N_BAR };
+enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MV = B_MD + 2, B_S, B_U = B_S + 2,
+       B_DO = B_U + 2, B_OFREE, B_DRAIN, N_BAR };
 
 constexpr uint32_t T_SH = 0, T_SL = 64;
-constexpr uint32_t T_X = 128;                        // (K S)^T
-constexpr uint32_t T_PO = 192;                       // forward: U^T; reverse: (P^T dO)^T
-constexpr uint32_t T_RH = 256, T_RL = 288;
+constexpr uint32_t T_U = 128;                        // forward: U^T; reverse: (K dS1)^T, then dV^T
+constexpr uint32_t T_UH = 192, T_UL = 224;           // forward: (eta U)^T; reverse: dU^T
+constexpr uint32_t T_PO = 256;                       // reverse: (P^T dO)^T
 constexpr uint32_t T_OH = 320, T_OL = 352;           // reverse: (gam dO~)^T
 constexpr uint32_t T_D = 384;
 
@@ -85,7 +86,6 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                                       uint8_t* sm, uint64_t* bars, volatile int* s_abort, uint32_t tm, int n, int hv)
 {
     using namespace tc;
-    constexpr uint32_t T_U = REV ? T_X : T_PO;       // reverse: dV^T, when K dS is done with
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = hv / (p.HV / p.HK);
     int begin, end;
@@ -97,7 +97,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     const Waits wait = {s_abort, &g_back_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
-        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
+        const int sp = warp & 3, part = warp >> 2, th = part >> 1, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         const float* init = REV ? p.dhT : p.h0;
         const float* h = init ? init + ((int64_t)n * p.HV + hv) * D * D + j : nullptr;
@@ -115,23 +115,16 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             fence_before_sync();
             arrive(b);
         };
-        auto put = [&](uint32_t hi_col, uint32_t lo_col, const float (&x)[16]) {
-            float hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
-            tmem_st8(t + hi_col + 8 * part, hi);
-            tmem_st8(t + lo_col + 8 * part, lo);
-        };
         // the state's half b: operand of the next chunk, and for the local kernel
+        uint8_t* dst0 = (REV ? p.dS1 : p.S0) + (slot0 * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF + 2 * part * ST_SBO + (j % 64) * 16;
         auto give_state = [&](int b, int c) {
             float hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) split_bf16(S[b][2 * i], S[b][2 * i + 1], hi[i], lo[i]);
             tmem_st8(t + T_SH + 32 * b + 8 * part, hi);
             tmem_st8(t + T_SL + 32 * b + 8 * part, lo);
-            give(B_S0 + b);
-            uint8_t* dst = (REV ? p.dS1 : p.S0) + ((slot0 + chunk_at(c)) * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF +
-                           (8 * b + 2 * part) * ST_SBO + (j % 64) * 16;
+            give(B_S + b);
+            uint8_t* dst = dst0 + chunk_at(c) * (int64_t)p.HV * (2 * (int64_t)PLANE) + 8 * b * ST_SBO;
             *reinterpret_cast<float4*>(dst) = make_float4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<float4*>(dst + ST_SBO) = make_float4(hi[4], hi[5], hi[6], hi[7]);
             *reinterpret_cast<float4*>(dst + PLANE) = make_float4(lo[0], lo[1], lo[2], lo[3]);
@@ -141,62 +134,50 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             give_state(0, 0);
             give_state(1, 0);
         }
-        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT) + 16 * part * D + j;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1;
-            const float4* gates = reinterpret_cast<const float4*>(sm + s * STAGE + S_REC + REC_NGAM) + 4 * part;
+            const float* gates = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM);
             wait(bar(B_FULL + s), (c >> 1) & 1);
-            const float last = -reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM)[C - 1];
-            float x[16];
-            auto scale_by = [&](int which) {         // 0: -gam, 1: eta
+            const float last = -gates[C - 1];
+            float4 eta[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = gates[16 * which + i];
-                    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
-                    const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
-                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
-                }
-            };
-            wait(bar(B_MX), c & 1);                  // K S, and in reverse P^T dO
+            for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
+            arrive(B_EMPTY + s);
+            float x[16];
+            wait(bar(B_MU + th), c & 1);             // U, or K dS1 and P^T dO
             fence_after_sync();
-            tmem_ld16(t + T_X + 16 * part, x);
+            tmem_ld16(t + T_U + 16 * part, x);
             if constexpr (REV) {
                 float y[16];
                 tmem_ld16(t + T_PO + 16 * part, y);
                 wait_ld();
-                scale_by(1);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] += y[i];
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = fma2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(eta[i].x, eta[i].y), make_float2(y[4 * i], y[4 * i + 1]));
+                    const float2 b = fma2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(eta[i].z, eta[i].w), make_float2(y[4 * i + 2], y[4 * i + 3]));
+                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+                }
             } else {
                 wait_ld();
-                scale_by(0);
-            }
-            put(T_RH, T_RL, x);
-            give(B_R);
-
-            wait(bar(B_MU), c & 1);
-            fence_after_sync();
-            tmem_ld16(t + T_U + 16 * part, x);
-            wait_ld();
-            float u[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = x[i];
-            scale_by(REV ? 0 : 1);
-            put(T_RH, T_RL, x);
-            give(B_U);
-            arrive(B_EMPTY + s);
-            if (c > 0) wait(bar(B_OUTFREE), (c - 1) & 1);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(u[i]);
-                so[i * D] = hi;
-                so[C * D + i * D] = __float2bfloat16_rn(u[i] - __bfloat162float(hi));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(eta[i].x, eta[i].y));
+                    const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(eta[i].z, eta[i].w));
+                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+                }
             }
-            arrive(B_OUT);
+            {
+                float hi[8], lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+                tmem_st8(t + T_UH + 8 * part, hi);
+                tmem_st8(t + T_UL + 8 * part, lo);
+            }
+            give(B_U + th);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                wait(bar(B_MD0 + b), c & 1);
+                wait(bar(B_MD + b), c & 1);
                 fence_after_sync();
                 tmem_ld16(t + T_D + 64 * b + 16 * part, x);
                 wait_ld();
@@ -219,13 +200,13 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        const __nv_bfloat16* so = reinterpret_cast<const __nv_bfloat16*>(sm + S_OUT);
+        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1, t0 = begin + chunk_at(c) * C, nv = min(C, end - t0);
             wait(bar(B_FULL + s), (c >> 1) & 1);
             if constexpr (REV) {                     // gam dO~ as an operand; the previous one has been read
-                if (c > 0) wait(bar(B_MD1), (c - 1) & 1);
+                if (c > 0) wait(bar(B_MD + 1), (c - 1) & 1);
                 fence_after_sync();
                 const uint8_t* box = sm + s * STAGE + S_V + (j / 64) * BOX + (j % 8) * 2;
                 const float* gq = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_GQ);
@@ -254,32 +235,58 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
-            wait(bar(B_OUT), c & 1);
-#pragma unroll 4
-            for (int e = 0; e < 2 * C * D / 8 / 128; ++e) {
-                const int i = ot + 128 * e, plane = i / (C * D / 8), r = (i / (D / 8)) % C, c8 = i % (D / 8);
-                if (r < nv)
-                    *reinterpret_cast<uint4*>((REV ? p.dv : p.u)[plane] + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
-                        *reinterpret_cast<const uint4*>(so + plane * C * D + r * D + 8 * c8);
+            if constexpr (REV) {
+                wait(bar(B_MV), c & 1);
+            } else {
+                wait(bar(B_MU), c & 1);
+                wait(bar(B_MU + 1), c & 1);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_OUTFREE));
+            fence_after_sync();
+#pragma unroll 1
+            for (int q = 0; q < 2; ++q) {
+                float x[32];
+                tmem_ld32(t + T_U + 32 * q, x);
+                wait_ld();
+                if (q == 1) {
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_OFREE));
+                }
+#pragma unroll 1
+                for (int plane = 0; plane < 2; ++plane) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
+                        so[i * D + j] = hi;
+                        x[i] -= __bfloat162float(hi);         // the second plane's
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    __nv_bfloat16* out = (REV ? p.dv : p.u)[plane];
+#pragma unroll
+                    for (int e = 0; e < 32 * D / 8 / 128; ++e) {
+                        const int i = ot + 128 * e, r = 32 * q + i / (D / 8), c8 = i % (D / 8);
+                        if (r < nv)
+                            *reinterpret_cast<uint4*>(out + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
+                                *reinterpret_cast<const uint4*>(so + (i / (D / 8)) * D + 8 * c8);
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+            }
         }
     } else if (warp == W_MMA) {
-        const uint32_t id_n64 = idesc_bf16(128, 64), id_bmn = idesc_bf16(128, 64, false, true);
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_n32 = idesc_bf16(128, 32), id_bmn = idesc_bf16(128, 64, false, true);
         const uint32_t id_v = idesc_bf16(128, 64, true, REV);
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        auto ok = [&](int b, uint32_t parity) {
+            const bool w = wait(bar(b), parity);
+            return __all_sync(0xffffffffu, w) != 0;
+        };
+        // chunk c is there: its rows behind the sequence count as zero, whatever they hold; what needs no state
+        auto begin_chunk = [&](int c) {
             const int s = c & 1;
+            if (!ok(B_FULL + s, (c >> 1) & 1)) return false;
             uint8_t* st = sm + s * STAGE;
-            const uint32_t base = smem_u32(st);
             const int nv = min(C, end - (begin + chunk_at(c) * C));
-            auto ok = [&](int b, uint32_t parity) {
-                const bool w = wait(bar(b), parity);
-                return __all_sync(0xffffffffu, w) != 0;
-            };
-            if (!ok(B_FULL + s, (c >> 1) & 1)) break;
-            if (nv < C) {      // rows behind the sequence count as zero, whatever they hold
+            if (nv < C) {
                 for (int e = lane; e < (C - nv) * 6 * 8; e += 32) {
                     const int piece = e & 7, box = (e >> 3) % 6, r = nv + (e >> 3) / 6;
                     *reinterpret_cast<uint4*>(st + box * BOX + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -287,26 +294,52 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 fence_smem_to_async();
                 __syncwarp();
             }
-            const uint64_t kq = sdesc_sw128(base);
+            const uint32_t base = smem_u32(st);
             const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
-            // T and P as right operands: rows (forward) or columns (reverse) as N
-            auto tp = [&](uint32_t off) { return REV ? sdesc(base + S_REC + off, 1024, 128) : sdesc(base + S_REC + off, 128, 1024); };
-            constexpr uint64_t tp_step = REV ? 128 : 16;
-            auto state_product = [&](uint32_t a, int box, int k0, uint32_t more) {
-                mma4_ts(tm + T_X, tm + a + 8 * k0, kq + (uint64_t)(box * (BOX >> 4)), 2, id_n64, more);
+            if constexpr (REV) {                     // (P^T dO)^T = dO^T P
+                if (!ok(B_P, c & 1)) return false;
+                const uint64_t ph = sdesc(smem_u32(sm + S_P), 1024, 128);
+                mma4_ss(tm + T_PO, vd, 128, ph, 128, id_v, 0u);
+                mma4_ss(tm + T_PO, vd, 128, ph + (uint64_t)(BOX >> 4), 128, id_v, 1u);
+            } else {                                 // U^T = V^T T^T
+                if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) return false;
+                fence_after_sync();
+                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
+                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
+            }
+            return true;
+        };
+        if (chunks > 0) begin_chunk(0);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t base = smem_u32(sm + (c & 1) * STAGE);
+            const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
+            constexpr uint64_t LO = 2 * BOX >> 4;
+            // forward: -(W S)^T; reverse: (K dS1)^T; half b of d_k, tokens from tok0 (32 or, by idesc, all 64)
+            auto s_product = [&](int b, int tok0, uint32_t id) {
+                const uint64_t h = (REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4))) + (uint64_t)(tok0 * 8);
+                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h, 2, id, REV && b == 0 ? 0u : 1u);
+                mma4_ts(tm + T_U + tok0, tm + T_SL + 32 * b, h, 2, id, 1u);
+                if (!REV) mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h + LO, 2, id, 1u);
             };
-            if (!ok(B_S0, c & 1)) break;
+            // forward: (K^T eta U)^T; reverse: -(W^T dU)^T; half b of d_k from the tokens of half k
+            auto d_product = [&](int b, int k) {
+                const uint64_t h = (REV ? wd + (uint64_t)(b * (BOX >> 4)) : kq + (uint64_t)(2 * b * (BOX >> 4))) + (uint64_t)(k * 256);
+                mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, h, 128, id_bmn, REV || k > 0 ? 1u : 0u);
+                mma2_ts(tm + T_D + 64 * b, tm + T_UL + 16 * k, h, 128, id_bmn, 1u);
+                if (REV) mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, h + LO, 128, id_bmn, 1u);
+            };
+            if (REV && c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
+            if (!ok(B_S, c & 1)) break;
             fence_after_sync();
-            state_product(T_SH, 0, 0, 0u);
-            state_product(T_SL, 0, 0, 1u);
-            if (!ok(B_S1, c & 1)) break;
+            s_product(0, 0, id_n64);
+            if (!ok(B_S + 1, c & 1)) break;
             fence_after_sync();
-            state_product(T_SH, 2, 4, 1u);
-            state_product(T_SL, 2, 4, 1u);
+            s_product(1, 0, id_n32);
+            mma_commit_w(bar(B_MU));
+            s_product(1, 32, id_n32);
+            mma_commit_w(bar(B_MU + 1));
             if constexpr (REV) {
-                mma4_ss(tm + T_PO, vd, 128, tp(REC_PH), tp_step, id_v, 0u);
-                mma4_ss(tm + T_PO, vd, 128, tp(REC_PL), tp_step, id_v, 1u);
-                mma_commit_w(bar(B_MX));
                 if (!ok(B_DO, c & 1)) break;
                 fence_after_sync();
 #pragma unroll
@@ -315,43 +348,42 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                     mma4_ts(tm + T_D + 64 * b, tm + T_OH, qd, 128, id_bmn, 0u);
                     mma4_ts(tm + T_D + 64 * b, tm + T_OL, qd, 128, id_bmn, 1u);
                 }
-            } else {
-                mma_commit_w(bar(B_MX));
-                mma4_ss(tm + T_PO, vd, 128, tp(REC_TH), tp_step, id_v, 0u);
-                mma4_ss(tm + T_PO, vd, 128, tp(REC_TL), tp_step, id_v, 1u);
             }
-            if (!ok(B_R, c & 1)) break;
-            fence_after_sync();
-            mma4_ts(tm + T_U, tm + T_RH, tp(REC_TH), tp_step, REV ? id_bmn : id_n64, REV ? 0u : 1u);
-            mma4_ts(tm + T_U, tm + T_RL, tp(REC_TH), tp_step, REV ? id_bmn : id_n64, 1u);
-            mma4_ts(tm + T_U, tm + T_RH, tp(REC_TL), tp_step, REV ? id_bmn : id_n64, 1u);
-            mma_commit_w(bar(B_MU));
             if (!ok(B_U, c & 1)) break;
             fence_after_sync();
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
-                mma4_ts(tm + T_D + 64 * b, tm + T_RH, kd, 128, id_bmn, REV ? 1u : 0u);
-                mma4_ts(tm + T_D + 64 * b, tm + T_RL, kd, 128, id_bmn, 1u);
-                mma_commit_w(bar(B_MD0 + b));
+            d_product(0, 0);
+            d_product(1, 0);
+            if (!ok(B_U + 1, c & 1)) break;
+            fence_after_sync();
+            d_product(0, 1);
+            mma_commit_w(bar(B_MD));
+            d_product(1, 1);
+            mma_commit_w(bar(B_MD + 1));
+            if constexpr (REV) {                     // dV^T = dU^T T
+                const uint64_t th = sdesc(base + S_REC + REC_TH, 1024, 128), tl = th + (uint64_t)(BOX >> 4);
+                mma4_ts(tm + T_U, tm + T_UH, th, 128, id_bmn, 0u);
+                mma4_ts(tm + T_U, tm + T_UL, th, 128, id_bmn, 1u);
+                mma4_ts(tm + T_U, tm + T_UH, tl, 128, id_bmn, 1u);
+                mma_commit_w(bar(B_MV));
             }
+            if (c + 1 < chunks && !begin_chunk(c + 1)) break;
         }
         if (chunks > 0) {                             // what was issued ends before its memory goes
             mma_commit_w(bar(B_DRAIN));
             mbar_wait(bar(B_DRAIN), 0, DRAIN_NS);
         }
     } else if (lane == 0) {
-        constexpr uint32_t bytes = REV ? 6 * BOX + REC_BYTES : 4 * BOX + REC_T_BYTES;
-        int loaded = 0;
+        constexpr uint32_t bytes = REV ? STAGE : 4 * BOX + REC_W_BYTES;
+        int loaded = 0, loaded_p = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1;
-            // the chain and output warps are done with chunk c - 2, and so are its last products
-            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1))) break;
-            if (c >= 2 && !wait(bar(B_MD1), c & 1)) break;
+            // chunk c - 2 is done with the stage: the gates' (and dO's) readers, its last product
+            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1) || !wait(bar(REV ? B_MV : B_MD + 1), c & 1))) break;
             if (*s_abort) break;
             const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
             const int y = begin + chunk_at(c) * C;
+            const uint8_t* rec = p.rec + ((slot0 + chunk_at(c)) * p.HV + hv) * REC_BYTES;
             mbar_arrive_expect_tx(full, bytes);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -359,11 +391,18 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 if (REV) tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
                 tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
             }
-            bulk_load(base + S_REC, p.rec + ((slot0 + chunk_at(c)) * p.HV + hv) * REC_BYTES, REV ? REC_BYTES : REC_T_BYTES, full);
+            bulk_load(base + S_REC, rec, REC_W_BYTES, full);
             loaded = c + 1;
+            if (REV) {                                // P's buffer has been read when chunk c - 1's first products are there
+                if (c >= 1 && !wait(bar(B_MU + 1), (c - 1) & 1)) break;
+                mbar_arrive_expect_tx(bar(B_P), P_BYTES);
+                bulk_load(smem_u32(sm + S_P), rec + REC_PH, P_BYTES, bar(B_P));
+                loaded_p = c + 1;
+            }
         }
         for (int c = max(0, loaded - STAGES); c < loaded; ++c)
             mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
+        if (loaded_p > 0) mbar_wait(bar(B_P), (loaded_p - 1) & 1, DRAIN_NS);
     }
 }
 
@@ -383,8 +422,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
             const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
-                            : b == B_S0 || b == B_S1 || b == B_R || b == B_U || b == B_OUT ? N_CHAIN
-                            : b == B_DO || b == B_OUTFREE ? N_OUT : 1;
+                            : b == B_S || b == B_S + 1 ? N_CHAIN
+                            : b == B_U || b == B_U + 1 ? N_CHAIN / 2 : b == B_DO || b == B_OFREE ? N_OUT : 1;
             mbar_init(smem_u32(&bars[b]), count);
         }
         fence_mbar_init();
@@ -933,7 +972,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && N > 0)
-        e = prep_launch(maps.q, maps.k, g, beta, a.seqs, const_cast<uint8_t*>(a.rec), scale, HK, HV, gate_f32, 9.313225746154785e-10f, stream);
+        e = prep_launch(maps.q, maps.k, g, beta, a.seqs, const_cast<uint8_t*>(a.rec), scale, HK, HV, gate_f32, true, stream);
     if (e == cudaSuccess && N > 0) {
         chains_kernel<<<(unsigned)(2 * (int64_t)N * HV), NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);
         e = cudaGetLastError();

@@ -4,14 +4,15 @@
 // A chunk is C = 64 tokens.  With G_r the running sum of g inside the chunk,
 // gam = exp(G), eta_r = exp(G_last - G_r), D_ri = exp(G_r - G_i):
 //     A  = strict_lower(beta_r D_ri k_r . k_i),   X = (I + A)^-1
-//     T  = X diag(beta),   U = T (V - gam K S0)
+//     T  = X diag(beta),   W = T diag(gam) K,   U = T V - W S0
 //     O  = scale gam Q S0 + P U,  P = scale lower(D_ri q_r . k_i)
 //     S1 = gam_last S0 + K^T (eta U)
-// One decay per head is one factor per token pair or token: K and Q enter
+// One decay per head is one factor per token pair or token: K, Q and V enter
 // every product as they are in memory, exact in bf16.  Everything else (the
-// state, T, gam K S0, U) is fp32 and enters as the sum of two bf16 numbers (16
+// state, T, W, P, U) is fp32 and enters as the sum of two bf16 numbers (16
 // significant bits; the products hi hi, hi lo and lo hi are kept), so the
-// state carries about fp32 accuracy through bf16 tensor-core products.
+// state carries about fp32 accuracy through bf16 tensor-core products (and so
+// do the outputs, whose sums over U cancel where keys repeat).
 //
 // Sequences are cut into chunks at their own begins.  Chunk c of sequence n,
 // which begins at token a, has the workspace slot a / 64 + n + c: a sequence
@@ -29,20 +30,30 @@ namespace gdn {
 constexpr int C = 64;
 constexpr int D = 128;
 
-// What the prep kernel leaves per (slot, value head), in bytes.  T and P are
-// stored as the no-swizzle operand layout wants them: element (r, i) at
-// (r / 8) * 1024 + (i / 8) * 128 + (r % 8) * 16 + (i % 8) * 2.
-constexpr uint32_t REC_TH = 0;                       // T = X diag(beta), upper 8 bits   [64 x 64] bf16
-constexpr uint32_t REC_TL = REC_TH + C * C * 2;      // T, the rest
-constexpr uint32_t REC_NGAM = REC_TL + C * C * 2;    // -gam_r   [64] fp32
+// What the prep kernel leaves per (slot, value head), in bytes.  W is stored
+// as a TMA box with the 128-byte swizzle would be (two boxes of 64 channels),
+// negated; T and P as the no-swizzle operand layout wants them: element (r, i)
+// at (r / 8) * 1024 + (i / 8) * 128 + (r % 8) * 16 + (i % 8) * 2.
+constexpr uint32_t BOX = C * 64 * 2;
+constexpr uint32_t REC_WH = 0;                       // -W, upper 8 bits   [2][64 x 64] bf16
+constexpr uint32_t REC_WL = REC_WH + 2 * BOX;        // and the rest
+constexpr uint32_t REC_TH = REC_WL + 2 * BOX;        // T, likewise   [64 x 64]
+constexpr uint32_t REC_TL = REC_TH + BOX;
+constexpr uint32_t REC_NGAM = REC_TL + BOX;          // -gam_r   [64] fp32
 constexpr uint32_t REC_ETA = REC_NGAM + C * 4;       // eta_r
 constexpr uint32_t REC_GQ = REC_ETA + C * 4;         // scale gam_r
 constexpr uint32_t REC_BETA = REC_GQ + C * 4;        // beta_r (0 behind the sequence)
 constexpr uint32_t REC_PH = REC_BETA + C * 4;        // P, likewise
-constexpr uint32_t REC_PL = REC_PH + C * C * 2;
-constexpr uint32_t REC_BYTES = REC_PL + C * C * 2;
-constexpr uint32_t REC_T_BYTES = REC_PH;             // T and the gates; P comes later in a chunk
-static_assert(REC_BYTES == 33792 && REC_T_BYTES % 1024 == 0, "record");
+constexpr uint32_t REC_PL = REC_PH + BOX;
+constexpr uint32_t REC_BYTES = REC_PL + BOX;
+constexpr uint32_t REC_W_BYTES = REC_PH;             // W, T and the gates; P is needed at another time
+constexpr uint32_t P_BYTES = REC_BYTES - REC_PH;
+static_assert(REC_BYTES == 66560 && REC_W_BYTES % 1024 == 0, "record");
+
+// The forward multiplies P with eta U, which it has as an operand anyway, so
+// there P's columns are divided by eta.  eta is held above 2^-100 for that: a
+// token whose write has decayed further leaves 2^-100 of it in the state.
+constexpr float ETA_FLOOR_LOG2 = -100.f;
 
 __host__ __device__ inline int64_t slot_count(const Seqs& s) { return s.tokens / C + s.n_seq; }
 
@@ -86,22 +97,24 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Four K steps of one product by a converged warp (one elected lane issues;
-// inlined, so that the descriptors stay warp-uniform).  A from tensor memory (8
-// columns per step) or shared memory, B from shared memory; the steps are in
+// K steps of one product by a converged warp (one elected lane issues;
+// inlined, so that the descriptors stay warp-uniform).  A from tensor memory
+// (8 columns per step) or shared memory, B from shared memory; the steps are in
 // descriptor units (16 bytes).
-__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
         "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
-        "add.u64 b1, %2, %3;\n\tadd.u64 b2, b1, %3;\n\tadd.u64 b3, b2, %3;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, %3;\n\t"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, q;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n\t}\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n\t}\n"
         :: "r"(d), "r"(a), "l"(b), "l"(b_step), "r"(idesc), "r"(more) : "memory");
+}
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
+{
+    mma2_ts(d, a, b, b_step, idesc, more);
+    mma2_ts(d, a + 16, b + 2 * b_step, b_step, idesc, 1u);
 }
 __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t a_step, uint64_t b, uint64_t b_step, uint32_t idesc,
                                      uint32_t more)
@@ -191,12 +204,18 @@ struct Waits {
 };
 constexpr uint64_t DRAIN_NS = 20000000ull;           // after an expired wait: 20 ms for what is in flight
 
+// Bulk store of shared memory (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
 // Host: bf16 [tokens][cols] with a row stride in elements, boxes of 64 rows by
 // 64 columns with the 128-byte swizzle.
 bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride);
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, float beta_floor, cudaStream_t stream);
+                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream);
 
 }  // namespace gdn
 }  // namespace kda

@@ -1,35 +1,32 @@
 // Gated delta rule, one decay per head: chunked forward, after the prep kernel
 // (gdn_prep.cu).  One CTA per sequence and value head carries the state
 // through the chunks; per chunk (gdn_chunk.cuh)
-//     X_K = K S,  X_Q = Q S,  U = T V - T (gam X_K),
-//     O = scale gam X_Q + P U,  S <- gam_last S + K^T (eta U).
+//     U = T V - W S,   O = scale gam Q S + P U,   S <- gam_last S + K^T (eta U).
 // Every product is computed transposed, with d_v as the M = 128 of the MMA:
-//     X^T = S^T K^T,  U^T = V^T T^T - (gam X)^T T^T,  O^T = U^T P^T,
+//     U^T = V^T T^T - S^T W^T,  X_Q^T = S^T Q^T,  O^T = (eta U)^T (P / eta)^T,
 //     S^T += (eta U)^T K,
-// so the left operands that are computed here (S, gam X_K, U: fp32 values as
-// two bf16) go from registers to tensor memory, everything that is in memory
-// (K, Q, V, T, P: bf16) is read by the MMA as TMA left it, and thread j owns
-// column j of S, X, U and O throughout: nothing the chain computes passes
-// through shared memory.  Sums are fp32; the state is updated in fp32
-// registers (never accumulated in tensor memory, whose additions need not
-// round to nearest).
+// so the left operands that are computed here (S, eta U: fp32 values as two
+// bf16) go from registers to tensor memory, everything that is in memory (K,
+// Q, V, T, W, P: bf16) is read by the MMA as TMA left it, and thread j owns
+// column j of S, U and O throughout: nothing the chain computes passes through
+// shared memory.  Sums are fp32; the state is updated in fp32 registers (never
+// accumulated in tensor memory, whose additions need not round to nearest).
 //
 // Roles (22 warps):
 //   warps 0-15  chain: thread (j, part) holds S[dk][j] for 16 + 16 values of
-//               dk and takes 16 of the chunk's tokens; gam X_K, U, the state
+//               dk and takes 16 of the chunk's tokens; eta U, the state
 //               update, and their split into bf16 pairs
 //   warps 16-19 output: thread j takes O^T's row j, 64 tokens, through
-//               shared memory (where V was) to 16-byte stores, off the
-//               chain's path
+//               shared memory to 16-byte stores, off the chain's path
 //   warp 20     issues every MMA
-//   warp 21     loads: K, Q, V (128-byte swizzle), T and the gates into three
+//   warp 21     loads: K, Q, V (128-byte swizzle), W, T and the gates into two
 //               stages, P into one buffer
-// Per chunk the MMAs take 2,900 cycles (84 of 32 to 48 cycles) and the chain
-// waits for three of them in turn (X_K, U, K^T U), with the conversions
-// between; what the chain does not wait for (T V, X_Q, O) is issued behind
-// those, to run while it converts.  The state is updated in two halves of
-// d_k: while the second half of K^T U is computed the first half is updated
-// and split, and X_K starts on it.
+// The chain waits for two products in turn (W S, K^T U) and converts between
+// them; splitting fp32 values into bf16 pairs is most of what the SM issues.
+// What the chain does not wait for (T V, X_Q, O) is issued where the tensor
+// cores would be idle.  The tokens go in two halves of 32 and the state in two
+// halves of d_k, one behind the other, so that a product runs on one half
+// while the other is converted.
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -43,28 +40,26 @@ constexpr int N_CHAIN = 16, N_OUT = 4;               // warps
 constexpr int W_MMA = N_CHAIN + N_OUT, W_LOAD = W_MMA + 1;
 constexpr int NT = 32 * (W_LOAD + 1);
 
-// a stage: K0 Q0 K1 Q1 V0 V1 (boxes of 64 tokens x 64 channels), T and gates
-constexpr int STAGES = 3;
-constexpr uint32_t BOX = C * 64 * 2;
+// a stage: K0 Q0 K1 Q1 V0 V1 (boxes of 64 tokens x 64 channels), W, T and gates
+constexpr int STAGES = 2;
 constexpr uint32_t S_V = 4 * BOX;
 constexpr uint32_t S_REC = 6 * BOX;
-constexpr uint32_t STAGE = S_REC + REC_T_BYTES;
+constexpr uint32_t STAGE = S_REC + REC_W_BYTES;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 constexpr uint32_t S_P = STAGES * STAGE;             // P, one buffer
-constexpr uint32_t P_BYTES = REC_BYTES - REC_PH;
-constexpr uint32_t SMEM = S_P + P_BYTES + 1024;
+constexpr uint32_t S_OUT = S_P + P_BYTES;            // o staging [32][128] bf16
+constexpr uint32_t SMEM = S_OUT + 32 * D * 2 + 1024;
 
-// barriers
-enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MX, B_MU, B_MD0, B_MD1, B_MO, B_S0, B_S1, B_R, B_U, B_UO, B_OFREE, B_DRAIN, N_BAR };
+// barriers (a pair where the work goes in halves)
+enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MO = B_MD + 2,
+       B_S, B_U = B_S + 2, B_OFREE = B_U + 2, B_DRAIN, N_BAR };
 
 // tensor memory columns
 constexpr uint32_t T_SH = 0, T_SL = 64;              // S^T, upper and lower half: two d_k per column
-constexpr uint32_t T_XK = 128, T_U = 192;            // X_K^T, U^T
-constexpr uint32_t T_D = 128;                        // (K^T U)^T, when X_K and U are done with
-constexpr uint32_t T_XQ = 256;
-constexpr uint32_t T_RH = 320, T_RL = 352;           // -(gam X_K)^T, then (eta U)^T
-constexpr uint32_t T_UH = 384, T_UL = 416;           // U^T, for O
-constexpr uint32_t T_O = 448;
+constexpr uint32_t T_U = 128;                        // U^T
+constexpr uint32_t T_UH = 192, T_UL = 224;           // (eta U)^T
+constexpr uint32_t T_XQ = 256, T_O = 320;
+constexpr uint32_t T_D = 384;                        // (K^T eta U)^T
 
 struct Args {
     Seqs seqs;
@@ -103,7 +98,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
             const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
-                            : b == B_S0 || b == B_S1 || b == B_R || b == B_U || b == B_UO ? N_CHAIN : b == B_OFREE ? N_OUT : 1;
+                            : b >= B_S && b < B_S + 2 ? N_CHAIN
+                            : b >= B_U && b < B_U + 2 ? N_CHAIN / 2 : b == B_OFREE ? N_OUT : 1;
             mbar_init(bar(b), count);
         }
         fence_mbar_init();
@@ -120,7 +116,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const Waits wait = {&s_abort, &g_fwd_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
-        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
+        const int sp = warp & 3, part = warp >> 2, th = part >> 1, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
         const float* h = p.h0 && row >= 0 ? p.h0 + ((int64_t)row * p.HV + hv) * D * D + j : nullptr;
@@ -148,49 +144,34 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         if (chunks > 0)
             for (int b = 0; b < 2; ++b) {
                 put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
-                give(B_S0 + b);
+                give(B_S + b);
             }
-        int s = 0, ph = 0;                           // stage and its phase
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const float4* gates = reinterpret_cast<const float4*>(sm + s * STAGE + S_REC + REC_NGAM) + 4 * part;
-            float x[16];
-            wait(bar(B_FULL + s), ph);
-            const float last = -reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM)[C - 1];
-            // x times one gate per token (NGAM or ETA: 16 float4 apart)
-            auto scale_by = [&](int which) {
+            const int s = c & 1;
+            const float* gates = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM);
+            wait(bar(B_FULL + s), (c >> 1) & 1);
+            const float last = -gates[C - 1];
+            float4 eta[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float4 f = gates[16 * which + i];
-                    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(f.x, f.y));
-                    const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(f.z, f.w));
-                    x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
-                }
-            };
-            wait(bar(B_MX), c & 1);
-            fence_after_sync();
-            tmem_ld16(t + T_XK + 16 * part, x);
-            wait_ld();
-            scale_by(0);
-            put(T_RH, T_RL, x);
-            give(B_R);
-
-            wait(bar(B_MU), c & 1);
+            for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
+            arrive(B_EMPTY + s);
+            float x[16];
+            wait(bar(B_MU + th), c & 1);
             fence_after_sync();
             tmem_ld16(t + T_U + 16 * part, x);
             wait_ld();
-            float u[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) u[i] = x[i];
-            scale_by(1);
-            put(T_RH, T_RL, x);
-            give(B_U);
-            arrive(B_EMPTY + s);
-            put(T_UH, T_UL, u);                      // while K^T U is computed
-            give(B_UO);
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), make_float2(eta[i].x, eta[i].y));
+                const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(eta[i].z, eta[i].w));
+                x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+            }
+            put(T_UH, T_UL, x);
+            give(B_U + th);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                wait(bar(B_MD0 + b), c & 1);
+                wait(bar(B_MD + b), c & 1);
                 fence_after_sync();
                 tmem_ld16(t + T_D + 64 * b + 16 * part, x);
                 wait_ld();
@@ -202,10 +183,9 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
                 if (c + 1 < chunks) {
                     put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
-                    give(B_S0 + b);
+                    give(B_S + b);
                 }
             }
-            if (++s == STAGES) s = 0, ph ^= 1;
         }
         if (p.hT && row >= 0) {
             float* hT = p.hT + ((int64_t)row * p.HV + hv) * D * D + j;
@@ -217,13 +197,12 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        int s = 0, ph = 0;
+        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1, t0 = begin + c * C, nv = min(C, end - t0);
             const float2* gq = reinterpret_cast<const float2*>(sm + s * STAGE + S_REC + REC_GQ);
-            __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + s * STAGE + S_V);    // V's products are done
-            const int t0 = begin + c * C, nv = min(C, end - t0);
-            wait(bar(B_FULL + s), ph);
+            wait(bar(B_FULL + s), (c >> 1) & 1);
             wait(bar(B_MO), c & 1);
             fence_after_sync();
 #pragma unroll 1
@@ -241,37 +220,38 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 for (int i = 0; i < 32; i += 2) {
                     const float2 v = fma2(gq[16 * q + i / 2], make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
-                    so[(32 * q + i) * D + j] = b2.x;
-                    so[(32 * q + i + 1) * D + j] = b2.y;
+                    so[i * D + j] = b2.x;
+                    so[(i + 1) * D + j] = b2.y;
                 }
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (q == 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-            for (int e = 0; e < C * D / 8 / 128; ++e) {
-                const int i = ot + 128 * e, r = i / (D / 8), c8 = i % (D / 8);
-                if (r < nv)
-                    *reinterpret_cast<uint4*>(p.o + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
-                        *reinterpret_cast<const uint4*>(so + r * D + 8 * c8);
+                for (int e = 0; e < 32 * D / 8 / 128; ++e) {
+                    const int i = ot + 128 * e, r = 32 * q + i / (D / 8), c8 = i % (D / 8);
+                    if (r < nv)
+                        *reinterpret_cast<uint4*>(p.o + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
+                            *reinterpret_cast<const uint4*>(so + (i / (D / 8)) * D + 8 * c8);
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            fence_smem_to_async();                   // the next load of this stage is the async proxy's write
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
-            if (++s == STAGES) s = 0, ph ^= 1;
         }
     } else if (warp == W_MMA) {
-        const uint32_t id_n64 = idesc_bf16(128, 64), id_d = idesc_bf16(128, 64, false, true), id_v = idesc_bf16(128, 64, true);
-        int s = 0, ph = 0;
-#pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_n32 = idesc_bf16(128, 32), id_d = idesc_bf16(128, 64, false, true);
+        const uint32_t id_v = idesc_bf16(128, 64, true);
+        auto ok = [&](int b, uint32_t parity) {       // every lane sees the same outcome
+            const bool w = wait(bar(b), parity);
+            return __all_sync(0xffffffffu, w) != 0;
+        };
+        // chunk c is there: its rows behind the sequence count as zero, whatever they hold; U^T = V^T T^T
+        auto begin_chunk = [&](int c) {
+            const int s = c & 1;
+            if (!ok(B_FULL + s, (c >> 1) & 1)) return false;
             uint8_t* st = sm + s * STAGE;
-            const uint32_t base = smem_u32(st);
             const int nv = min(C, end - (begin + c * C));
-            auto ok = [&](int b, uint32_t parity) {   // every lane sees the same outcome
-                const bool w = wait(bar(b), parity);
-                return __all_sync(0xffffffffu, w) != 0;
-            };
-            if (!ok(B_FULL + s, ph)) break;
-            if (nv < C) {      // rows behind the sequence count as zero, whatever they hold
+            if (nv < C) {
                 for (int e = lane; e < (C - nv) * 6 * 8; e += 32) {
                     const int piece = e & 7, box = (e >> 3) % 6, r = nv + (e >> 3) / 6;
                     *reinterpret_cast<uint4*>(st + box * BOX + r * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -279,96 +259,104 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 fence_smem_to_async();
                 __syncwarp();
             }
-            // (K S)^T or (Q S)^T: d_k steps [k0, k0 + 4), the box of K or Q that holds them
-            const uint64_t kq = sdesc_sw128(base);
-            auto state_product = [&](uint32_t d, uint32_t a, int box, int k0, uint32_t more) {
-                mma4_ts(tm + d, tm + a + 8 * k0, kq + (uint64_t)(box * (BOX >> 4)), 2, id_n64, more);
+            const uint32_t base = smem_u32(st);
+            const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
+            mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
+            mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
+            return true;
+        };
+        if (chunks > 0) begin_chunk(0);
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const uint32_t base = smem_u32(sm + (c & 1) * STAGE);
+            const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
+            // -(W S)^T over half b of d_k, tokens from tok0 (32 or, by idesc, all 64)
+            auto w_product = [&](int b, int tok0, uint32_t id) {
+                const uint64_t h = wd + (uint64_t)(b * (BOX >> 4) + tok0 * 8), l = h + (uint64_t)(2 * BOX >> 4);
+                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h, 2, id, 1u);
+                mma4_ts(tm + T_U + tok0, tm + T_SL + 32 * b, h, 2, id, 1u);
+                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, l, 2, id, 1u);
             };
-            // (x)^T T^T or U^T P^T over the 64 tokens
-            auto token_product = [&](uint32_t d, uint32_t a, uint32_t b, uint32_t more) {
-                mma4_ts(tm + d, tm + a, sdesc(b, 128, 1024), 16, id_n64, more);
+            // (K^T eta U)^T, half b of d_k from the tokens of half k
+            auto d_product = [&](int b, int k) {
+                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4) + k * 256);
+                mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, kd, 128, id_d, k > 0 ? 1u : 0u);
+                mma2_ts(tm + T_D + 64 * b, tm + T_UL + 16 * k, kd, 128, id_d, 1u);
             };
-            if (!ok(B_S0, c & 1)) break;
+            if (!ok(B_S, c & 1)) break;
             fence_after_sync();
-            state_product(T_XK, T_SH, 0, 0, 0u);
-            state_product(T_XK, T_SL, 0, 0, 1u);
-            if (!ok(B_S1, c & 1)) break;
+            w_product(0, 0, id_n64);
+            if (!ok(B_S + 1, c & 1)) break;
             fence_after_sync();
-            state_product(T_XK, T_SH, 2, 4, 1u);
-            state_product(T_XK, T_SL, 2, 4, 1u);
-            mma_commit_w(bar(B_MX));
-            {   // U^T = V^T T^T, while the chain takes X_K
-                const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
-                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
-                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
-            }
-            if (!ok(B_R, c & 1)) break;
-            fence_after_sync();
-            token_product(T_U, T_RH, base + S_REC + REC_TH, 1u);
-            token_product(T_U, T_RL, base + S_REC + REC_TH, 1u);
-            token_product(T_U, T_RH, base + S_REC + REC_TL, 1u);
+            w_product(1, 0, id_n32);
             mma_commit_w(bar(B_MU));
+            w_product(1, 32, id_n32);
+            mma_commit_w(bar(B_MU + 1));
             if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
             fence_after_sync();
-            state_product(T_XQ, T_SH, 1, 0, 0u);      // while the chain splits U
-            state_product(T_XQ, T_SH, 3, 4, 1u);
-            state_product(T_XQ, T_SL, 1, 0, 1u);
-            state_product(T_XQ, T_SL, 3, 4, 1u);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {             // (Q S)^T, before a new state replaces the old one
+                const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
+                mma4_ts(tm + T_XQ, tm + T_SH + 32 * b, qd, 2, id_n64, b > 0 ? 1u : 0u);
+                mma4_ts(tm + T_XQ, tm + T_SL + 32 * b, qd, 2, id_n64, 1u);
+            }
             if (!ok(B_U, c & 1)) break;
             fence_after_sync();
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {             // (K^T U)^T, 64 values of d_k each
-                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
-                mma4_ts(tm + T_D + 64 * b, tm + T_RH, kd, 128, id_d, 0u);
-                mma4_ts(tm + T_D + 64 * b, tm + T_RL, kd, 128, id_d, 1u);
-                mma_commit_w(bar(B_MD0 + b));
-            }
-            if (!ok(B_P, c & 1) || !ok(B_UO, c & 1)) break;
+            d_product(0, 0);
+            d_product(1, 0);
+            if (!ok(B_U + 1, c & 1)) break;
             fence_after_sync();
-            token_product(T_O, T_UH, smem_u32(sm + S_P), 0u);     // while it updates the state
-            token_product(T_O, T_UL, smem_u32(sm + S_P), 1u);
-            token_product(T_O, T_UH, smem_u32(sm + S_P) + C * C * 2, 1u);
+            d_product(0, 1);
+            mma_commit_w(bar(B_MD));
+            d_product(1, 1);
+            mma_commit_w(bar(B_MD + 1));
+            if (!ok(B_P, c & 1)) break;
+            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
+            mma4_ts(tm + T_O, tm + T_UH, ph, 16, id_n64, 0u);
+            mma4_ts(tm + T_O, tm + T_UL, ph, 16, id_n64, 1u);
+            mma4_ts(tm + T_O, tm + T_UH, pl, 16, id_n64, 1u);
             mma_commit_w(bar(B_MO));
-            if (++s == STAGES) s = 0, ph ^= 1;
+            if (c + 1 < chunks && !begin_chunk(c + 1)) break;
         }
         if (chunks > 0) {                             // what was issued ends before its memory goes
             mma_commit_w(bar(B_DRAIN));
             mbar_wait(bar(B_DRAIN), 0, DRAIN_NS);
         }
     } else if (lane == 0) {
-        constexpr uint32_t bytes = 6 * BOX + REC_T_BYTES;
         const uint8_t* rec = p.rec + (slot0 * p.HV + hv) * REC_BYTES;
-        int s = 0, ph = 0, loaded = 0, loaded_p = 0;
+        int loaded = 0, loaded_p = 0;
 #pragma unroll 1
-        for (int c = 0; c < chunks + 1; ++c) {
-            // the stage of chunk c is free once chunk c - STAGES is done with it, P's buffer after each chunk
-            if (c < chunks) {
-                if (c >= STAGES && !wait(bar(B_EMPTY + s), ph ^ 1)) break;
-                if (*(volatile int*)&s_abort) break;
-                const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
-                const int y = begin + c * C;
-                mbar_arrive_expect_tx(full, bytes);
+        for (int c = 0; c < chunks; ++c) {
+            const int s = c & 1;
+            // the stage of chunk c is free once chunk c - 2 is done with it: its products (O's is the last), the
+            // gates' readers; P's buffer once the products of chunk c - 1 are
+            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1) || !wait(bar(B_MO), c & 1))) break;
+            if (*(volatile int*)&s_abort) break;
+            const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
+            const int y = begin + c * C;
+            mbar_arrive_expect_tx(full, STAGE);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
-                    tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
-                    tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
-                }
-                bulk_load(base + S_REC, rec + (int64_t)c * p.HV * REC_BYTES, REC_T_BYTES, full);
-                loaded = c + 1;
-                if (++s == STAGES) s = 0, ph ^= 1;
+            for (int b = 0; b < 2; ++b) {
+                tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
+                tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
+                tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
             }
-            // P one chunk behind the stages: its buffer is read until the previous chunk's O is complete
-            if (c >= 1) {
-                if (c >= 2 && !wait(bar(B_MO), c & 1)) break;
-                mbar_arrive_expect_tx(bar(B_P), P_BYTES);
-                bulk_load(smem_u32(sm + S_P), rec + (int64_t)(c - 1) * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
-                loaded_p = c;
-            }
+            bulk_load(base + S_REC, rec + (int64_t)c * p.HV * REC_BYTES, REC_W_BYTES, full);
+            loaded = c + 1;
+            if (c == 1) continue;                     // its P follows when the first chunk is done
+            const int cp = c == 0 ? 0 : c - 1;        // chunk c - 2's products are done: P of chunk c - 1
+            mbar_arrive_expect_tx(bar(B_P), P_BYTES);
+            bulk_load(smem_u32(sm + S_P), rec + (int64_t)cp * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
+            loaded_p = cp + 1;
+        }
+        if (loaded == chunks && chunks > 1 && wait(bar(B_MO), chunks & 1)) {     // the last chunk's P, after chunk - 2
+            mbar_arrive_expect_tx(bar(B_P), P_BYTES);
+            bulk_load(smem_u32(sm + S_P), rec + (int64_t)(chunks - 1) * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
+            loaded_p = chunks;
         }
         // everything loaded has landed before the end
         for (int c = max(0, loaded - STAGES); c < loaded; ++c)
-            mbar_wait(bar(B_FULL + c % STAGES), (c / STAGES) & 1, DRAIN_NS);
+            mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
         if (loaded_p > 0) mbar_wait(bar(B_P), (loaded_p - 1) & 1, DRAIN_NS);
     }
     fence_before_sync();
@@ -425,7 +413,7 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         keep_pool_memory();
         e = cudaMallocAsync(reinterpret_cast<void**>(&rec), (size_t)slot_count(a.seqs) * HV * REC_BYTES, stream);
         if (e != cudaSuccess) return e;
-        e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, 0.f, stream);
+        e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, false, stream);
     }
     a.rec = rec;
     if (e == cudaSuccess) {

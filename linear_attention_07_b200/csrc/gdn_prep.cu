@@ -1,6 +1,6 @@
 // Gated delta rule, one decay per head: the part of a chunk that needs no
 // state, for every chunk at once (one CTA per value head and chunk slot):
-// T = (I + A)^-1 diag(beta), P and the gate factors (gdn_chunk.cuh).
+// T = (I + A)^-1 diag(beta), W, P and the gate factors (gdn_chunk.cuh).
 //
 // K K^T and Q K^T are one tensor-core product of M = 128 ([K; Q]), N = 64,
 // K = 128 from the TMA-staged rows.  The running sums of g are taken in 64
@@ -21,14 +21,14 @@ __device__ int g_prep_status;
 namespace prep {
 constexpr int NT = 128;
 constexpr int LD = C + 4;                            // rows stay 16-byte aligned
-// K and Q rows (two boxes of 64 channels each: K0 Q0 K1 Q1), then A and X in
-// their place
-constexpr uint32_t KQ_BYTES = 2 * C * D * 2;
-constexpr uint32_t A_OFF = 0;
+// K and Q rows (boxes of 64 channels: K0 K1 Q0 Q1); A where Q was, and X; then
+// -T diag(gam) as two planes where A was; at the end W's two planes over K and
+// that
+constexpr uint32_t KQ_BYTES = 4 * BOX;
+constexpr uint32_t A_OFF = 2 * BOX;
 constexpr uint32_t X_OFF = A_OFF + C * LD * 4;
-constexpr uint32_t BODY = X_OFF + C * LD * 4;
-static_assert(BODY >= KQ_BYTES, "one body for both");
-constexpr uint32_t SMEM = BODY + 1024;               // room to align the tiles to 1024 bytes
+constexpr uint32_t SMEM = X_OFF + C * LD * 4 + 1024; // room to align the tiles to 1024 bytes
+static_assert(C * LD * 4 >= 2 * BOX, "T in the place of A");
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -118,10 +118,10 @@ __device__ __forceinline__ void join(const float* sA, float* sX, int base, int c
 }
 }  // namespace prep
 
-__global__ void __launch_bounds__(prep::NT, 6)
+__global__ void __launch_bounds__(prep::NT, 4)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, uint8_t* __restrict__ rec_all, float scale, int HK, int HV,
-            bool gate_f32, float beta_floor, uint64_t wait_ns)
+            bool gate_f32, bool backward, uint64_t wait_ns)
 {
     using namespace prep;
     using namespace tc;
@@ -129,6 +129,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     __shared__ __align__(8) uint64_t bars[2];
     // the running sum of g in units of log 2, as two fp32 numbers
     __shared__ __align__(16) float sGh[C], sGl[C];
+    __shared__ __align__(16) float sCh[C], sCl[C];    // what P's columns are measured from, likewise
+    __shared__ __align__(16) float sNG[C];            // -gam
     __shared__ __align__(16) float sB[C];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
@@ -149,12 +151,12 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         s_abort = 0;
         mbar_arrive_expect_tx(full, KQ_BYTES);
         for (int b = 0; b < 2; ++b) {
-            tma_load_2d(tile + b * 16384, &mk, hk * D + 64 * b, t0, full);
-            tma_load_2d(tile + b * 16384 + 8192, &mq, hk * D + 64 * b, t0, full);
+            tma_load_2d(tile + b * BOX, &mk, hk * D + 64 * b, t0, full);
+            tma_load_2d(tile + (2 + b) * BOX, &mq, hk * D + 64 * b, t0, full);
         }
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), 64);
+        tmem_alloc(smem_u32(&s_tmem), 128);
         tmem_relinquish();
     }
     if (warp == 2) {                                  // running sum of g in 64 bits, two tokens per lane
@@ -164,7 +166,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             const int64_t at = (int64_t)(t0 + r) * HV + hv;
             x[i] = r < nv ? (double)cut_decay(gate(g, at, gate_f32)) : 0.0;
             const float b = r < nv ? gate(beta, at, gate_f32) : 0.f;
-            sB[r] = r < nv && fabsf(b) < beta_floor ? copysignf(beta_floor, b) : b;
+            // the backward divides by beta: not below 2^-30
+            sB[r] = backward && r < nv && fabsf(b) < 0x1p-30f ? copysignf(0x1p-30f, b) : b;
         }
         double sum = x[0] + x[1];
 #pragma unroll
@@ -174,8 +177,13 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         }
         for (int i = 0; i < 2; ++i) {
             const double G = (i == 0 ? sum - x[1] : sum) * 1.4426950408889634;
+            const double last = __shfl_sync(0xffffffffu, sum, 31) * 1.4426950408889634;
+            // P / eta: exp(G_r - G_i) / exp(G_last - G_i), the latter not below its floor
+            const double c = backward ? G : last - G > (double)ETA_FLOOR_LOG2 ? last : G + (double)ETA_FLOOR_LOG2;
             sGh[2 * lane + i] = (float)G;
             sGl[2 * lane + i] = (float)(G - (double)(float)G);
+            sCh[2 * lane + i] = (float)c;
+            sCl[2 * lane + i] = (float)(c - (double)(float)c);
         }
     }
     fence_before_sync();
@@ -183,6 +191,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     fence_after_sync();
     const uint32_t tm = s_tmem;
     const Waits wait = {&s_abort, &g_prep_status, wait_ns};
+    bool issued = false;
     if (warp == 0) {
         const bool here = wait(full, 0);
         if (!here) mbar_wait(full, 0, DRAIN_NS);      // the loads land before their space is used again
@@ -195,13 +204,17 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             __syncwarp();
         }
         if (__all_sync(0xffffffffu, here)) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                const uint64_t d = sdesc_sw128(tile + (ks / 4) * 16384) + (uint64_t)(2 * (ks % 4));
-                mma_f16_ss_w(tm, d, d, idesc_bf16(128, C), ks > 0 ? 1u : 0u);
-            }
+            // K K^T into lanes 0-63 of one block of columns, Q K^T into lanes 64-127 of the other: the other 64 rows
+            // of either left operand are the neighbouring boxes, their results are not read
+            constexpr uint32_t id = idesc_bf16(128, C);
+            const uint64_t k0 = sdesc_sw128(tile), k1 = sdesc_sw128(tile + BOX), q0 = sdesc_sw128(tile + 2 * BOX);
+            mma4_ss(tm, k0, 2, k0, 2, id, 0u);
+            mma4_ss(tm, k1, 2, k1, 2, id, 1u);
+            mma4_ss(tm + C, k1, 2, k0, 2, id, 0u);
+            mma4_ss(tm + C, q0, 2, k1, 2, id, 1u);
             mma_commit_w(done);
             if (!wait(done, 0)) mbar_wait(done, 0, DRAIN_NS);
+            issued = true;
         }
     }
     __syncthreads();
@@ -211,6 +224,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     {   // thread: one row of [K K^T; Q K^T]; warps 0-1 make A, warps 2-3 P
         const int r = tid % C;
         const float gh = sGh[r], gl = sGl[r], f = warp < 2 ? sB[r] : scale;
+        const float* from_h = warp < 2 ? sGh : sCh;
+        const float* from_l = warp < 2 ? sGl : sCl;
         const int last = warp < 2 ? r - 1 : r;        // the row's last column
 #pragma unroll 1
         for (int col = 0; col < C; col += 32) {
@@ -223,11 +238,11 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 }
                 continue;
             }
-            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + col, x);
+            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + (warp < 2 ? 0 : C) + col, x);
             wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-                const float4 ch = *reinterpret_cast<const float4*>(sGh + col + i), cl = *reinterpret_cast<const float4*>(sGl + col + i);
+                const float4 ch = *reinterpret_cast<const float4*>(from_h + col + i), cl = *reinterpret_cast<const float4*>(from_l + col + i);
                 const float dh[4] = {ch.x, ch.y, ch.z, ch.w}, dl[4] = {cl.x, cl.y, cl.z, cl.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -246,17 +261,15 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     if (tid < C) {
         const float gh = sGh[tid], gl = sGl[tid], gam = exp2f(gh + gl);
+        const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
         reinterpret_cast<float*>(rec + REC_NGAM)[tid] = s_abort ? __int_as_float(0x7fc00000) : -gam;
-        reinterpret_cast<float*>(rec + REC_ETA)[tid] = exp2f((sGh[C - 1] - gh) + (sGl[C - 1] - gl));
+        reinterpret_cast<float*>(rec + REC_ETA)[tid] = exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
         reinterpret_cast<float*>(rec + REC_GQ)[tid] = scale * gam;
         reinterpret_cast<float*>(rec + REC_BETA)[tid] = sB[tid];
+        sNG[tid] = -gam;
     }
     fence_before_sync();
     __syncthreads();
-    if (warp == 1) {
-        fence_after_sync();
-        tmem_dealloc(tm, 64);
-    }
     {   // the 16 x 16 diagonal blocks, one per warp: forward substitution, one column per thread (lanes 16-31 repeat
         // lanes 0-15), its values in registers and the rows of A as broadcast reads
         const float* a = sA + 16 * warp * (LD + 1);
@@ -308,6 +321,61 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 for (int e = 0; e < 16; ++e) x[i + e] = 0.f;
             }
         store_split(rec + REC_TH, rec + REC_TL, r, col, x);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(sNG + col + i);
+            x[i] *= v.x; x[i + 1] *= v.y; x[i + 2] *= v.z; x[i + 3] *= v.w;
+        }
+        store_split(sm + A_OFF, sm + A_OFF + BOX, r, col, x);
+    }
+    fence_smem_to_async();
+    __syncthreads();
+    // -W^T = K^T (-T diag(gam))^T, d_k as M
+    if (warp == 0) {
+        fence_after_sync();
+        if (issued) {
+            constexpr uint32_t id = idesc_bf16(128, C, true);
+            const uint64_t kd = (sdesc_sw128(tile) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
+            mma4_ss(tm, kd, 128, sdesc(tile + A_OFF, 128, 1024), 16, id, 0u);
+            mma4_ss(tm, kd, 128, sdesc(tile + A_OFF + BOX, 128, 1024), 16, id, 1u);
+            mma_commit_w(done);
+            if (!wait(done, 1)) mbar_wait(done, 1, DRAIN_NS);
+        }
+    }
+    __syncthreads();
+    fence_after_sync();
+    {   // thread: channel `tid`, all 64 rows, as two planes of swizzled boxes
+        uint8_t* dst = sm + (tid / 64) * BOX + (tid % 8) * 2;
+        const int piece = (tid % 64) / 8;
+#pragma unroll 1
+        for (int col = 0; col < C; col += 32) {
+            float x[32];
+            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + col, x);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                float hi, lo;
+                split_bf16(x[i], x[i + 1], hi, lo);
+                uint8_t* a = dst + (col + i) * 128 + ((piece ^ (i & 7)) * 16);
+                uint8_t* b = dst + (col + i + 1) * 128 + ((piece ^ ((i + 1) & 7)) * 16);
+                *reinterpret_cast<uint16_t*>(a) = (uint16_t)__float_as_uint(hi);
+                *reinterpret_cast<uint16_t*>(b) = (uint16_t)(__float_as_uint(hi) >> 16);
+                *reinterpret_cast<uint16_t*>(a + 2 * BOX) = (uint16_t)__float_as_uint(lo);
+                *reinterpret_cast<uint16_t*>(b + 2 * BOX) = (uint16_t)(__float_as_uint(lo) >> 16);
+            }
+        }
+    }
+    fence_smem_to_async();
+    fence_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+        bulk_store(rec + REC_WH, tile, 4 * BOX);
+        bulk_commit();
+        bulk_wait_all();
+    }
+    if (warp == 1) {
+        fence_after_sync();
+        tmem_dealloc(tm, 128);
     }
 }
 
@@ -337,14 +405,14 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
 static DeviceFlags g_prep_attr_done;
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, float beta_floor, cudaStream_t stream)
+                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream)
 {
     const cudaError_t e = once_per_device(g_prep_attr_done, [](int) {
         return cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep::SMEM);
     });
     if (e != cudaSuccess) return e;
     prep_kernel<<<(unsigned)(slot_count(seqs) * HV), prep::NT, prep::SMEM, stream>>>(
-        mq, mk, g, beta, seqs, rec, scale, HK, HV, gate_f32, beta_floor, bounded_wait_limit_ns());
+        mq, mk, g, beta, seqs, rec, scale, HK, HV, gate_f32, backward, bounded_wait_limit_ns());
     note_launches(1);
     return cudaGetLastError();
 }
