@@ -54,14 +54,17 @@ constexpr uint32_t S_V = 4 * BOX, S_REC = 6 * BOX;
 constexpr uint32_t STAGE = S_REC + REC_W_BYTES;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 constexpr uint32_t S_P = STAGES * STAGE;             // reverse: P, one buffer
-constexpr uint32_t S_OUT = S_P + P_BYTES;            // U or dV staging [32][128] bf16
-constexpr uint32_t SMEM = S_OUT + 32 * D * 2 + 1024;
+constexpr uint32_t SMEM = S_P + P_BYTES + 1024;
 
-enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MV = B_MD + 2, B_S, B_U = B_S + 2,
-       B_DO = B_U + 2, B_OFREE, B_DRAIN, N_BAR };
+// A wait by parity may not fall two completions behind, so what a slower role
+// waits for goes by chunk parity: a stage's last product (B_FREE, the loads),
+// U or dV (B_MV, the output warps) and its having been read (B_OFREE).
+enum { B_FULL = 0, B_FREE = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MV = B_MD + 2, B_S = B_MV + 2, B_U = B_S + 2,
+       B_DO = B_U + 2, B_OFREE, B_DRAIN = B_OFREE + 2, N_BAR };
 
 constexpr uint32_t T_SH = 0, T_SL = 64;
-constexpr uint32_t T_U = 128;                        // forward: U^T; reverse: (K dS1)^T, then dV^T
+constexpr uint32_t T_U = 128;                        // forward: U^T, by chunk parity here or in T_U2; reverse: (K dS1)^T, then dV^T
+constexpr uint32_t T_U2 = 256;
 constexpr uint32_t T_UH = 192, T_UL = 224;           // forward: (eta U)^T; reverse: dU^T
 constexpr uint32_t T_PO = 256;                       // reverse: (P^T dO)^T
 constexpr uint32_t T_OH = 320, T_OL = 352;           // reverse: (gam dO~)^T
@@ -94,6 +97,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     const int64_t slot0 = (int64_t)(begin / C) + n;
     auto bar = [&](int b) { return smem_u32(&bars[b]); };
     auto chunk_at = [&](int c) { return REV ? chunks - 1 - c : c; };
+    auto u_cols = [](int c) { return REV || (c & 1) == 0 ? T_U : T_U2; };
     const Waits wait = {s_abort, &g_back_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
@@ -143,11 +147,10 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             float4 eta[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
-            arrive(B_EMPTY + s);
             float x[16];
             wait(bar(B_MU + th), c & 1);             // U, or K dS1 and P^T dO
             fence_after_sync();
-            tmem_ld16(t + T_U + 16 * part, x);
+            tmem_ld16(t + u_cols(c) + 16 * part, x);
             if constexpr (REV) {
                 float y[16];
                 tmem_ld16(t + T_PO + 16 * part, y);
@@ -198,14 +201,14 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 for (int i = 0; i < 16; ++i) out[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
         }
     } else if (warp < W_MMA) {
-        const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
+        const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
+        const int64_t step = (int64_t)p.HV * D;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1, t0 = begin + chunk_at(c) * C, nv = min(C, end - t0);
-            wait(bar(B_FULL + s), (c >> 1) & 1);
             if constexpr (REV) {                     // gam dO~ as an operand; the previous one has been read
+                wait(bar(B_FULL + s), (c >> 1) & 1);
                 if (c > 0) wait(bar(B_MD + 1), (c - 1) & 1);
                 fence_after_sync();
                 const uint8_t* box = sm + s * STAGE + S_V + (j / 64) * BOX + (j % 8) * 2;
@@ -233,44 +236,34 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_DO));
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
-            if constexpr (REV) {
-                wait(bar(B_MV), c & 1);
-            } else {
-                wait(bar(B_MU), c & 1);
-                wait(bar(B_MU + 1), c & 1);
-            }
+            wait(bar(B_MV + s), (c >> 1) & 1);
             fence_after_sync();
+            const int64_t at = (int64_t)t0 * step + hv * D + j;
+            __nv_bfloat16* out0 = (REV ? p.dv : p.u)[0] + at;
+            __nv_bfloat16* out1 = (REV ? p.dv : p.u)[1] + at;
+            int left = nv;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 float x[32];
-                tmem_ld32(t + T_U + 32 * q, x);
+                tmem_ld32(t + u_cols(c) + 32 * q, x);
                 wait_ld();
                 if (q == 1) {
                     fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_OFREE));
+                    if (lane == 0) mbar_arrive(bar(B_OFREE + s));
                 }
-#pragma unroll 1
-                for (int plane = 0; plane < 2; ++plane) {
+                // a warp's store is 64 bytes of one row: two whole sectors
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
-                        so[i * D + j] = hi;
-                        x[i] -= __bfloat162float(hi);         // the second plane's
+                for (int i = 0; i < 32; ++i) {
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
+                    if (i < left) {
+                        *out0 = hi;
+                        *out1 = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
                     }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    __nv_bfloat16* out = (REV ? p.dv : p.u)[plane];
-#pragma unroll
-                    for (int e = 0; e < 32 * D / 8 / 128; ++e) {
-                        const int i = ot + 128 * e, r = 32 * q + i / (D / 8), c8 = i % (D / 8);
-                        if (r < nv)
-                            *reinterpret_cast<uint4*>(out + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
-                                *reinterpret_cast<const uint4*>(so + (i / (D / 8)) * D + 8 * c8);
-                    }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    out0 += step;
+                    out1 += step;
                 }
+                left -= 32;
             }
         }
     } else if (warp == W_MMA) {
@@ -302,10 +295,10 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 mma4_ss(tm + T_PO, vd, 128, ph, 128, id_v, 0u);
                 mma4_ss(tm + T_PO, vd, 128, ph + (uint64_t)(BOX >> 4), 128, id_v, 1u);
             } else {                                 // U^T = V^T T^T
-                if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) return false;
+                if (c > 1 && !ok(B_OFREE + (c & 1), ((c >> 1) - 1) & 1)) return false;      // chunk c - 2's U has been read
                 fence_after_sync();
-                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
-                mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
+                mma4_ss(tm + u_cols(c), vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
+                mma4_ss(tm + u_cols(c), vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
             }
             return true;
         };
@@ -318,9 +311,10 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             // forward: -(W S)^T; reverse: (K dS1)^T; half b of d_k, tokens from tok0 (32 or, by idesc, all 64)
             auto s_product = [&](int b, int tok0, uint32_t id) {
                 const uint64_t h = (REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4))) + (uint64_t)(tok0 * 8);
-                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h, 2, id, REV && b == 0 ? 0u : 1u);
-                mma4_ts(tm + T_U + tok0, tm + T_SL + 32 * b, h, 2, id, 1u);
-                if (!REV) mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h + LO, 2, id, 1u);
+                const uint32_t u = tm + u_cols(c) + tok0;
+                mma4_ts(u, tm + T_SH + 32 * b, h, 2, id, REV && b == 0 ? 0u : 1u);
+                mma4_ts(u, tm + T_SL + 32 * b, h, 2, id, 1u);
+                if (!REV) mma4_ts(u, tm + T_SH + 32 * b, h + LO, 2, id, 1u);
             };
             // forward: (K^T eta U)^T; reverse: -(W^T dU)^T; half b of d_k from the tokens of half k
             auto d_product = [&](int b, int k) {
@@ -329,7 +323,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 mma2_ts(tm + T_D + 64 * b, tm + T_UL + 16 * k, h, 128, id_bmn, 1u);
                 if (REV) mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, h + LO, 128, id_bmn, 1u);
             };
-            if (REV && c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
+            if (REV && c > 0 && !ok(B_OFREE + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
             if (!ok(B_S, c & 1)) break;
             fence_after_sync();
             s_product(0, 0, id_n64);
@@ -339,6 +333,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             mma_commit_w(bar(B_MU));
             s_product(1, 32, id_n32);
             mma_commit_w(bar(B_MU + 1));
+            if (!REV) mma_commit_w(bar(B_MV + (c & 1)));
             if constexpr (REV) {
                 if (!ok(B_DO, c & 1)) break;
                 fence_after_sync();
@@ -364,8 +359,9 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 mma4_ts(tm + T_U, tm + T_UH, th, 128, id_bmn, 0u);
                 mma4_ts(tm + T_U, tm + T_UL, th, 128, id_bmn, 1u);
                 mma4_ts(tm + T_U, tm + T_UH, tl, 128, id_bmn, 1u);
-                mma_commit_w(bar(B_MV));
+                mma_commit_w(bar(B_MV + (c & 1)));
             }
+            mma_commit_w(bar(B_FREE + (c & 1)));
             if (c + 1 < chunks && !begin_chunk(c + 1)) break;
         }
         if (chunks > 0) {                             // what was issued ends before its memory goes
@@ -378,8 +374,9 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const int s = c & 1;
-            // chunk c - 2 is done with the stage: the gates' (and dO's) readers, its last product
-            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1) || !wait(bar(REV ? B_MV : B_MD + 1), c & 1))) break;
+            // chunk c - 2's last product is complete: it is done with the stage (who reads the gates or dO does so
+            // before a product that this one waits for)
+            if (c >= 2 && !wait(bar(B_FREE + s), ((c >> 1) - 1) & 1)) break;
             if (*s_abort) break;
             const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
             const int y = begin + chunk_at(c) * C;
@@ -393,6 +390,16 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             }
             bulk_load(base + S_REC, rec, REC_W_BYTES, full);
             loaded = c + 1;
+            if (c + 2 < chunks) {                     // on its way to L2
+                const int yn = begin + chunk_at(c + 2) * C;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tma_prefetch_2d(&mk, hk * D + 64 * b, yn);
+                    if (REV) tma_prefetch_2d(&mq, hk * D + 64 * b, yn);
+                    tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
+                }
+                bulk_prefetch(p.rec + ((slot0 + chunk_at(c + 2)) * p.HV + hv) * REC_BYTES, REV ? REC_BYTES : REC_W_BYTES);
+            }
             if (REV) {                                // P's buffer has been read when chunk c - 1's first products are there
                 if (c >= 1 && !wait(bar(B_MU + 1), (c - 1) & 1)) break;
                 mbar_arrive_expect_tx(bar(B_P), P_BYTES);
@@ -421,9 +428,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     const int hv = (blockIdx.x >> 1) % p.HV, n = (blockIdx.x >> 1) / p.HV;
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
-                            : b == B_S || b == B_S + 1 ? N_CHAIN
-                            : b == B_U || b == B_U + 1 ? N_CHAIN / 2 : b == B_DO || b == B_OFREE ? N_OUT : 1;
+            const int count = b == B_S || b == B_S + 1 ? N_CHAIN
+                            : b == B_U || b == B_U + 1 ? N_CHAIN / 2 : b == B_DO || b == B_OFREE || b == B_OFREE + 1 ? N_OUT : 1;
             mbar_init(smem_u32(&bars[b]), count);
         }
         fence_mbar_init();

@@ -47,6 +47,7 @@ constexpr uint32_t REC_PH = REC_BETA + C * 4;        // P, likewise
 constexpr uint32_t REC_PL = REC_PH + BOX;
 constexpr uint32_t REC_BYTES = REC_PL + BOX;
 constexpr uint32_t REC_W_BYTES = REC_PH;             // W, T and the gates; P is needed at another time
+constexpr uint32_t GATE_BYTES = REC_PH - REC_NGAM;
 constexpr uint32_t P_BYTES = REC_BYTES - REC_PH;
 static_assert(REC_BYTES == 66560 && REC_W_BYTES % 1024 == 0, "record");
 
@@ -135,6 +136,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x
 {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(mbar) : "memory");
+}
+// The same data on its way to L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t mbar)
 {

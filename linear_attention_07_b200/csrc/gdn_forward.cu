@@ -16,11 +16,11 @@
 //   warps 0-15  chain: thread (j, part) holds S[dk][j] for 16 + 16 values of
 //               dk and takes 16 of the chunk's tokens; eta U, the state
 //               update, and their split into bf16 pairs
-//   warps 16-19 output: thread j takes O^T's row j, 64 tokens, through
-//               shared memory to 16-byte stores, off the chain's path
+//   warps 16-19 output: thread j takes O^T's row j, 64 tokens, off the
+//               chain's path
 //   warp 20     issues every MMA
-//   warp 21     loads: K, Q, V (128-byte swizzle), W, T and the gates into two
-//               stages, P into one buffer
+//   warp 21     loads: K, Q, V (128-byte swizzle), W and T into two stages, P
+//               into one buffer, the gates into four slots; prefetches to L2
 // The chain waits for two products in turn (W S, K^T U) and converts between
 // them; splitting fp32 values into bf16 pairs is most of what the SM issues.
 // What the chain does not wait for (T V, X_Q, O) is issued where the tensor
@@ -40,18 +40,21 @@ constexpr int N_CHAIN = 16, N_OUT = 4;               // warps
 constexpr int W_MMA = N_CHAIN + N_OUT, W_LOAD = W_MMA + 1;
 constexpr int NT = 32 * (W_LOAD + 1);
 
-// a stage: K0 Q0 K1 Q1 V0 V1 (boxes of 64 tokens x 64 channels), W, T and gates
-constexpr int STAGES = 2;
+// a stage: K0 Q0 K1 Q1 V0 V1 (boxes of 64 tokens x 64 channels), W and T
+constexpr int STAGES = 2, GATE_SLOTS = 4;
 constexpr uint32_t S_V = 4 * BOX;
 constexpr uint32_t S_REC = 6 * BOX;
-constexpr uint32_t STAGE = S_REC + REC_W_BYTES;
+constexpr uint32_t STAGE = S_REC + REC_NGAM;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 constexpr uint32_t S_P = STAGES * STAGE;             // P, one buffer
-constexpr uint32_t S_OUT = S_P + P_BYTES;            // o staging [32][128] bf16
-constexpr uint32_t SMEM = S_OUT + 32 * D * 2 + 1024;
+constexpr uint32_t S_GATE = S_P + P_BYTES;           // the gates, which the output warps read later than the rest
+constexpr uint32_t SMEM = S_GATE + GATE_SLOTS * GATE_BYTES + 1024;
 
 // barriers (a pair where the work goes in halves)
-enum { B_FULL = 0, B_EMPTY = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MO = B_MD + 2,
+// A wait by parity may not fall two completions behind: the gates, whose
+// readers may still be at chunk c while the stage takes chunk c + 2, have
+// barriers of their own.
+enum { B_FULL = 0, B_GATE = STAGES, B_P = B_GATE + GATE_SLOTS, B_MU, B_MD = B_MU + 2, B_MO = B_MD + 2,
        B_S, B_U = B_S + 2, B_OFREE = B_U + 2, B_DRAIN, N_BAR };
 
 // tensor memory columns
@@ -97,8 +100,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b >= B_EMPTY && b < B_EMPTY + STAGES ? N_CHAIN + N_OUT
-                            : b >= B_S && b < B_S + 2 ? N_CHAIN
+            const int count = b >= B_S && b < B_S + 2 ? N_CHAIN
                             : b >= B_U && b < B_U + 2 ? N_CHAIN / 2 : b == B_OFREE ? N_OUT : 1;
             mbar_init(bar(b), count);
         }
@@ -148,14 +150,12 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
-            const float* gates = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_NGAM);
-            wait(bar(B_FULL + s), (c >> 1) & 1);
+            const float* gates = reinterpret_cast<const float*>(sm + S_GATE + (c % GATE_SLOTS) * GATE_BYTES);
+            wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1);
             const float last = -gates[C - 1];
             float4 eta[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
-            arrive(B_EMPTY + s);
             float x[16];
             wait(bar(B_MU + th), c & 1);
             fence_after_sync();
@@ -195,14 +195,15 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 for (int i = 0; i < 16; ++i) hT[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
         }
     } else if (warp < W_MMA) {
-        const int sp = warp & 3, j = 32 * sp + lane, ot = tid - 32 * N_CHAIN;
+        const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
+        const int64_t step = (int64_t)p.HV * D;
+        __nv_bfloat16* out = p.o + (int64_t)begin * step + hv * D + j;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1, t0 = begin + c * C, nv = min(C, end - t0);
-            const float2* gq = reinterpret_cast<const float2*>(sm + s * STAGE + S_REC + REC_GQ);
-            wait(bar(B_FULL + s), (c >> 1) & 1);
+            const float2* gq = reinterpret_cast<const float2*>(sm + S_GATE + (c % GATE_SLOTS) * GATE_BYTES + (REC_GQ - REC_NGAM));
+            int left = end - begin - c * C;          // rows behind the sequence are not stored
+            wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1);
             wait(bar(B_MO), c & 1);
             fence_after_sync();
 #pragma unroll 1
@@ -216,26 +217,16 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_OFREE));
                 }
+                // a warp's store is 64 bytes of one row: two whole sectors
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     const float2 v = fma2(gq[16 * q + i / 2], make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
-                    so[i * D + j] = b2.x;
-                    so[(i + 1) * D + j] = b2.y;
+                    if (i < left) out[0] = b2.x;
+                    if (i + 1 < left) out[step] = b2.y;
+                    out += 2 * step;
                 }
-                if (q == 1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_EMPTY + s));
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                for (int e = 0; e < 32 * D / 8 / 128; ++e) {
-                    const int i = ot + 128 * e, r = 32 * q + i / (D / 8), c8 = i % (D / 8);
-                    if (r < nv)
-                        *reinterpret_cast<uint4*>(p.o + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
-                            *reinterpret_cast<const uint4*>(so + (i / (D / 8)) * D + 8 * c8);
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                left -= 32;
             }
         }
     } else if (warp == W_MMA) {
@@ -324,39 +315,59 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         }
     } else if (lane == 0) {
         const uint8_t* rec = p.rec + (slot0 * p.HV + hv) * REC_BYTES;
+        const int64_t rec_step = (int64_t)p.HV * REC_BYTES;
         int loaded = 0, loaded_p = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1;
-            // the stage of chunk c is free once chunk c - 2 is done with it: its products (O's is the last), the
-            // gates' readers; P's buffer once the products of chunk c - 1 are
-            if (c >= 2 && (!wait(bar(B_EMPTY + s), ((c >> 1) - 1) & 1) || !wait(bar(B_MO), c & 1))) break;
+            // chunk c - 2's products (O's is the last) are complete: its stage is free, and P's buffer for chunk c - 1.
+            // Its gates slot is that of chunk c + 2, which waits for a later output.
+            if (c >= 2 && !wait(bar(B_MO), c & 1)) break;
             if (*(volatile int*)&s_abort) break;
-            const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
+            auto load_p = [&](int cp) {
+                mbar_arrive_expect_tx(bar(B_P), P_BYTES);
+                bulk_load(smem_u32(sm + S_P), rec + cp * rec_step + REC_PH, P_BYTES, bar(B_P));
+                loaded_p = cp + 1;
+            };
+            if (c >= 2) load_p(c - 1);
+            const uint32_t base = smem_u32(sm + (c & 1) * STAGE), full = bar(B_FULL + (c & 1));
             const int y = begin + c * C;
+            const uint8_t* r = rec + c * rec_step;
             mbar_arrive_expect_tx(full, STAGE);
+            const uint32_t gate = bar(B_GATE + c % GATE_SLOTS);
+            mbar_arrive_expect_tx(gate, GATE_BYTES);
+            bulk_load(smem_u32(sm + S_GATE) + (c % GATE_SLOTS) * GATE_BYTES, r + REC_NGAM, GATE_BYTES, gate);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
+            bulk_load(base + S_REC, r, REC_NGAM, full);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
                 tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
-                tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
             }
-            bulk_load(base + S_REC, rec + (int64_t)c * p.HV * REC_BYTES, REC_W_BYTES, full);
             loaded = c + 1;
-            if (c == 1) continue;                     // its P follows when the first chunk is done
-            const int cp = c == 0 ? 0 : c - 1;        // chunk c - 2's products are done: P of chunk c - 1
-            mbar_arrive_expect_tx(bar(B_P), P_BYTES);
-            bulk_load(smem_u32(sm + S_P), rec + (int64_t)cp * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
-            loaded_p = cp + 1;
+            if (c == 0) load_p(0);
+            const int cn = c < 2 ? c + 2 : c + 1;     // what will be loaded next, on its way to L2
+            if (cn < chunks && c >= 1) {
+                const int yn = begin + cn * C;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
+                    tma_prefetch_2d(&mk, hk * D + 64 * b, yn);
+                    tma_prefetch_2d(&mq, hk * D + 64 * b, yn);
+                }
+                bulk_prefetch(rec + cn * rec_step, REC_BYTES);
+            }
         }
-        if (loaded == chunks && chunks > 1 && wait(bar(B_MO), chunks & 1)) {     // the last chunk's P, after chunk - 2
+        if (loaded == chunks && chunks > 1 && wait(bar(B_MO), chunks & 1)) {     // the last chunk's P
             mbar_arrive_expect_tx(bar(B_P), P_BYTES);
-            bulk_load(smem_u32(sm + S_P), rec + (int64_t)(chunks - 1) * p.HV * REC_BYTES + REC_PH, P_BYTES, bar(B_P));
+            bulk_load(smem_u32(sm + S_P), rec + (chunks - 1) * rec_step + REC_PH, P_BYTES, bar(B_P));
             loaded_p = chunks;
         }
         // everything loaded has landed before the end
         for (int c = max(0, loaded - STAGES); c < loaded; ++c)
             mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
+        for (int c = max(0, loaded - GATE_SLOTS); c < loaded; ++c)
+            mbar_wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1, DRAIN_NS);
         if (loaded_p > 0) mbar_wait(bar(B_P), (loaded_p - 1) & 1, DRAIN_NS);
     }
     fence_before_sync();
