@@ -372,8 +372,8 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * Tokens before the first sequence and behind the last get zero gradients.  A
  * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
  * atomics: the same inputs give the same bits.  Three launches (one more with
- * cu_seqlens); stream-ordered workspace of 197,632 bytes per value head and
- * 64-token chunk and 768 bytes per token and value head (KDA_ERR_NO_MEMORY if
+ * cu_seqlens); stream-ordered workspace of 263,168 bytes per value head and
+ * 64-token chunk (KDA_ERR_NO_MEMORY if
  * it cannot be had).  Supported: d_k == d_v == 128.
  *
  * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits

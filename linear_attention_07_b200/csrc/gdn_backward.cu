@@ -42,6 +42,12 @@ namespace bk {
 // (j / 64) * 16384 + (i / 8) * 1024 + (j % 64) * 16 + (i % 8) * 2
 constexpr uint32_t PLANE = D * D * 2, HALF = PLANE / 2;
 constexpr uint32_t ST_SBO = 1024, ST_LBO = 128;
+// U and dV as two planes each, as operands with the tokens as M or N and d_v
+// as K (MN-major without swizzle): element (r, j) at (r / 8) * 2048 + j * 16 +
+// (r % 8) * 2.  In both, the thread that owns column j writes 16 bytes, a warp
+// 512 in a row.
+constexpr uint32_t UPLANE = C * D * 2;
+constexpr uint32_t U_SBO = 2048, U_LBO = 128;
 
 // ------------------------------------------------------------------ chains --
 
@@ -59,8 +65,8 @@ constexpr uint32_t SMEM = S_P + P_BYTES + 1024;
 // A wait by parity may not fall two completions behind, so what a slower role
 // waits for goes by chunk parity: a stage's last product (B_FREE, the loads),
 // U or dV (B_MV, the output warps) and its having been read (B_OFREE).
-enum { B_FULL = 0, B_FREE = STAGES, B_P = 2 * STAGES, B_MU, B_MD = B_MU + 2, B_MV = B_MD + 2, B_S = B_MV + 2, B_U = B_S + 2,
-       B_DO = B_U + 2, B_OFREE, B_DRAIN = B_OFREE + 2, N_BAR };
+enum { B_FULL = 0, B_FREE = STAGES, B_P = 2 * STAGES, B_MU, B_MD, B_MV = B_MD + 2, B_S = B_MV + 2, B_U = B_S + 2, B_DO,
+       B_OFREE, B_DRAIN = B_OFREE + 2, N_BAR };
 
 constexpr uint32_t T_SH = 0, T_SL = 64;
 constexpr uint32_t T_U = 128;                        // forward: U^T, by chunk parity here or in T_U2; reverse: (K dS1)^T, then dV^T
@@ -78,17 +84,18 @@ struct Args {
     float* dh0;
     uint8_t* S0;            // per (slot, value head): the chunk's start state, two planes
     uint8_t* dS1;           // and its end state's gradient
-    __nv_bfloat16* u[2];    // U and dV, two planes [tokens][HV][D] each; dV's first is the gradient
-    __nv_bfloat16* dv[2];
+    uint8_t* u;             // U, two planes
+    uint8_t* dv;            // dV, two planes
     int HK, HV;
     uint64_t wait_ns;
 };
 
 template <bool REV>
 __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& p,
-                                      uint8_t* sm, uint64_t* bars, volatile int* s_abort, uint32_t tm, int n, int hv)
+                                      uint8_t* sm, uint64_t* bars, volatile int* s_abort, int n, int hv)
 {
     using namespace tc;
+    constexpr uint32_t tm = 0;                       // all of tensor memory is this CTA's
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hk = hv / (p.HV / p.HK);
     int begin, end;
@@ -101,7 +108,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     const Waits wait = {s_abort, &g_back_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
-        const int sp = warp & 3, part = warp >> 2, th = part >> 1, j = 32 * sp + lane;
+        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         const float* init = REV ? p.dhT : p.h0;
         const float* h = init ? init + ((int64_t)n * p.HV + hv) * D * D + j : nullptr;
@@ -148,7 +155,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll
             for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
             float x[16];
-            wait(bar(B_MU + th), c & 1);             // U, or K dS1 and P^T dO
+            wait(bar(B_MU), c & 1);                  // U, or K dS1 and P^T dO
             fence_after_sync();
             tmem_ld16(t + u_cols(c) + 16 * part, x);
             if constexpr (REV) {
@@ -177,7 +184,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 tmem_st8(t + T_UH + 8 * part, hi);
                 tmem_st8(t + T_UL + 8 * part, lo);
             }
-            give(B_U + th);
+            give(B_U);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 wait(bar(B_MD + b), c & 1);
@@ -203,10 +210,9 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        const int64_t step = (int64_t)p.HV * D;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1, t0 = begin + chunk_at(c) * C, nv = min(C, end - t0);
+            const int s = c & 1, nv = min(C, end - begin - chunk_at(c) * C);
             if constexpr (REV) {                     // gam dO~ as an operand; the previous one has been read
                 wait(bar(B_FULL + s), (c >> 1) & 1);
                 if (c > 0) wait(bar(B_MD + 1), (c - 1) & 1);
@@ -238,10 +244,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             }
             wait(bar(B_MV + s), (c >> 1) & 1);
             fence_after_sync();
-            const int64_t at = (int64_t)t0 * step + hv * D + j;
-            __nv_bfloat16* out0 = (REV ? p.dv : p.u)[0] + at;
-            __nv_bfloat16* out1 = (REV ? p.dv : p.u)[1] + at;
-            int left = nv;
+            uint8_t* out = (REV ? p.dv : p.u) + ((slot0 + chunk_at(c)) * p.HV + hv) * (2 * (int64_t)UPLANE) + j * 16;
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 float x[32];
@@ -252,24 +255,21 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_OFREE + s));
                 }
-                // a warp's store is 64 bytes of one row: two whole sectors
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(x[i]);
-                    if (i < left) {
-                        *out0 = hi;
-                        *out1 = __float2bfloat16_rn(x[i] - __bfloat162float(hi));
-                    }
-                    out0 += step;
-                    out1 += step;
+                for (int i = 0; i < 32; i += 8) {
+                    float hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split_bf16(x[i + 2 * e], x[i + 2 * e + 1], hi[e], lo[e]);
+                    *reinterpret_cast<float4*>(out) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<float4*>(out + UPLANE) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+                    out += U_SBO;
                 }
-                left -= 32;
             }
         }
     } else if (warp == W_MMA) {
-        const uint32_t id_n64 = idesc_bf16(128, 64), id_n32 = idesc_bf16(128, 32), id_bmn = idesc_bf16(128, 64, false, true);
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_bmn = idesc_bf16(128, 64, false, true);
         const uint32_t id_v = idesc_bf16(128, 64, true, REV);
-        auto ok = [&](int b, uint32_t parity) {
+        auto ok = [&](int b, uint32_t parity) {       // every lane sees the same outcome
             const bool w = wait(bar(b), parity);
             return __all_sync(0xffffffffu, w) != 0;
         };
@@ -292,13 +292,13 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             if constexpr (REV) {                     // (P^T dO)^T = dO^T P
                 if (!ok(B_P, c & 1)) return false;
                 const uint64_t ph = sdesc(smem_u32(sm + S_P), 1024, 128);
-                mma4_ss(tm + T_PO, vd, 128, ph, 128, id_v, 0u);
-                mma4_ss(tm + T_PO, vd, 128, ph + (uint64_t)(BOX >> 4), 128, id_v, 1u);
+                mma4_ss<128, 128>(tm + T_PO, vd, ph, id_v, 0u);
+                mma4_ss<128, 128>(tm + T_PO, vd, ph + (uint64_t)(BOX >> 4), id_v, 1u);
             } else {                                 // U^T = V^T T^T
                 if (c > 1 && !ok(B_OFREE + (c & 1), ((c >> 1) - 1) & 1)) return false;      // chunk c - 2's U has been read
                 fence_after_sync();
-                mma4_ss(tm + u_cols(c), vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
-                mma4_ss(tm + u_cols(c), vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
+                mma4_ss<128, 16>(tm + u_cols(c), vd, sdesc(base + S_REC + REC_TH, 128, 1024), id_v, 0u);
+                mma4_ss<128, 16>(tm + u_cols(c), vd, sdesc(base + S_REC + REC_TL, 128, 1024), id_v, 1u);
             }
             return true;
         };
@@ -308,31 +308,22 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             const uint32_t base = smem_u32(sm + (c & 1) * STAGE);
             const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
             constexpr uint64_t LO = 2 * BOX >> 4;
-            // forward: -(W S)^T; reverse: (K dS1)^T; half b of d_k, tokens from tok0 (32 or, by idesc, all 64)
-            auto s_product = [&](int b, int tok0, uint32_t id) {
-                const uint64_t h = (REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4))) + (uint64_t)(tok0 * 8);
-                const uint32_t u = tm + u_cols(c) + tok0;
-                mma4_ts(u, tm + T_SH + 32 * b, h, 2, id, REV && b == 0 ? 0u : 1u);
-                mma4_ts(u, tm + T_SL + 32 * b, h, 2, id, 1u);
-                if (!REV) mma4_ts(u, tm + T_SH + 32 * b, h + LO, 2, id, 1u);
-            };
-            // forward: (K^T eta U)^T; reverse: -(W^T dU)^T; half b of d_k from the tokens of half k
-            auto d_product = [&](int b, int k) {
-                const uint64_t h = (REV ? wd + (uint64_t)(b * (BOX >> 4)) : kq + (uint64_t)(2 * b * (BOX >> 4))) + (uint64_t)(k * 256);
-                mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, h, 128, id_bmn, REV || k > 0 ? 1u : 0u);
-                mma2_ts(tm + T_D + 64 * b, tm + T_UL + 16 * k, h, 128, id_bmn, 1u);
-                if (REV) mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, h + LO, 128, id_bmn, 1u);
+            // forward: -(W S)^T; reverse: (K dS1)^T; half b of d_k
+            auto s_product = [&](int b) {
+                const uint64_t h = REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4));
+                const uint32_t u = tm + u_cols(c);
+                mma4_ts<2>(u, tm + T_SH + 32 * b, h, id_n64, REV && b == 0 ? 0u : 1u);
+                mma4_ts<2>(u, tm + T_SL + 32 * b, h, id_n64, 1u);
+                if (!REV) mma4_ts<2>(u, tm + T_SH + 32 * b, h + LO, id_n64, 1u);
             };
             if (REV && c > 0 && !ok(B_OFREE + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
             if (!ok(B_S, c & 1)) break;
             fence_after_sync();
-            s_product(0, 0, id_n64);
+            s_product(0);
             if (!ok(B_S + 1, c & 1)) break;
             fence_after_sync();
-            s_product(1, 0, id_n32);
+            s_product(1);
             mma_commit_w(bar(B_MU));
-            s_product(1, 32, id_n32);
-            mma_commit_w(bar(B_MU + 1));
             if (!REV) mma_commit_w(bar(B_MV + (c & 1)));
             if constexpr (REV) {
                 if (!ok(B_DO, c & 1)) break;
@@ -340,25 +331,25 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {        // Q^T (gam dO~), while the chain computes dU
                     const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
-                    mma4_ts(tm + T_D + 64 * b, tm + T_OH, qd, 128, id_bmn, 0u);
-                    mma4_ts(tm + T_D + 64 * b, tm + T_OL, qd, 128, id_bmn, 1u);
+                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OH, qd, id_bmn, 0u);
+                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OL, qd, id_bmn, 1u);
                 }
             }
             if (!ok(B_U, c & 1)) break;
             fence_after_sync();
-            d_product(0, 0);
-            d_product(1, 0);
-            if (!ok(B_U + 1, c & 1)) break;
-            fence_after_sync();
-            d_product(0, 1);
-            mma_commit_w(bar(B_MD));
-            d_product(1, 1);
-            mma_commit_w(bar(B_MD + 1));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {            // forward: (K^T eta U)^T; reverse: -(W^T dU)^T; half b of d_k
+                const uint64_t h = REV ? wd + (uint64_t)(b * (BOX >> 4)) : kq + (uint64_t)(2 * b * (BOX >> 4));
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, h, id_bmn, REV ? 1u : 0u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UL, h, id_bmn, 1u);
+                if (REV) mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, h + LO, id_bmn, 1u);
+                mma_commit_w(bar(B_MD + b));
+            }
             if constexpr (REV) {                     // dV^T = dU^T T
                 const uint64_t th = sdesc(base + S_REC + REC_TH, 1024, 128), tl = th + (uint64_t)(BOX >> 4);
-                mma4_ts(tm + T_U, tm + T_UH, th, 128, id_bmn, 0u);
-                mma4_ts(tm + T_U, tm + T_UL, th, 128, id_bmn, 1u);
-                mma4_ts(tm + T_U, tm + T_UH, tl, 128, id_bmn, 1u);
+                mma4_ts<128>(tm + T_U, tm + T_UH, th, id_bmn, 0u);
+                mma4_ts<128>(tm + T_U, tm + T_UL, th, id_bmn, 1u);
+                mma4_ts<128>(tm + T_U, tm + T_UH, tl, id_bmn, 1u);
                 mma_commit_w(bar(B_MV + (c & 1)));
             }
             mma_commit_w(bar(B_FREE + (c & 1)));
@@ -401,7 +392,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 bulk_prefetch(p.rec + ((slot0 + chunk_at(c + 2)) * p.HV + hv) * REC_BYTES, REV ? REC_BYTES : REC_W_BYTES);
             }
             if (REV) {                                // P's buffer has been read when chunk c - 1's first products are there
-                if (c >= 1 && !wait(bar(B_MU + 1), (c - 1) & 1)) break;
+                if (c >= 1 && !wait(bar(B_MU), (c - 1) & 1)) break;
                 mbar_arrive_expect_tx(bar(B_P), P_BYTES);
                 bulk_load(smem_u32(sm + S_P), rec + REC_PH, P_BYTES, bar(B_P));
                 loaded_p = c + 1;
@@ -428,8 +419,7 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     const int hv = (blockIdx.x >> 1) % p.HV, n = (blockIdx.x >> 1) / p.HV;
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b == B_S || b == B_S + 1 ? N_CHAIN
-                            : b == B_U || b == B_U + 1 ? N_CHAIN / 2 : b == B_DO || b == B_OFREE || b == B_OFREE + 1 ? N_OUT : 1;
+            const int count = b == B_S || b == B_S + 1 || b == B_U ? N_CHAIN : b == B_DO || b == B_OFREE || b == B_OFREE + 1 ? N_OUT : 1;
             mbar_init(smem_u32(&bars[b]), count);
         }
         fence_mbar_init();
@@ -443,8 +433,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = s_tmem;
-    if (rev) chain<true>(mq, mk, mdo, p, sm, bars, &s_abort, tm, n, hv);
-    else chain<false>(mq, mk, mv, p, sm, bars, &s_abort, tm, n, hv);
+    if (rev) chain<true>(mq, mk, mdo, p, sm, bars, &s_abort, n, hv);
+    else chain<false>(mq, mk, mv, p, sm, bars, &s_abort, n, hv);
     fence_before_sync();
     __syncthreads();
     if (warp == W_MMA) {
@@ -454,10 +444,11 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     if (*(volatile int*)&s_abort) {                  // a wait expired: no partial result passes for a real one
         int begin, end;
         seq_range(p.seqs, n, begin, end);
-        const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7fc00000));
-        __nv_bfloat16* out = rev ? p.dv[0] : p.u[0]; // the local kernel reads both: its gradients become NaN
-        for (int64_t e = tid; e < (int64_t)(end - begin) * D; e += NT)
-            out[((int64_t)(begin + e / D) * p.HV + hv) * D + e % D] = nan;
+        const int64_t first = (int64_t)(begin / C) + n;
+        uint8_t* out = rev ? p.dv : p.u;             // the local kernel reads both: its gradients become NaN
+        for (int c = 0; c * C < end - begin; ++c)
+            for (int e = tid; e < (int)UPLANE / 4; e += NT)
+                reinterpret_cast<uint32_t*>(out + ((first + c) * p.HV + hv) * (2 * (int64_t)UPLANE))[e] = 0x7fc07fc0u;
         if (rev && p.dh0)
             for (int e = tid; e < D * D; e += NT) p.dh0[((int64_t)n * p.HV + hv) * D * D + e] = __int_as_float(0x7fc00000);
     }
@@ -467,17 +458,17 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 
 namespace lo {
 constexpr int LNT = 256;
-// boxes of 64 tokens x 64 channels, first and second 64 channels: dV0 dO0 dV1
-// dO1 (upper planes), then the lower plane of dV with U's upper plane between,
-// so that 128 rows from either are an operand, U's lower plane, K0 Q0 K1 Q1
-constexpr int X_V = 0, X_VL = 4, X_U = 5, X_UL = 8, X_K = 10, X_Q = 11, BOXES = 14;
+// dV and U (two planes each), then boxes of 64 tokens x 64 channels: dO0 dO1 K0 Q0 K1 Q1
+constexpr uint32_t O_V = 0, O_U = 2 * UPLANE, O_X = 4 * UPLANE;
+constexpr int X_DO = 0, X_K = 2, X_Q = 3, BOXES = 6;
 // halves (64 of d_v) of S0 and dS1, two planes each
-constexpr uint32_t O_ST = BOXES * BOX;
+constexpr uint32_t O_ST = O_X + BOXES * BOX;
 // the pair gradients [dkk; dqk] (128 rows of 64, swizzled as a box), two planes; the gates
 constexpr uint32_t O_L = O_ST + 4 * HALF, O_G = O_L + 4 * BOX;
 constexpr uint32_t SMEM = O_G + 1024 + 1024;
 constexpr uint32_t O_OUT = 0;                        // dk and dq [64][128] bf16, at the end
-// tensor memory: S0 [dV; dO]^T, dS1 U^T, [dkk; dqk] with K and the rest of dk, [dV; dO] U^T in two parts, [K; Q] K^T
+// tensor memory: S0 [dV; dO]^T, dS1 U^T, [dkk; dqk] with K and the rest of dk, dV U^T (lanes 0-63), dO U^T (lanes
+// 64-127), [K; Q] K^T
 constexpr uint32_t T_A = 0, T_B = 128, T_C = 192, T_G = 320, T_G2 = 384, T_KK = 448;
 
 // Sum over the warp's lanes of each of 32 values: lane l gets that of x[l].
@@ -502,14 +493,16 @@ struct LocalArgs {
     const uint8_t* rec;
     const uint8_t* S0;
     const uint8_t* dS1;
-    __nv_bfloat16 *dq, *dk, *dg, *dbeta;
+    const uint8_t* u;
+    const uint8_t* dvp;
+    __nv_bfloat16 *dq, *dk, *dv, *dg, *dbeta;
     float scale;
     int HK, HV;
     bool gate_f32;
     uint64_t wait_ns;
 };
 struct LocalMaps {
-    CUtensorMap q, k, dO, dv, dvl, u, ul;
+    CUtensorMap q, k, dO;
 };
 
 __global__ void __launch_bounds__(lo::LNT, 1)
@@ -554,10 +547,12 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     float ak[32], aq[32];                            // dk, dq at channel `row`, 32 tokens, over the group
 #pragma unroll
     for (int i = 0; i < 32; ++i) ak[i] = aq[i] = 0.f;
-    auto xb = [&](int b) { return sdesc_sw128(base + b * BOX); };
+    auto xb = [&](int b) { return sdesc_sw128(base + O_X + b * BOX); };
     auto xb_mn = [&](int b) {                        // 128 channels as M or N: the next 64 are two boxes on
-        return (sdesc_sw128(base + b * BOX) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(2 * BOX >> 4) << 16);
+        return (sdesc_sw128(base + O_X + b * BOX) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(2 * BOX >> 4) << 16);
     };
+    // a plane of dV or U, half h of d_v
+    auto up = [&](uint32_t off, int h) { return sdesc(base + off + h * 1024, U_LBO, U_SBO); };
     auto finish = [&](int which, int m) {            // every thread waits for the products
         if (!wait(done[which], m & 1) && warp == 0) mbar_wait(done[which], m & 1, DRAIN_NS);
         fence_after_sync();
@@ -573,16 +568,18 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     };
     // products with the states' half in shared memory: S0 [dV; dO]^T and dS1 U^T (d_k as M)
     auto state_products = [&](int h) {
-        const uint32_t id128 = idesc_bf16(128, 128, true, false), id64 = idesc_bf16(128, 64, true, false);
+        const uint32_t idk = idesc_bf16(128, 64, true, false), idm = idesc_bf16(128, 64, true, true);
         const uint64_t s0 = sdesc(base + O_ST, ST_LBO, ST_SBO), s0l = sdesc(base + O_ST + HALF, ST_LBO, ST_SBO);
         const uint64_t ds = sdesc(base + O_ST + 2 * HALF, ST_LBO, ST_SBO), dsl = sdesc(base + O_ST + 3 * HALF, ST_LBO, ST_SBO);
         const uint32_t more = h > 0 ? 1u : 0u;
-        mma4_ss(tm + T_A, s0, 16, xb(X_V + 2 * h), 2, id128, more);
-        mma4_ss(tm + T_A, s0l, 16, xb(X_V + 2 * h), 2, id128, 1u);
-        mma4_ss(tm + T_A, s0, 16, xb(X_VL + 2 * h), 2, id64, 1u);
-        mma4_ss(tm + T_B, ds, 16, xb(X_U + 2 * h), 2, id64, more);
-        mma4_ss(tm + T_B, dsl, 16, xb(X_U + 2 * h), 2, id64, 1u);
-        mma4_ss(tm + T_B, ds, 16, xb(X_UL + h), 2, id64, 1u);
+        mma4_ss<16, 16>(tm + T_A, s0, up(O_V, h), idm, more);
+        mma4_ss<16, 16>(tm + T_A, s0l, up(O_V, h), idm, 1u);
+        mma4_ss<16, 16>(tm + T_A, s0, up(O_V + UPLANE, h), idm, 1u);
+        mma4_ss<16, 2>(tm + T_A + 64, s0, xb(X_DO + h), idk, more);
+        mma4_ss<16, 2>(tm + T_A + 64, s0l, xb(X_DO + h), idk, 1u);
+        mma4_ss<16, 16>(tm + T_B, ds, up(O_U, h), idm, more);
+        mma4_ss<16, 16>(tm + T_B, dsl, up(O_U, h), idm, 1u);
+        mma4_ss<16, 16>(tm + T_B, ds, up(O_U + UPLANE, h), idm, 1u);
         mma_commit_w(done[1 + h]);
     };
     // <dS1, S0> over the half in shared memory
@@ -611,18 +608,16 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         const int hv = hk * group + m;
         const int64_t unit = slot * p.HV + hv;
         if (tid == 0) {
-            mbar_arrive_expect_tx(full, (m == 0 ? 14 : 10) * BOX + 4 * HALF + 1024);
+            mbar_arrive_expect_tx(full, (m == 0 ? 6 : 2) * BOX + 4 * UPLANE + 4 * HALF + 1024);
+            bulk_load(base + O_V, p.dvp + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, full);
+            bulk_load(base + O_U, p.u + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, full);
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 const int x = hv * D + 64 * b, y = hk * D + 64 * b;
-                tma_load_2d(base + (X_V + 2 * b) * BOX, &maps.dv, x, t0, full);
-                tma_load_2d(base + (X_V + 1 + 2 * b) * BOX, &maps.dO, x, t0, full);
-                tma_load_2d(base + (X_VL + 2 * b) * BOX, &maps.dvl, x, t0, full);
-                tma_load_2d(base + (X_U + 2 * b) * BOX, &maps.u, x, t0, full);
-                tma_load_2d(base + (X_UL + b) * BOX, &maps.ul, x, t0, full);
+                tma_load_2d(base + O_X + (X_DO + b) * BOX, &maps.dO, x, t0, full);
                 if (m == 0) {
-                    tma_load_2d(base + (X_K + 2 * b) * BOX, &maps.k, y, t0, full);
-                    tma_load_2d(base + (X_Q + 2 * b) * BOX, &maps.q, y, t0, full);
+                    tma_load_2d(base + O_X + (X_K + 2 * b) * BOX, &maps.k, y, t0, full);
+                    tma_load_2d(base + O_X + (X_Q + 2 * b) * BOX, &maps.q, y, t0, full);
                 }
             }
             load_states(unit, 0, full);
@@ -647,24 +642,27 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             }
         }
         land(full, m & 1);
-        if (nv < C) {                                 // rows behind the sequence
+        if (nv < C) {                                 // rows behind the sequence (U's and dV's are zero)
             for (int e = tid; e < (C - nv) * BOXES * 8; e += LNT) {
                 const int piece = e & 7, box = (e >> 3) % BOXES, rr = nv + (e >> 3) / BOXES;
-                *reinterpret_cast<uint4*>(sm + box * BOX + rr * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(sm + O_X + box * BOX + rr * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_smem_to_async();
         }
         __syncthreads();
         bool issued = false;
         if (warp == 0 && (issued = !__any_sync(0xffffffffu, *(volatile int*)&s_abort != 0))) {
-            const uint32_t id = idesc_bf16(128, 64);
+            // an operand of 64 rows is taken as 128 with its neighbours in shared memory, whose results are not read
+            const uint32_t id = idesc_bf16(128, 64), idm = idesc_bf16(128, 64, true, true), idb = idesc_bf16(128, 64, false, true);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
                 const uint32_t more = h > 0 ? 1u : 0u;
-                if (m == 0) mma4_ss(tm + T_KK, xb(X_K + 2 * h), 2, xb(X_K + 2 * h), 2, id, more);
-                mma4_ss(tm + T_G, xb(X_V + 2 * h), 2, xb(X_U + 2 * h), 2, id, more);
-                mma4_ss(tm + T_G, xb(X_V + 2 * h), 2, xb(X_UL + h), 2, id, 1u);
-                mma4_ss(tm + T_G2, xb(X_VL + 2 * h), 2, xb(X_U + 2 * h), 2, id, more);
+                if (m == 0) mma4_ss<2, 2>(tm + T_KK, xb(X_K + 2 * h), xb(X_K + 2 * h), id, more);
+                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U, h), idm, more);
+                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U + UPLANE, h), idm, 1u);
+                mma4_ss<16, 16>(tm + T_G, up(O_V + UPLANE, h), up(O_U, h), idm, 1u);
+                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U, h), idb, more);
+                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U + UPLANE, h), idb, 1u);
             }
             mma_commit_w(done[0]);
             state_products(0);
@@ -675,13 +673,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             float x[32], y[32];
             const int r = row % C;
             const bool is_q = row >= C;
-            tmem_ld32(t + T_G + 32 * half, x);
-            if (!is_q) tmem_ld32(t + T_G2 + 32 * half, y);      // warp-uniform
-            wait_ld();
-            if (!is_q) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] += y[i];
-            }
+            tmem_ld32(t + (is_q ? T_G2 : T_G) + 32 * half, x);  // is_q is warp-uniform
             tmem_ld32(t + T_KK + 32 * half, y);
             wait_ld();
             const float gh = sGh[r], gl = sGl[r], f = is_q ? p.scale : -1.f;
@@ -728,12 +720,12 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             const uint64_t l = sdesc_sw128(base + O_L), k = xb_mn(X_K), q = xb_mn(X_Q);
             constexpr uint64_t LO = 2 * BOX >> 4, Q_ROWS = BOX >> 4;
             // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk
-            mma4_ss(tm + T_C, k, 128, l, 2, id128, 0u);
-            mma4_ss(tm + T_C, k, 128, l + LO, 2, id128, 1u);
-            mma4_ss(tm + T_C, k, 128, l, 128, idmn, 1u);
-            mma4_ss(tm + T_C, k, 128, l + LO, 128, idmn, 1u);
-            mma4_ss(tm + T_C, q, 128, l + Q_ROWS, 128, idmn, 1u);
-            mma4_ss(tm + T_C, q, 128, l + LO + Q_ROWS, 128, idmn, 1u);
+            mma4_ss<128, 2>(tm + T_C, k, l, id128, 0u);
+            mma4_ss<128, 2>(tm + T_C, k, l + LO, id128, 1u);
+            mma4_ss<128, 128>(tm + T_C, k, l, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, k, l + LO, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, q, l + Q_ROWS, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, q, l + LO + Q_ROWS, idmn, 1u);
         }
         land(full2, m & 1);
         if (warp == 0 && issued) {
@@ -748,7 +740,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         const float* gates = reinterpret_cast<const float*>(sm + O_G);       // -gam, eta, scale gam, beta: 64 each
         {   // channel `row`, tokens 32 half .. + 31
             float a[32], b[32], pa[32];
-            const uint8_t* kp = sm + (X_K + 2 * (row / 64)) * BOX + (row % 8) * 2;
+            const uint8_t* kp = sm + O_X + (X_K + 2 * (row / 64)) * BOX + (row % 8) * 2;
             const int piece = (row % 64) / 8;
             auto at = [&](const uint8_t* x, int tok) {
                 return to_f32(*reinterpret_cast<const __nv_bfloat16*>(x + tok * 128 + ((piece ^ (tok & 7)) * 16)));
@@ -781,6 +773,22 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 ak[i] += z;
             }
             sB[sp][32 * half + lane] = lane_sums(b, lane);
+        }
+        {   // dv: dV's upper plane, token by token
+            const int tok = tid / 4, j0 = 32 * (tid % 4);
+            const uint8_t* src = sm + O_V + (tok / 8) * U_SBO + (tok % 8) * 2;
+            __nv_bfloat16* out = p.dv + ((int64_t)(t0 + tok) * p.HV + hv) * D + j0;
+            if (tok < nv)
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint8_t* a = src + (j0 + i + 2 * e) * 16;
+                        w[e] = *reinterpret_cast<const uint16_t*>(a) | ((uint32_t)*reinterpret_cast<const uint16_t*>(a + 16) << 16);
+                    }
+                    *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
         }
         fence_smem_to_async();                        // the next loads write where these threads did
         fence_before_sync();
@@ -855,6 +863,8 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             p.dg[at] = nan;
             p.dbeta[at] = nan;
         }
+        for (int e = tid; e < nv * group * D; e += LNT)
+            p.dv[((int64_t)(t0 + e / (group * D)) * p.HV + hk * group) * D + e % (group * D)] = nan;
     }
 }
 
@@ -913,7 +923,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     if (e != cudaSuccess) return e;
     const size_t units = (size_t)slot_count(a.seqs) * HV;
     const size_t u_bytes = (size_t)tokens * HV * D * 2, qk_bytes = (size_t)tokens * HK * D * 2;
-    size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE) + 3 * u_bytes;
+    size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE + 4 * (size_t)UPLANE);
     if (scales) bytes += 2 * qk_bytes + u_bytes;
     uint8_t* ws = nullptr;
     keep_pool_memory();
@@ -924,10 +934,8 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     a.rec = take(units * REC_BYTES);
     a.S0 = take(units * 2 * PLANE);
     a.dS1 = take(units * 2 * PLANE);
-    a.u[0] = (__nv_bfloat16*)take(u_bytes);
-    a.u[1] = (__nv_bfloat16*)take(u_bytes);
-    a.dv[0] = (__nv_bfloat16*)dv;
-    a.dv[1] = (__nv_bfloat16*)take(u_bytes);
+    a.u = take(units * 2 * UPLANE);
+    a.dv = take(units * 2 * UPLANE);
     if (scales) {
         void* out[3] = {take(qk_bytes), take(qk_bytes), take(u_bytes)};
         const void* src[3] = {q, k, v};
@@ -950,6 +958,9 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     l.rec = a.rec;
     l.S0 = a.S0;
     l.dS1 = a.dS1;
+    l.u = a.u;
+    l.dvp = a.dv;
+    l.dv = (__nv_bfloat16*)dv;
     l.dq = (__nv_bfloat16*)dq;
     l.dk = (__nv_bfloat16*)dk;
     l.dg = (__nv_bfloat16*)dg;
@@ -964,9 +975,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     const int64_t row = (int64_t)HV * D;
     if (e == cudaSuccess &&
         (!make_token_map(&maps.q, q, tokens, (int64_t)HK * D, q_stride) || !make_token_map(&maps.k, k, tokens, (int64_t)HK * D, k_stride) ||
-         !make_token_map(&mv, v, tokens, row, v_stride) || !make_token_map(&maps.dO, dO, tokens, row, row) ||
-         !make_token_map(&maps.dv, a.dv[0], tokens, row, row) || !make_token_map(&maps.dvl, a.dv[1], tokens, row, row) ||
-         !make_token_map(&maps.u, a.u[0], tokens, row, row) || !make_token_map(&maps.ul, a.u[1], tokens, row, row)))
+         !make_token_map(&mv, v, tokens, row, v_stride) || !make_token_map(&maps.dO, dO, tokens, row, row)))
         e = cudaErrorInvalidValue;
     if (e == cudaSuccess && cu) {
         const int64_t rows[5] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D, HV, HV};

@@ -98,38 +98,42 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// K steps of one product by a converged warp (one elected lane issues;
-// inlined, so that the descriptors stay warp-uniform).  A from tensor memory
-// (8 columns per step) or shared memory, B from shared memory; the steps are in
-// descriptor units (16 bytes).
-__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
+// Four K steps of one product by a converged warp (one elected lane issues).
+// A from tensor memory (8 columns per step) or shared memory, B from shared
+// memory; the steps are in descriptor units (16 bytes) and change a
+// descriptor's lower word only.  Issuing is close to what bounds the chains, so
+// it is kept to few instructions: warp-uniform operands, one election for four.
+template <uint32_t B_STEP>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %5, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u64 b1, %2, %3;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, q;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n\t}\n"
-        :: "r"(d), "r"(a), "l"(b), "l"(b_step), "r"(idesc), "r"(more) : "memory");
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 l, h;\n\t.reg .b64 b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %7, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 {l, h}, %5;\n\t"
+        "add.u32 l, l, %8;\n\tmov.b64 b1, {l, h};\n\tadd.u32 l, l, %8;\n\tmov.b64 b2, {l, h};\n\t"
+        "add.u32 l, l, %8;\n\tmov.b64 b3, {l, h};\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %5, %6, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], b1, %6, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], b2, %6, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], b3, %6, t;\n\t}\n"
+        :: "r"(d), "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "r"(idesc), "r"(more), "n"(B_STEP) : "memory");
 }
-__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint64_t b_step, uint32_t idesc, uint32_t more)
-{
-    mma2_ts(d, a, b, b_step, idesc, more);
-    mma2_ts(d, a + 16, b + 2 * b_step, b_step, idesc, 1u);
-}
-__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t a_step, uint64_t b, uint64_t b_step, uint32_t idesc,
-                                     uint32_t more)
+template <uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more)
 {
     asm volatile(
-        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-        "add.u64 a1, %1, %2;\n\tadd.u64 a2, a1, %2;\n\tadd.u64 a3, a2, %2;\n\t"
-        "add.u64 b1, %3, %4;\n\tadd.u64 b2, b1, %4;\n\tadd.u64 b3, b2, %4;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %3, %5, q;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n\t"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n\t}\n"
-        :: "r"(d), "l"(a), "l"(a_step), "l"(b), "l"(b_step), "r"(idesc), "r"(more) : "memory");
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b32 l, h, m, g;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "mov.b64 {l, h}, %2;\n\tmov.b64 {m, g}, %1;\n\t"
+        "add.u32 l, l, %6;\n\tmov.b64 b1, {l, h};\n\tadd.u32 l, l, %6;\n\tmov.b64 b2, {l, h};\n\t"
+        "add.u32 l, l, %6;\n\tmov.b64 b3, {l, h};\n\t"
+        "add.u32 m, m, %5;\n\tmov.b64 a1, {m, g};\n\tadd.u32 m, m, %5;\n\tmov.b64 a2, {m, g};\n\t"
+        "add.u32 m, m, %5;\n\tmov.b64 a3, {m, g};\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}\n"
+        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(more), "n"(A_STEP), "n"(B_STEP) : "memory");
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int x, int y, uint32_t mbar)
@@ -187,7 +191,9 @@ __device__ __forceinline__ void split_bf16(float a, float b, float& hi, float& l
     lo = __uint_as_float(pack_bf16(r.x, r.y));
 }
 
-// A bounded wait of one role.  Once any wait of the CTA has expired, every
+// A bounded wait of one role.  All lanes of a warp poll with try_wait, which
+// suspends them: polling by one lane, or with test_wait, made the forward's
+// chain 1.4 to 2.5 times slower.  Once any wait of the CTA has expired, every
 // later one returns at once: the roles run to their ends without issuing.
 struct Waits {
     volatile int* abort;
@@ -201,12 +207,14 @@ struct Waits {
     __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
     {
         if (ns == 0 && tc::mbar_test_wait(bar, parity)) return true;
-        const uint64_t t0 = tc::globaltimer_ns();
+        // by the SM's clock (2 cycles per ns at most): reading the global timer takes about as long as its 1 us step,
+        // and every wait of the chain would end that much later
+        const long long t0 = clock64();
         while (ns != 0 && !*abort) {
 #pragma unroll 1
             for (int i = 0; i < 64; ++i)              // each try may itself block for a while
                 if (tc::mbar_try_wait(bar, parity)) return true;
-            if (tc::globaltimer_ns() - t0 > ns) break;
+            if ((uint64_t)(clock64() - t0) > 2 * ns) break;
         }
         *abort = 1;
         atomicExch(status, (int)KDA_ERR_TIMEOUT);
@@ -221,9 +229,16 @@ __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t byt
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" :: "l"(dst), "r"(src), "r"(bytes) : "memory");
 }
 
-// Host: bf16 [tokens][cols] with a row stride in elements, boxes of 64 rows by
-// 64 columns with the 128-byte swizzle.
-bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride);
+__device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                 :: "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(src) : "memory");
+}
+
+// Host: bf16 [tokens][cols] with a row stride in elements; boxes of 64 rows by
+// 64 columns with the 128-byte swizzle (loads), or of 32 rows by 128 columns
+// without (stores).
+bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, bool store = false);
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
                         uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream);

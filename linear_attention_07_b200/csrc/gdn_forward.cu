@@ -16,17 +16,17 @@
 //   warps 0-15  chain: thread (j, part) holds S[dk][j] for 16 + 16 values of
 //               dk and takes 16 of the chunk's tokens; eta U, the state
 //               update, and their split into bf16 pairs
-//   warps 16-19 output: thread j takes O^T's row j, 64 tokens, off the
-//               chain's path
+//   warps 16-19 output: thread j takes O^T's row j, 64 tokens, through
+//               shared memory to tensor stores, off the chain's path
 //   warp 20     issues every MMA
 //   warp 21     loads: K, Q, V (128-byte swizzle), W and T into two stages, P
 //               into one buffer, the gates into four slots; prefetches to L2
 // The chain waits for two products in turn (W S, K^T U) and converts between
 // them; splitting fp32 values into bf16 pairs is most of what the SM issues.
 // What the chain does not wait for (T V, X_Q, O) is issued where the tensor
-// cores would be idle.  The tokens go in two halves of 32 and the state in two
-// halves of d_k, one behind the other, so that a product runs on one half
-// while the other is converted.
+// cores would be idle.  The state goes in two halves of d_k, so that a product
+// runs on one while the other is converted (halves of the tokens gain nothing:
+// an MMA of N = 32 takes as long as one of N = 64).
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -48,14 +48,15 @@ constexpr uint32_t STAGE = S_REC + REC_NGAM;
 static_assert(STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 constexpr uint32_t S_P = STAGES * STAGE;             // P, one buffer
 constexpr uint32_t S_GATE = S_P + P_BYTES;           // the gates, which the output warps read later than the rest
-constexpr uint32_t SMEM = S_GATE + GATE_SLOTS * GATE_BYTES + 1024;
+constexpr uint32_t S_OUT = S_GATE + GATE_SLOTS * GATE_BYTES;   // o staging [32][128] bf16
+constexpr uint32_t SMEM = S_OUT + 32 * D * 2 + 1024;
 
 // barriers (a pair where the work goes in halves)
 // A wait by parity may not fall two completions behind: the gates, whose
 // readers may still be at chunk c while the stage takes chunk c + 2, have
 // barriers of their own.
-enum { B_FULL = 0, B_GATE = STAGES, B_P = B_GATE + GATE_SLOTS, B_MU, B_MD = B_MU + 2, B_MO = B_MD + 2,
-       B_S, B_U = B_S + 2, B_OFREE = B_U + 2, B_DRAIN, N_BAR };
+enum { B_FULL = 0, B_GATE = STAGES, B_MU = B_GATE + GATE_SLOTS, B_MD, B_MO = B_MD + 2, B_S, B_U = B_S + 2, B_OFREE,
+       B_DRAIN, N_BAR };
 
 // tensor memory columns
 constexpr uint32_t T_SH = 0, T_SL = 64;              // S^T, upper and lower half: two d_k per column
@@ -79,7 +80,8 @@ struct Args {
 
 __global__ void __launch_bounds__(fw::NT, 1)
 forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-               const __grid_constant__ CUtensorMap mv, const __grid_constant__ fw::Args p)
+               const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+               const __grid_constant__ fw::Args p)
 {
     using namespace fw;
     using namespace tc;
@@ -100,8 +102,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b >= B_S && b < B_S + 2 ? N_CHAIN
-                            : b >= B_U && b < B_U + 2 ? N_CHAIN / 2 : b == B_OFREE ? N_OUT : 1;
+            const int count = b == B_S || b == B_S + 1 ? N_CHAIN : b == B_U ? N_CHAIN + 1 : b == B_OFREE ? N_OUT : 1;
             mbar_init(bar(b), count);
         }
         fence_mbar_init();
@@ -114,11 +115,11 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    const uint32_t tm = s_tmem;
+    constexpr uint32_t tm = 0;                       // all of tensor memory is this CTA's
     const Waits wait = {&s_abort, &g_fwd_status, p.wait_ns};
 
     if (warp < N_CHAIN) {
-        const int sp = warp & 3, part = warp >> 2, th = part >> 1, j = 32 * sp + lane;
+        const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
         const float* h = p.h0 && row >= 0 ? p.h0 + ((int64_t)row * p.HV + hv) * D * D + j : nullptr;
@@ -157,7 +158,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
             float x[16];
-            wait(bar(B_MU + th), c & 1);
+            wait(bar(B_MU), c & 1);
             fence_after_sync();
             tmem_ld16(t + T_U + 16 * part, x);
             wait_ld();
@@ -168,7 +169,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
             }
             put(T_UH, T_UL, x);
-            give(B_U + th);
+            give(B_U);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 wait(bar(B_MD + b), c & 1);
@@ -197,17 +198,17 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        const int64_t step = (int64_t)p.HV * D;
-        __nv_bfloat16* out = p.o + (int64_t)begin * step + hv * D + j;
+        const int ot = tid - 32 * N_CHAIN;
+        __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             const float2* gq = reinterpret_cast<const float2*>(sm + S_GATE + (c % GATE_SLOTS) * GATE_BYTES + (REC_GQ - REC_NGAM));
-            int left = end - begin - c * C;          // rows behind the sequence are not stored
             wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1);
             wait(bar(B_MO), c & 1);
             fence_after_sync();
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
+                const int t0 = begin + c * C + 32 * q;
                 float x[32], y[32];
                 tmem_ld32(t + T_XQ + 32 * q, x);
                 tmem_ld32(t + T_O + 32 * q, y);
@@ -217,20 +218,35 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_OFREE));
                 }
-                // a warp's store is 64 bytes of one row: two whole sectors
+                if (ot == 0) bulk_wait_read_all();    // the staging's last store has read it
+                asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
                     const float2 v = fma2(gq[16 * q + i / 2], make_float2(x[i], x[i + 1]), make_float2(y[i], y[i + 1]));
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
-                    if (i < left) out[0] = b2.x;
-                    if (i + 1 < left) out[step] = b2.y;
-                    out += 2 * step;
+                    so[i * D + j] = b2.x;
+                    so[(i + 1) * D + j] = b2.y;
                 }
-                left -= 32;
+                fence_smem_to_async();
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (t0 + 32 <= end) {
+                    if (ot == 0) {
+                        tma_store_2d(&mo, hv * D, t0, smem_u32(so));
+                        bulk_commit();
+                    }
+                } else {                             // rows behind the sequence are not stored
+                    for (int e = ot; e < 32 * D / 8; e += 128) {
+                        const int r = e / (D / 8), c8 = e % (D / 8);
+                        if (t0 + r < end)
+                            *reinterpret_cast<uint4*>(p.o + ((int64_t)(t0 + r) * p.HV + hv) * D + 8 * c8) =
+                                *reinterpret_cast<const uint4*>(so + r * D + 8 * c8);
+                    }
+                }
             }
         }
+        if (ot == 0) bulk_wait_all();
     } else if (warp == W_MMA) {
-        const uint32_t id_n64 = idesc_bf16(128, 64), id_n32 = idesc_bf16(128, 32), id_d = idesc_bf16(128, 64, false, true);
+        const uint32_t id_n64 = idesc_bf16(128, 64), id_d = idesc_bf16(128, 64, false, true);
         const uint32_t id_v = idesc_bf16(128, 64, true);
         auto ok = [&](int b, uint32_t parity) {       // every lane sees the same outcome
             const bool w = wait(bar(b), parity);
@@ -252,8 +268,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
             const uint32_t base = smem_u32(st);
             const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
-            mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TH, 128, 1024), 16, id_v, 0u);
-            mma4_ss(tm + T_U, vd, 128, sdesc(base + S_REC + REC_TL, 128, 1024), 16, id_v, 1u);
+            mma4_ss<128, 16>(tm + T_U, vd, sdesc(base + S_REC + REC_TH, 128, 1024), id_v, 0u);
+            mma4_ss<128, 16>(tm + T_U, vd, sdesc(base + S_REC + REC_TL, 128, 1024), id_v, 1u);
             return true;
         };
         if (chunks > 0) begin_chunk(0);
@@ -261,53 +277,43 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         for (int c = 0; c < chunks; ++c) {
             const uint32_t base = smem_u32(sm + (c & 1) * STAGE);
             const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
-            // -(W S)^T over half b of d_k, tokens from tok0 (32 or, by idesc, all 64)
-            auto w_product = [&](int b, int tok0, uint32_t id) {
-                const uint64_t h = wd + (uint64_t)(b * (BOX >> 4) + tok0 * 8), l = h + (uint64_t)(2 * BOX >> 4);
-                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, h, 2, id, 1u);
-                mma4_ts(tm + T_U + tok0, tm + T_SL + 32 * b, h, 2, id, 1u);
-                mma4_ts(tm + T_U + tok0, tm + T_SH + 32 * b, l, 2, id, 1u);
-            };
-            // (K^T eta U)^T, half b of d_k from the tokens of half k
-            auto d_product = [&](int b, int k) {
-                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4) + k * 256);
-                mma2_ts(tm + T_D + 64 * b, tm + T_UH + 16 * k, kd, 128, id_d, k > 0 ? 1u : 0u);
-                mma2_ts(tm + T_D + 64 * b, tm + T_UL + 16 * k, kd, 128, id_d, 1u);
+            auto w_product = [&](int b) {             // -(W S)^T over half b of d_k
+                const uint64_t h = wd + (uint64_t)(b * (BOX >> 4)), l = h + (uint64_t)(2 * BOX >> 4);
+                mma4_ts<2>(tm + T_U, tm + T_SH + 32 * b, h, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_SL + 32 * b, h, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_SH + 32 * b, l, id_n64, 1u);
             };
             if (!ok(B_S, c & 1)) break;
             fence_after_sync();
-            w_product(0, 0, id_n64);
+            w_product(0);
             if (!ok(B_S + 1, c & 1)) break;
             fence_after_sync();
-            w_product(1, 0, id_n32);
+            w_product(1);
             mma_commit_w(bar(B_MU));
-            w_product(1, 32, id_n32);
-            mma_commit_w(bar(B_MU + 1));
             if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
             fence_after_sync();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {             // (Q S)^T, before a new state replaces the old one
                 const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
-                mma4_ts(tm + T_XQ, tm + T_SH + 32 * b, qd, 2, id_n64, b > 0 ? 1u : 0u);
-                mma4_ts(tm + T_XQ, tm + T_SL + 32 * b, qd, 2, id_n64, 1u);
+                mma4_ts<2>(tm + T_XQ, tm + T_SH + 32 * b, qd, id_n64, b > 0 ? 1u : 0u);
+                mma4_ts<2>(tm + T_XQ, tm + T_SL + 32 * b, qd, id_n64, 1u);
             }
-            if (!ok(B_U, c & 1)) break;
+            if (!ok(B_U, c & 1)) break;               // eta U, and P has landed
             fence_after_sync();
-            d_product(0, 0);
-            d_product(1, 0);
-            if (!ok(B_U + 1, c & 1)) break;
-            fence_after_sync();
-            d_product(0, 1);
-            mma_commit_w(bar(B_MD));
-            d_product(1, 1);
-            mma_commit_w(bar(B_MD + 1));
-            if (!ok(B_P, c & 1)) break;
-            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
-            mma4_ts(tm + T_O, tm + T_UH, ph, 16, id_n64, 0u);
-            mma4_ts(tm + T_O, tm + T_UL, ph, 16, id_n64, 1u);
-            mma4_ts(tm + T_O, tm + T_UH, pl, 16, id_n64, 1u);
-            mma_commit_w(bar(B_MO));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {             // (K^T eta U)^T, half b of d_k
+                const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, kd, id_d, 0u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UL, kd, id_d, 1u);
+                mma_commit_w(bar(B_MD + b));
+            }
+            // T_U is free: the next chunk's U^T = V^T T^T
             if (c + 1 < chunks && !begin_chunk(c + 1)) break;
+            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
+            mma4_ts<16>(tm + T_O, tm + T_UH, ph, id_n64, 0u);
+            mma4_ts<16>(tm + T_O, tm + T_UL, ph, id_n64, 1u);
+            mma4_ts<16>(tm + T_O, tm + T_UH, pl, id_n64, 1u);
+            mma_commit_w(bar(B_MO));
         }
         if (chunks > 0) {                             // what was issued ends before its memory goes
             mma_commit_w(bar(B_DRAIN));
@@ -324,8 +330,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             if (c >= 2 && !wait(bar(B_MO), c & 1)) break;
             if (*(volatile int*)&s_abort) break;
             auto load_p = [&](int cp) {
-                mbar_arrive_expect_tx(bar(B_P), P_BYTES);
-                bulk_load(smem_u32(sm + S_P), rec + cp * rec_step + REC_PH, P_BYTES, bar(B_P));
+                mbar_arrive_expect_tx(bar(B_U), P_BYTES);    // one of the arrivals that chunk cp's U waits for
+                bulk_load(smem_u32(sm + S_P), rec + cp * rec_step + REC_PH, P_BYTES, bar(B_U));
                 loaded_p = cp + 1;
             };
             if (c >= 2) load_p(c - 1);
@@ -359,8 +365,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             }
         }
         if (loaded == chunks && chunks > 1 && wait(bar(B_MO), chunks & 1)) {     // the last chunk's P
-            mbar_arrive_expect_tx(bar(B_P), P_BYTES);
-            bulk_load(smem_u32(sm + S_P), rec + (chunks - 1) * rec_step + REC_PH, P_BYTES, bar(B_P));
+            mbar_arrive_expect_tx(bar(B_U), P_BYTES);
+            bulk_load(smem_u32(sm + S_P), rec + (chunks - 1) * rec_step + REC_PH, P_BYTES, bar(B_U));
             loaded_p = chunks;
         }
         // everything loaded has landed before the end
@@ -368,13 +374,13 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_wait(bar(B_FULL + (c & 1)), (c >> 1) & 1, DRAIN_NS);
         for (int c = max(0, loaded - GATE_SLOTS); c < loaded; ++c)
             mbar_wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1, DRAIN_NS);
-        if (loaded_p > 0) mbar_wait(bar(B_P), (loaded_p - 1) & 1, DRAIN_NS);
+        if (loaded_p > 0) mbar_wait(bar(B_U), (loaded_p - 1) & 1, DRAIN_NS);
     }
     fence_before_sync();
     __syncthreads();
     if (warp == W_MMA) {
         fence_after_sync();
-        tmem_dealloc(tm, 512);
+        tmem_dealloc(s_tmem, 512);
     }
     if (s_abort) {             // a wait expired: no partial result passes for a real one
         const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7fc00000));
@@ -413,13 +419,14 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         return cudaFuncSetAttribute(forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fw::SMEM);
     });
     if (e != cudaSuccess) return e;
-    CUtensorMap mq = {}, mk = {}, mv = {};
+    CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
     uint8_t* rec = nullptr;
     const int64_t tokens = a.seqs.tokens;
     if (tokens > 0) {
         if (!make_token_map(&mq, q, tokens, (int64_t)HK * D, q_stride) ||
             !make_token_map(&mk, k, tokens, (int64_t)HK * D, k_stride) ||
-            !make_token_map(&mv, v, tokens, (int64_t)HV * D, v_stride))
+            !make_token_map(&mv, v, tokens, (int64_t)HV * D, v_stride) ||
+            !make_token_map(&mo, o, tokens, (int64_t)HV * D, (int64_t)HV * D, true))
             return cudaErrorInvalidValue;
         keep_pool_memory();
         e = cudaMallocAsync(reinterpret_cast<void**>(&rec), (size_t)slot_count(a.seqs) * HV * REC_BYTES, stream);
@@ -428,7 +435,7 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
     }
     a.rec = rec;
     if (e == cudaSuccess) {
-        forward_kernel<<<(unsigned)((int64_t)N * HV), fw::NT, fw::SMEM, stream>>>(mq, mk, mv, a);
+        forward_kernel<<<(unsigned)((int64_t)N * HV), fw::NT, fw::SMEM, stream>>>(mq, mk, mv, mo, a);
         note_launches(1);
         e = cudaGetLastError();
     }

@@ -208,10 +208,10 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             // of either left operand are the neighbouring boxes, their results are not read
             constexpr uint32_t id = idesc_bf16(128, C);
             const uint64_t k0 = sdesc_sw128(tile), k1 = sdesc_sw128(tile + BOX), q0 = sdesc_sw128(tile + 2 * BOX);
-            mma4_ss(tm, k0, 2, k0, 2, id, 0u);
-            mma4_ss(tm, k1, 2, k1, 2, id, 1u);
-            mma4_ss(tm + C, k1, 2, k0, 2, id, 0u);
-            mma4_ss(tm + C, q0, 2, k1, 2, id, 1u);
+            mma4_ss<2, 2>(tm, k0, k0, id, 0u);
+            mma4_ss<2, 2>(tm, k1, k1, id, 1u);
+            mma4_ss<2, 2>(tm + C, k1, k0, id, 0u);
+            mma4_ss<2, 2>(tm + C, q0, k1, id, 1u);
             mma_commit_w(done);
             if (!wait(done, 0)) mbar_wait(done, 0, DRAIN_NS);
             issued = true;
@@ -336,8 +336,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         if (issued) {
             constexpr uint32_t id = idesc_bf16(128, C, true);
             const uint64_t kd = (sdesc_sw128(tile) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
-            mma4_ss(tm, kd, 128, sdesc(tile + A_OFF, 128, 1024), 16, id, 0u);
-            mma4_ss(tm, kd, 128, sdesc(tile + A_OFF + BOX, 128, 1024), 16, id, 1u);
+            mma4_ss<128, 16>(tm, kd, sdesc(tile + A_OFF, 128, 1024), id, 0u);
+            mma4_ss<128, 16>(tm, kd, sdesc(tile + A_OFF + BOX, 128, 1024), id, 1u);
             mma_commit_w(done);
             if (!wait(done, 1)) mbar_wait(done, 1, DRAIN_NS);
         }
@@ -379,7 +379,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
 }
 
-bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride)
+bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, bool store)
 {
     typedef CUresult (*encode_fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -395,10 +395,10 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
     if (!encode) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)tokens};
     const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)C};
+    const cuuint32_t box[2] = {store ? 128u : 64u, store ? 32u : (cuuint32_t)C};
     const cuuint32_t estr[2] = {1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, store ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -272,7 +272,7 @@ def test_forward_bad_offsets_are_contained():
     torch.cuda.synchronize()
     assert kda.device_status() == kda.KDA_OK
     ro, _ = reference([t[:30] for t in x], [30])
-    assert rel(o[0, :30], ro) <= TOL_O               # the one sequence that is whole
+    assert rel(o[0, :20], ro[:20]) <= TOL_O          # tokens 20-29 are in [0, 30) and [20, 70): either may be there
 
 
 @pytest.mark.gpu
