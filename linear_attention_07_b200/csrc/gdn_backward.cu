@@ -68,12 +68,14 @@ constexpr uint32_t SMEM = S_P + P_BYTES + 1024;
 enum { B_FULL = 0, B_FREE = STAGES, B_P = 2 * STAGES, B_MU, B_MD, B_MV = B_MD + 2, B_S = B_MV + 2, B_U = B_S + 2, B_DO,
        B_OFREE, B_DRAIN = B_OFREE + 2, N_BAR };
 
-constexpr uint32_t T_SH = 0, T_SL = 64;
+// operands by 16 values: 8 columns of the upper plane (two values each), 8 of the lower
+constexpr uint32_t LOWER = 8;
+constexpr uint32_t T_S = 0;
 constexpr uint32_t T_U = 128;                        // forward: U^T, by chunk parity here or in T_U2; reverse: (K dS1)^T, then dV^T
 constexpr uint32_t T_U2 = 256;
-constexpr uint32_t T_UH = 192, T_UL = 224;           // forward: (eta U)^T; reverse: dU^T
+constexpr uint32_t T_UE = 192;                       // forward: (eta U)^T; reverse: dU^T
 constexpr uint32_t T_PO = 256;                       // reverse: (P^T dO)^T
-constexpr uint32_t T_OH = 320, T_OL = 352;           // reverse: (gam dO~)^T
+constexpr uint32_t T_OG = 320;                       // reverse: (gam dO~)^T
 constexpr uint32_t T_D = 384;
 
 struct Args {
@@ -129,17 +131,14 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
         // the state's half b: operand of the next chunk, and for the local kernel
         uint8_t* dst0 = (REV ? p.dS1 : p.S0) + (slot0 * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF + 2 * part * ST_SBO + (j % 64) * 16;
         auto give_state = [&](int b, int c) {
-            float hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split_bf16(S[b][2 * i], S[b][2 * i + 1], hi[i], lo[i]);
-            tmem_st8(t + T_SH + 32 * b + 8 * part, hi);
-            tmem_st8(t + T_SL + 32 * b + 8 * part, lo);
+            float w[16];
+            tmem_put16(t + T_S + 64 * b + 16 * part, S[b], w);
             give(B_S + b);
             uint8_t* dst = dst0 + chunk_at(c) * (int64_t)p.HV * (2 * (int64_t)PLANE) + 8 * b * ST_SBO;
-            *reinterpret_cast<float4*>(dst) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<float4*>(dst + ST_SBO) = make_float4(hi[4], hi[5], hi[6], hi[7]);
-            *reinterpret_cast<float4*>(dst + PLANE) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-            *reinterpret_cast<float4*>(dst + PLANE + ST_SBO) = make_float4(lo[4], lo[5], lo[6], lo[7]);
+            *reinterpret_cast<float4*>(dst) = make_float4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<float4*>(dst + ST_SBO) = make_float4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<float4*>(dst + PLANE) = make_float4(w[8], w[9], w[10], w[11]);
+            *reinterpret_cast<float4*>(dst + PLANE + ST_SBO) = make_float4(w[12], w[13], w[14], w[15]);
         };
         if (chunks > 0) {
             give_state(0, 0);
@@ -155,6 +154,18 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll
             for (int i = 0; i < 4; ++i) eta[i] = reinterpret_cast<const float4*>(gates + C + 16 * part)[i];
             float x[16];
+            if constexpr (REV) {                     // gam dO~ as an operand, while K dS1 is computed
+                const uint8_t* box = sm + s * STAGE + S_V + (j / 64) * BOX + (j % 8) * 2;
+                const int piece = (j % 64) / 8, left = end - begin - chunk_at(c) * C - 16 * part;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float d = to_f32(*reinterpret_cast<const __nv_bfloat16*>(box + (16 * part + i) * 128 + ((piece ^ (i & 7)) * 16)));
+                    x[i] = i < left ? gates[2 * C + 16 * part + i] * d : 0.f;
+                }
+                float w[16];
+                tmem_put16(t + T_OG + 16 * part, x, w);
+                give(B_DO);
+            }
             wait(bar(B_MU), c & 1);                  // U, or K dS1 and P^T dO
             fence_after_sync();
             tmem_ld16(t + u_cols(c) + 16 * part, x);
@@ -178,11 +189,8 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 }
             }
             {
-                float hi[8], lo[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
-                tmem_st8(t + T_UH + 8 * part, hi);
-                tmem_st8(t + T_UL + 8 * part, lo);
+                float w[16];
+                tmem_put16(t + T_UE + 16 * part, x, w);
             }
             give(B_U);
 #pragma unroll
@@ -212,36 +220,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
-            const int s = c & 1, nv = min(C, end - begin - chunk_at(c) * C);
-            if constexpr (REV) {                     // gam dO~ as an operand; the previous one has been read
-                wait(bar(B_FULL + s), (c >> 1) & 1);
-                if (c > 0) wait(bar(B_MD + 1), (c - 1) & 1);
-                fence_after_sync();
-                const uint8_t* box = sm + s * STAGE + S_V + (j / 64) * BOX + (j % 8) * 2;
-                const float* gq = reinterpret_cast<const float*>(sm + s * STAGE + S_REC + REC_GQ);
-                const int piece = (j % 64) / 8;
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    float hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float x[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int r = 16 * q + 2 * i + e;
-                            const float d = to_f32(*reinterpret_cast<const __nv_bfloat16*>(box + r * 128 + ((piece ^ (r & 7)) * 16)));
-                            x[e] = r < nv ? gq[r] * d : 0.f;
-                        }
-                        split_bf16(x[0], x[1], hi[i], lo[i]);
-                    }
-                    tmem_st8(t + T_OH + 8 * q, hi);
-                    tmem_st8(t + T_OL + 8 * q, lo);
-                }
-                wait_st();
-                fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_DO));
-            }
+            const int s = c & 1;
             wait(bar(B_MV + s), (c >> 1) & 1);
             fence_after_sync();
             uint8_t* out = (REV ? p.dv : p.u) + ((slot0 + chunk_at(c)) * p.HV + hv) * (2 * (int64_t)UPLANE) + j * 16;
@@ -312,9 +291,9 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             auto s_product = [&](int b) {
                 const uint64_t h = REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4));
                 const uint32_t u = tm + u_cols(c);
-                mma4_ts<2>(u, tm + T_SH + 32 * b, h, id_n64, REV && b == 0 ? 0u : 1u);
-                mma4_ts<2>(u, tm + T_SL + 32 * b, h, id_n64, 1u);
-                if (!REV) mma4_ts<2>(u, tm + T_SH + 32 * b, h + LO, id_n64, 1u);
+                mma4_ts<2>(u, tm + T_S + 64 * b, h, id_n64, REV && b == 0 ? 0u : 1u);
+                mma4_ts<2>(u, tm + T_S + 64 * b + LOWER, h, id_n64, 1u);
+                if (!REV) mma4_ts<2>(u, tm + T_S + 64 * b, h + LO, id_n64, 1u);
             };
             if (REV && c > 0 && !ok(B_OFREE + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
             if (!ok(B_S, c & 1)) break;
@@ -331,8 +310,8 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {        // Q^T (gam dO~), while the chain computes dU
                     const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
-                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OH, qd, id_bmn, 0u);
-                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OL, qd, id_bmn, 1u);
+                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OG, qd, id_bmn, 0u);
+                    mma4_ts<128>(tm + T_D + 64 * b, tm + T_OG + LOWER, qd, id_bmn, 1u);
                 }
             }
             if (!ok(B_U, c & 1)) break;
@@ -340,16 +319,16 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
 #pragma unroll
             for (int b = 0; b < 2; ++b) {            // forward: (K^T eta U)^T; reverse: -(W^T dU)^T; half b of d_k
                 const uint64_t h = REV ? wd + (uint64_t)(b * (BOX >> 4)) : kq + (uint64_t)(2 * b * (BOX >> 4));
-                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, h, id_bmn, REV ? 1u : 0u);
-                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UL, h, id_bmn, 1u);
-                if (REV) mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, h + LO, id_bmn, 1u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE, h, id_bmn, REV ? 1u : 0u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE + LOWER, h, id_bmn, 1u);
+                if (REV) mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE, h + LO, id_bmn, 1u);
                 mma_commit_w(bar(B_MD + b));
             }
             if constexpr (REV) {                     // dV^T = dU^T T
                 const uint64_t th = sdesc(base + S_REC + REC_TH, 1024, 128), tl = th + (uint64_t)(BOX >> 4);
-                mma4_ts<128>(tm + T_U, tm + T_UH, th, id_bmn, 0u);
-                mma4_ts<128>(tm + T_U, tm + T_UL, th, id_bmn, 1u);
-                mma4_ts<128>(tm + T_U, tm + T_UH, tl, id_bmn, 1u);
+                mma4_ts<128>(tm + T_U, tm + T_UE, th, id_bmn, 0u);
+                mma4_ts<128>(tm + T_U, tm + T_UE + LOWER, th, id_bmn, 1u);
+                mma4_ts<128>(tm + T_U, tm + T_UE, tl, id_bmn, 1u);
                 mma_commit_w(bar(B_MV + (c & 1)));
             }
             mma_commit_w(bar(B_FREE + (c & 1)));
@@ -419,7 +398,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     const int hv = (blockIdx.x >> 1) % p.HV, n = (blockIdx.x >> 1) / p.HV;
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
-            const int count = b == B_S || b == B_S + 1 || b == B_U ? N_CHAIN : b == B_DO || b == B_OFREE || b == B_OFREE + 1 ? N_OUT : 1;
+            const int count = b == B_S || b == B_S + 1 || b == B_U || b == B_DO ? N_CHAIN
+                            : b == B_OFREE || b == B_OFREE + 1 ? N_OUT : 1;
             mbar_init(smem_u32(&bars[b]), count);
         }
         fence_mbar_init();
@@ -687,7 +667,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 for (int e = 0; e < 4; ++e) {
                     const int c = 32 * half + i + e;
                     if (!is_q && c == r) sDB[r] = x[i + e];
-                    x[i + e] = c <= last ? f * exp2f((gh - dh[e]) + (gl - dl[e])) * x[i + e] : 0.f;
+                    x[i + e] = c <= last ? f * exp2_fast((gh - dh[e]) + (gl - dl[e])) * x[i + e] : 0.f;
                     pre = fmaf(x[i + e], c < r ? y[i + e] : 0.f, pre);
                     y[i + e] = c + 1 <= r ? pre : 0.f;           // token t = c + 1: this row's part of sum_{i < t <= r} w_ri
                 }

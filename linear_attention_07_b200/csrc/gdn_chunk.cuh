@@ -99,9 +99,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
 }
 
 // Four K steps of one product by a converged warp (one elected lane issues).
-// A from tensor memory (8 columns per step) or shared memory, B from shared
-// memory; the steps are in descriptor units (16 bytes) and change a
-// descriptor's lower word only.  Issuing is close to what bounds the chains, so
+// A from tensor memory (16 columns per step: 8 of the upper and 8 of the lower
+// plane, written by one store) or shared memory, B from shared memory, its steps
+// in descriptor units (16 bytes), which change a descriptor's lower word only.  Issuing is close to what bounds the chains, so
 // it is kept to few instructions: warp-uniform operands, one election for four.
 template <uint32_t B_STEP>
 __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more)
@@ -116,7 +116,7 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%2], b1, %6, t;\n\t"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], b2, %6, t;\n\t"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%4], b3, %6, t;\n\t}\n"
-        :: "r"(d), "r"(a), "r"(a + 8), "r"(a + 16), "r"(a + 24), "l"(b), "r"(idesc), "r"(more), "n"(B_STEP) : "memory");
+        :: "r"(d), "r"(a), "r"(a + 16), "r"(a + 32), "r"(a + 48), "l"(b), "r"(idesc), "r"(more), "n"(B_STEP) : "memory");
 }
 template <uint32_t A_STEP, uint32_t B_STEP>
 __device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more)
@@ -175,6 +175,13 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return d;
 }
 
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values as packed bf16 pairs hi and lo with x ~ hi + lo (each
 // rounded to nearest: 16 significant bits together).
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -189,6 +196,15 @@ __device__ __forceinline__ void split_bf16(float a, float b, float& hi, float& l
     const float2 r = fma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)), make_float2(-1.f, -1.f),
                           make_float2(a, b));         // exact
     lo = __uint_as_float(pack_bf16(r.x, r.y));
+}
+
+// 16 values of one lane as two planes of an operand in tensor memory: the upper
+// bf16 pairs in columns [0, 8), the lower in [8, 16).
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const float (&x)[16], float (&w)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], w[i], w[8 + i]);
+    tc::tmem_st16(taddr, w);
 }
 
 // A bounded wait of one role.  All lanes of a warp poll with try_wait, which

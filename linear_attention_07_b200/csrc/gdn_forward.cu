@@ -59,9 +59,11 @@ enum { B_FULL = 0, B_GATE = STAGES, B_MU = B_GATE + GATE_SLOTS, B_MD, B_MO = B_M
        B_DRAIN, N_BAR };
 
 // tensor memory columns
-constexpr uint32_t T_SH = 0, T_SL = 64;              // S^T, upper and lower half: two d_k per column
+// operands by 16 values: 8 columns of the upper plane (two values each), 8 of the lower
+constexpr uint32_t LOWER = 8;
+constexpr uint32_t T_S = 0;                          // S^T
 constexpr uint32_t T_U = 128;                        // U^T
-constexpr uint32_t T_UH = 192, T_UL = 224;           // (eta U)^T
+constexpr uint32_t T_UE = 192;                       // (eta U)^T
 constexpr uint32_t T_XQ = 256, T_O = 320;
 constexpr uint32_t T_D = 384;                        // (K^T eta U)^T
 
@@ -127,13 +129,9 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 16 * part + i) * D] : 0.f;
-        // 16 values into the operand columns of this part, two per column
-        auto put = [&](uint32_t hi_col, uint32_t lo_col, const float (&x)[16]) {
-            float hi[8], lo[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) split_bf16(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
-            tmem_st8(t + hi_col + 8 * part, hi);
-            tmem_st8(t + lo_col + 8 * part, lo);
+        auto put = [&](uint32_t col, const float (&x)[16]) {     // this part's 16 values of an operand
+            float w[16];
+            tmem_put16(t + col + 16 * part, x, w);
         };
         auto arrive = [&](int b) {
             __syncwarp();
@@ -146,7 +144,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         };
         if (chunks > 0)
             for (int b = 0; b < 2; ++b) {
-                put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
+                put(T_S + 64 * b, S[b]);
                 give(B_S + b);
             }
 #pragma unroll 1
@@ -168,7 +166,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const float2 b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), make_float2(eta[i].z, eta[i].w));
                 x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
             }
-            put(T_UH, T_UL, x);
+            put(T_UE, x);
             give(B_U);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
@@ -183,7 +181,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     S[b][i + 1] = y.y;
                 }
                 if (c + 1 < chunks) {
-                    put(T_SH + 32 * b, T_SL + 32 * b, S[b]);
+                    put(T_S + 64 * b, S[b]);
                     give(B_S + b);
                 }
             }
@@ -206,18 +204,13 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1);
             wait(bar(B_MO), c & 1);
             fence_after_sync();
+            float x[32], y[32];
+            tmem_ld32(t + T_XQ, x);
+            tmem_ld32(t + T_O, y);
+            wait_ld();
 #pragma unroll 1
             for (int q = 0; q < 2; ++q) {
                 const int t0 = begin + c * C + 32 * q;
-                float x[32], y[32];
-                tmem_ld32(t + T_XQ + 32 * q, x);
-                tmem_ld32(t + T_O + 32 * q, y);
-                wait_ld();
-                if (q == 1) {
-                    fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_OFREE));
-                }
                 if (ot == 0) bulk_wait_read_all();    // the staging's last store has read it
                 asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
@@ -226,6 +219,14 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(v.x, v.y);
                     so[i * D + j] = b2.x;
                     so[(i + 1) * D + j] = b2.y;
+                }
+                if (q == 0) {                        // the second half, so that the next products may begin
+                    tmem_ld32(t + T_XQ + 32, x);
+                    tmem_ld32(t + T_O + 32, y);
+                    wait_ld();
+                    fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_OFREE));
                 }
                 fence_smem_to_async();
                 asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -279,9 +280,9 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
             auto w_product = [&](int b) {             // -(W S)^T over half b of d_k
                 const uint64_t h = wd + (uint64_t)(b * (BOX >> 4)), l = h + (uint64_t)(2 * BOX >> 4);
-                mma4_ts<2>(tm + T_U, tm + T_SH + 32 * b, h, id_n64, 1u);
-                mma4_ts<2>(tm + T_U, tm + T_SL + 32 * b, h, id_n64, 1u);
-                mma4_ts<2>(tm + T_U, tm + T_SH + 32 * b, l, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_S + 64 * b, h, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_S + 64 * b + LOWER, h, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_S + 64 * b, l, id_n64, 1u);
             };
             if (!ok(B_S, c & 1)) break;
             fence_after_sync();
@@ -295,25 +296,25 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
             for (int b = 0; b < 2; ++b) {             // (Q S)^T, before a new state replaces the old one
                 const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
-                mma4_ts<2>(tm + T_XQ, tm + T_SH + 32 * b, qd, id_n64, b > 0 ? 1u : 0u);
-                mma4_ts<2>(tm + T_XQ, tm + T_SL + 32 * b, qd, id_n64, 1u);
+                mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b, qd, id_n64, b > 0 ? 1u : 0u);
+                mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b + LOWER, qd, id_n64, 1u);
             }
             if (!ok(B_U, c & 1)) break;               // eta U, and P has landed
             fence_after_sync();
 #pragma unroll
             for (int b = 0; b < 2; ++b) {             // (K^T eta U)^T, half b of d_k
                 const uint64_t kd = kq + (uint64_t)(2 * b * (BOX >> 4));
-                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UH, kd, id_d, 0u);
-                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UL, kd, id_d, 1u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE, kd, id_d, 0u);
+                mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE + LOWER, kd, id_d, 1u);
                 mma_commit_w(bar(B_MD + b));
             }
+            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
+            mma4_ts<16>(tm + T_O, tm + T_UE, ph, id_n64, 0u);
+            mma4_ts<16>(tm + T_O, tm + T_UE + LOWER, ph, id_n64, 1u);
+            mma4_ts<16>(tm + T_O, tm + T_UE, pl, id_n64, 1u);
+            mma_commit_w(bar(B_MO));
             // T_U is free: the next chunk's U^T = V^T T^T
             if (c + 1 < chunks && !begin_chunk(c + 1)) break;
-            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
-            mma4_ts<16>(tm + T_O, tm + T_UH, ph, id_n64, 0u);
-            mma4_ts<16>(tm + T_O, tm + T_UL, ph, id_n64, 1u);
-            mma4_ts<16>(tm + T_O, tm + T_UH, pl, id_n64, 1u);
-            mma_commit_w(bar(B_MO));
         }
         if (chunks > 0) {                             // what was issued ends before its memory goes
             mma_commit_w(bar(B_DRAIN));

@@ -30,12 +30,6 @@ constexpr uint32_t X_OFF = A_OFF + C * LD * 4;
 constexpr uint32_t SMEM = X_OFF + C * LD * 4 + 1024; // room to align the tiles to 1024 bytes
 static_assert(C * LD * 4 >= 2 * BOX, "T in the place of A");
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 32 columns of row r as pairs of bf16, in the operand layout.
 __device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, int r, int col, const float (&x)[32])
 {
@@ -371,7 +365,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     if (tid == 0) {
         bulk_store(rec + REC_WH, tile, 4 * BOX);
         bulk_commit();
-        bulk_wait_all();
+        bulk_wait_read_all();
     }
     if (warp == 1) {
         fence_after_sync();
