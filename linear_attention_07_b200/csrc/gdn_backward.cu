@@ -128,12 +128,19 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             fence_before_sync();
             arrive(b);
         };
-        // the state's half b: operand of the next chunk, and for the local kernel
-        uint8_t* dst0 = (REV ? p.dS1 : p.S0) + (slot0 * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF + 2 * part * ST_SBO + (j % 64) * 16;
-        auto give_state = [&](int b, int c) {
+        auto give_state = [&](int b) {               // the state's half b: operand of the next chunk
             float w[16];
             tmem_put16(t + T_S + 64 * b + 16 * part, S[b], w);
             give(B_S + b);
+        };
+        // The same words for the local kernel.  An SM stores about 32 bytes a cycle, so that a chunk's 64 KB take as
+        // long as half its chain: each half goes out where the chain would wait for a product, read back from the
+        // operand, which this warp replaces itself.
+        uint8_t* dst0 = (REV ? p.dS1 : p.S0) + (slot0 * p.HV + hv) * (2 * (int64_t)PLANE) + (j / 64) * HALF + 2 * part * ST_SBO + (j % 64) * 16;
+        auto store_state = [&](int b, int c) {
+            float w[16];
+            tmem_ld16(t + T_S + 64 * b + 16 * part, w);
+            wait_ld();
             uint8_t* dst = dst0 + chunk_at(c) * (int64_t)p.HV * (2 * (int64_t)PLANE) + 8 * b * ST_SBO;
             *reinterpret_cast<float4*>(dst) = make_float4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<float4*>(dst + ST_SBO) = make_float4(w[4], w[5], w[6], w[7]);
@@ -141,8 +148,8 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             *reinterpret_cast<float4*>(dst + PLANE + ST_SBO) = make_float4(w[12], w[13], w[14], w[15]);
         };
         if (chunks > 0) {
-            give_state(0, 0);
-            give_state(1, 0);
+            give_state(0);
+            give_state(1);
         }
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
@@ -166,6 +173,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 tmem_put16(t + T_OG + 16 * part, x, w);
                 give(B_DO);
             }
+            store_state(0, c);
             wait(bar(B_MU), c & 1);                  // U, or K dS1 and P^T dO
             fence_after_sync();
             tmem_ld16(t + u_cols(c) + 16 * part, x);
@@ -193,6 +201,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 tmem_put16(t + T_UE + 16 * part, x, w);
             }
             give(B_U);
+            store_state(1, c);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 wait(bar(B_MD + b), c & 1);
@@ -205,7 +214,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                     S[b][i] = y.x;
                     S[b][i + 1] = y.y;
                 }
-                if (c + 1 < chunks) give_state(b, c + 1);
+                if (c + 1 < chunks) give_state(b);
             }
         }
         if (REV && p.dh0) {
