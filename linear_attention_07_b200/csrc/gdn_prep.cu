@@ -20,27 +20,31 @@ __device__ int g_prep_status;
 
 namespace prep {
 constexpr int NT = 128;
-constexpr int LD = C + 4;                            // rows stay 16-byte aligned
-// K and Q rows (boxes of 64 channels: K0 K1 Q0 Q1); A where Q was, and X; then
-// -T diag(gam) as two planes where A was; at the end W's two planes over K and
-// that
-constexpr uint32_t KQ_BYTES = 4 * BOX;
-constexpr uint32_t A_OFF = 2 * BOX;
-constexpr uint32_t X_OFF = A_OFF + C * LD * 4;
-constexpr uint32_t SMEM = X_OFF + C * LD * 4 + 1024; // room to align the tiles to 1024 bytes
-static_assert(C * LD * 4 >= 2 * BOX, "T in the place of A");
+// K and Q rows (boxes of 64 channels: K0 Q0 K1 Q1); then the lower triangle of
+// A, which becomes X in place, where Q was: three blocks of 32 x 32; then
+// -T diag(gam) as two planes there; at the end W's two planes over all of it.
+// No more than that, and 64 columns of tensor memory: six CTAs of an SM hide
+// one another's latency.
+constexpr int BLK = 32 * 32;                         // fp32 values of a block
+constexpr uint32_t B00 = BOX, B10 = BOX + 4 * BLK, B11 = 3 * BOX;
+constexpr uint32_t SMEM = 4 * BOX + 1024;            // room to align the tiles to 1024 bytes
 
-// 32 columns of row r as pairs of bf16, in the operand layout.
-__device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, int r, int col, const float (&x)[32])
+// Element (r, c) of a block: rows of 32, their groups of four columns permuted
+// so that neither rows of a column nor the matrix fragments meet in a bank.
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 1) | ((r >> 2) & 1); }
+__device__ __forceinline__ int at(int r, int c) { return r * 32 + (((c >> 2) ^ swz(r)) << 2) + (c & 3); }
+
+// 16 columns of row r as pairs of bf16, in the operand layout.
+__device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, int r, int col, const float* x)
 {
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < 2; ++p) {
         float hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split_bf16(x[8 * p + 2 * e], x[8 * p + 2 * e + 1], hi[e], lo[e]);
-        const uint32_t at = (r / 8) * 1024 + (col / 8 + p) * 128 + (r % 8) * 16;
-        *reinterpret_cast<float4*>(hi_dst + at) = make_float4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<float4*>(lo_dst + at) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        const uint32_t o = (r / 8) * 1024 + (col / 8 + p) * 128 + (r % 8) * 16;
+        *reinterpret_cast<float4*>(hi_dst + o) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<float4*>(lo_dst + o) = make_float4(lo[0], lo[1], lo[2], lo[3]);
     }
 }
 
@@ -57,9 +61,10 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// (16 MT x 16 MT at m) times (16 MT x 8 at x), both of row stride LD.
+// (16 MT x 16 MT at (mr, mc) of block m) times (16 MT x 8 at (xr, xc) of block x).
 template <int MT>
-__device__ __forceinline__ void block_product(const float* m, const float* x, int lane, float (&d)[MT][4])
+__device__ __forceinline__ void block_product(const float* m, int mr, int mc, const float* x, int xr, int xc, int lane,
+                                              float (&d)[MT][4])
 {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -69,50 +74,50 @@ __device__ __forceinline__ void block_product(const float* m, const float* x, in
 #pragma unroll
     for (int k = 0; k < 2 * MT; ++k) {
         uint32_t bh[2], bl[2];
-        split_tf32(x[(8 * k + t) * LD + g], bh[0], bl[0]);
-        split_tf32(x[(8 * k + t + 4) * LD + g], bh[1], bl[1]);
+        split_tf32(x[at(xr + 8 * k + t, xc + g)], bh[0], bl[0]);
+        split_tf32(x[at(xr + 8 * k + t + 4, xc + g)], bh[1], bl[1]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            const float* a = m + (16 * i + g) * LD + 8 * k + t;
+            const int r = mr + 16 * i + g, c = mc + 8 * k + t;
             uint32_t ah[4], al[4];
-            split_tf32(a[0], ah[0], al[0]);
-            split_tf32(a[8 * LD], ah[1], al[1]);
-            split_tf32(a[4], ah[2], al[2]);
-            split_tf32(a[8 * LD + 4], ah[3], al[3]);
+            split_tf32(m[at(r, c)], ah[0], al[0]);
+            split_tf32(m[at(r, c) + 8 * 32], ah[1], al[1]);
+            split_tf32(m[at(r, c + 4)], ah[2], al[2]);
+            split_tf32(m[at(r, c + 4) + 8 * 32], ah[3], al[3]);
             mma_tf32(d[i], al, bh);
             mma_tf32(d[i], ah, bl);
             mma_tf32(d[i], ah, bh);
         }
     }
 }
-// Columns [col, col + 8) of X10 = -X11 (A10 X00) for the blocks of 16 MT rows at `base`.
 template <int MT>
-__device__ __forceinline__ void join(const float* sA, float* sX, int base, int col, int lane)
+__device__ __forceinline__ void put(float* x, int xr, int xc, int lane, float sign, const float (&d)[MT][4])
 {
-    constexpr int S = 16 * MT;
     const int g = lane >> 2, t = lane & 3;
-    float d[MT][4];
-    float* x10 = sX + (base + S) * LD + col;
-    auto put = [&](float sign) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            float* y = x10 + (16 * i + g) * LD + 2 * t;
-            y[0] = sign * d[i][0];
-            y[1] = sign * d[i][1];
-            y[8 * LD] = sign * d[i][2];
-            y[8 * LD + 1] = sign * d[i][3];
-        }
-    };
-    block_product<MT>(sA + (base + S) * LD + base, sX + base * LD + col, lane, d);
-    put(1.f);
+    for (int i = 0; i < MT; ++i) {
+        float* y = x + at(xr + 16 * i + g, xc + 2 * t);
+        *reinterpret_cast<float2*>(y) = make_float2(sign * d[i][0], sign * d[i][1]);
+        *reinterpret_cast<float2*>(y + 8 * 32) = make_float2(sign * d[i][2], sign * d[i][3]);
+    }
+}
+// Columns [c, c + 8) of X10 = -X11 (A10 X00), in A10's place; all threads take part.
+template <int MT>
+__device__ __forceinline__ void join(const float* x00, float* a10, int ar, const float* x11, int xc, int c, int lane)
+{
+    float d[MT][4];
+    block_product<MT>(a10, ar, 0, x00, 0, c, lane, d);
+    __syncthreads();                                  // every warp has read A10
+    put<MT>(a10, ar, c, lane, 1.f, d);
     __syncwarp();
-    block_product<MT>(sX + (base + S) * LD + base + S, x10, lane, d);
+    block_product<MT>(x11, ar, xc, a10, ar, c, lane, d);
     __syncwarp();
-    put(-1.f);
+    put<MT>(a10, ar, c, lane, -1.f, d);
+    __syncthreads();
 }
 }  // namespace prep
 
-__global__ void __launch_bounds__(prep::NT, 4)
+__global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, uint8_t* __restrict__ rec_all, float scale, int HK, int HV,
             bool gate_f32, bool backward, uint64_t wait_ns)
@@ -143,14 +148,14 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         mbar_init(done, 1);
         fence_mbar_init();
         s_abort = 0;
-        mbar_arrive_expect_tx(full, KQ_BYTES);
+        mbar_arrive_expect_tx(full, 4 * BOX);
         for (int b = 0; b < 2; ++b) {
-            tma_load_2d(tile + b * BOX, &mk, hk * D + 64 * b, t0, full);
-            tma_load_2d(tile + (2 + b) * BOX, &mq, hk * D + 64 * b, t0, full);
+            tma_load_2d(tile + 2 * b * BOX, &mk, hk * D + 64 * b, t0, full);
+            tma_load_2d(tile + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, t0, full);
         }
     }
     if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), 128);
+        tmem_alloc(smem_u32(&s_tmem), C);
         tmem_relinquish();
     }
     if (warp == 2) {                                  // running sum of g in 64 bits, two tokens per lane
@@ -192,20 +197,16 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         if (nv < C) {                                 // rows behind the sequence: whatever is there counts as zero
             for (int e = lane; e < (C - nv) * 4 * 8; e += 32) {
                 const int piece = e & 7, row = nv + (e >> 5), box = (e >> 3) & 3;
-                *reinterpret_cast<uint4*>(sm + box * 8192 + row * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(sm + box * BOX + row * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_smem_to_async();
             __syncwarp();
         }
         if (__all_sync(0xffffffffu, here)) {
-            // K K^T into lanes 0-63 of one block of columns, Q K^T into lanes 64-127 of the other: the other 64 rows
-            // of either left operand are the neighbouring boxes, their results are not read
+            // [K; Q] K^T: K K^T in lanes 0-63, Q K^T in lanes 64-127
             constexpr uint32_t id = idesc_bf16(128, C);
-            const uint64_t k0 = sdesc_sw128(tile), k1 = sdesc_sw128(tile + BOX), q0 = sdesc_sw128(tile + 2 * BOX);
-            mma4_ss<2, 2>(tm, k0, k0, id, 0u);
-            mma4_ss<2, 2>(tm, k1, k1, id, 1u);
-            mma4_ss<2, 2>(tm + C, k1, k0, id, 0u);
-            mma4_ss<2, 2>(tm + C, q0, k1, id, 1u);
+            mma4_ss<2, 2>(tm, sdesc_sw128(tile), sdesc_sw128(tile), id, 0u);
+            mma4_ss<2, 2>(tm, sdesc_sw128(tile + 2 * BOX), sdesc_sw128(tile + 2 * BOX), id, 1u);
             mma_commit_w(done);
             if (!wait(done, 0)) mbar_wait(done, 0, DRAIN_NS);
             issued = true;
@@ -213,8 +214,9 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     __syncthreads();
     fence_after_sync();
-    float* sA = reinterpret_cast<float*>(sm + A_OFF);
-    float* sX = reinterpret_cast<float*>(sm + X_OFF);
+    float* x00 = reinterpret_cast<float*>(sm + B00);
+    float* x10 = reinterpret_cast<float*>(sm + B10);
+    float* x11 = reinterpret_cast<float*>(sm + B11);
     {   // thread: one row of [K K^T; Q K^T]; warps 0-1 make A, warps 2-3 P
         const int r = tid % C;
         const float gh = sGh[r], gl = sGl[r], f = warp < 2 ? sB[r] : scale;
@@ -222,20 +224,20 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         const float* from_l = warp < 2 ? sGl : sCl;
         const int last = warp < 2 ? r - 1 : r;        // the row's last column
 #pragma unroll 1
-        for (int col = 0; col < C; col += 32) {
-            float x[32];
+        for (int col = 0; col < C; col += 16) {
+            float x[16];
             if (col > (r | 31)) {                     // a block above the diagonal (warp-uniform): A's is never read
                 if (warp >= 2) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = 0.f;
+                    for (int i = 0; i < 16; ++i) x[i] = 0.f;
                     store_split(rec + REC_PH, rec + REC_PL, r, col, x);
                 }
                 continue;
             }
-            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + (warp < 2 ? 0 : C) + col, x);
+            tmem_ld16(tm + ((uint32_t)(32 * warp) << 16) + col, x);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
+            for (int i = 0; i < 16; i += 4) {
                 const float4 ch = *reinterpret_cast<const float4*>(from_h + col + i), cl = *reinterpret_cast<const float4*>(from_l + col + i);
                 const float dh[4] = {ch.x, ch.y, ch.z, ch.w}, dl[4] = {cl.x, cl.y, cl.z, cl.w};
 #pragma unroll
@@ -245,9 +247,10 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
                 }
             }
             if (warp < 2) {
+                float* a = warp == 0 ? x00 : col < 32 ? x10 : x11;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4*>(sA + r * LD + col + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(a + at(lane, col % 32 + i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
             } else {
                 store_split(rec + REC_PH, rec + REC_PL, r, col, x);
             }
@@ -256,9 +259,12 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     if (tid < C) {
         const float gh = sGh[tid], gl = sGl[tid], gam = exp2f(gh + gl);
         const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
-        reinterpret_cast<float*>(rec + REC_NGAM)[tid] = s_abort ? __int_as_float(0x7fc00000) : -gam;
-        reinterpret_cast<float*>(rec + REC_ETA)[tid] = exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
-        reinterpret_cast<float*>(rec + REC_GQ)[tid] = scale * gam;
+        // a wait that expired leaves NaN in the state, the outputs and the gradients
+        const bool bad = s_abort != 0;
+        const float nan = __int_as_float(0x7fc00000);
+        reinterpret_cast<float*>(rec + REC_NGAM)[tid] = bad ? nan : -gam;
+        reinterpret_cast<float*>(rec + REC_ETA)[tid] = bad ? nan : exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
+        reinterpret_cast<float*>(rec + REC_GQ)[tid] = bad ? nan : scale * gam;
         reinterpret_cast<float*>(rec + REC_BETA)[tid] = sB[tid];
         sNG[tid] = -gam;
     }
@@ -266,15 +272,15 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     __syncthreads();
     {   // the 16 x 16 diagonal blocks, one per warp: forward substitution, one column per thread (lanes 16-31 repeat
         // lanes 0-15), its values in registers and the rows of A as broadcast reads
-        const float* a = sA + 16 * warp * (LD + 1);
-        const int j = lane & 15;
+        float* blk = warp < 2 ? x00 : x11;
+        const int o = 16 * (warp & 1), j = lane & 15;
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < r; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(a + r * LD + i);
+                const float4 v = *reinterpret_cast<const float4*>(blk + at(o + r, o + i));
                 s[0] = fmaf(v.x, x[i], s[0]);
                 if (i + 1 < r) s[1] = fmaf(v.y, x[i + 1], s[1]);
                 if (i + 2 < r) s[2] = fmaf(v.z, x[i + 2], s[2]);
@@ -282,45 +288,41 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             }
             x[r] = r == j ? 1.f : r > j ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
         }
+        __syncwarp();
         if (lane < 16)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) sX[(16 * warp + r) * LD + 16 * warp + j] = x[r];
-        else if ((warp & 1) == 0)                     // the joined blocks of 32 have zeros above their diagonal
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sX[(16 * warp + r) * LD + 16 * warp + 16 + j] = 0.f;
+            for (int r = 0; r < 16; ++r) blk[at(o + r, o + j)] = x[r];
     }
     __syncthreads();
-    // blocks next to one another: X10 = -X11 (A10 X00), of 16 and then of 32; every warp takes 8 columns, its own
-    // part of A10 X00 passing through X10's place
+    // blocks next to one another: X10 = -X11 (A10 X00), of 16 and then of 32; every warp takes 8 columns
     {
-        const int base = 32 * (warp >> 1), col = base + 8 * (warp & 1);
-        join<1>(sA, sX, base, col, lane);
+        float* blk = warp < 2 ? x00 : x11;
+        join<1>(blk, blk, 16, blk, 16, 8 * (warp & 1), lane);
     }
-    __syncthreads();
-    join<2>(sA, sX, 0, 8 * warp, lane);
-    __syncthreads();
+    join<2>(x00, x10, 0, x11, 0, 8 * warp, lane);
     {   // T = X diag(beta) as two bf16 numbers, in the operand layout: one row and 32 columns per thread
-        const int r = tid % C, col = 32 * (tid / C);
+        const int r = tid % C, half = tid / C, col = 32 * half;
+        const float* blk = half ? x11 : r < 32 ? x00 : x10;
         float x[32];
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(sX + r * LD + col + i), b = *reinterpret_cast<const float4*>(sB + col + i);
+            const float4 v = *reinterpret_cast<const float4*>(blk + at(lane, i)), b = *reinterpret_cast<const float4*>(sB + col + i);
             x[i] = v.x * b.x; x[i + 1] = v.y * b.y; x[i + 2] = v.z * b.z; x[i + 3] = v.w * b.w;
         }
-        const int d = r / 16 * 16 + 16;               // from here on row r was never written
+        if (r < col) {                                // above the diagonal (warp-uniform): not kept
 #pragma unroll
-        for (int i = 0; i < 32; i += 16)
-            if (col + i >= d) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[i + e] = 0.f;
-            }
+            for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
         store_split(rec + REC_TH, rec + REC_TL, r, col, x);
+        store_split(rec + REC_TH, rec + REC_TL, r, col + 16, x + 16);
+        __syncthreads();                              // X has been read
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             const float4 v = *reinterpret_cast<const float4*>(sNG + col + i);
             x[i] *= v.x; x[i + 1] *= v.y; x[i + 2] *= v.z; x[i + 3] *= v.w;
         }
-        store_split(sm + A_OFF, sm + A_OFF + BOX, r, col, x);
+        store_split(sm + BOX, sm + 3 * BOX, r, col, x);
+        store_split(sm + BOX, sm + 3 * BOX, r, col + 16, x + 16);
     }
     fence_smem_to_async();
     __syncthreads();
@@ -329,9 +331,9 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         fence_after_sync();
         if (issued) {
             constexpr uint32_t id = idesc_bf16(128, C, true);
-            const uint64_t kd = (sdesc_sw128(tile) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
-            mma4_ss<128, 16>(tm, kd, sdesc(tile + A_OFF, 128, 1024), id, 0u);
-            mma4_ss<128, 16>(tm, kd, sdesc(tile + A_OFF + BOX, 128, 1024), id, 1u);
+            const uint64_t kd = (sdesc_sw128(tile) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(2 * BOX >> 4) << 16);
+            mma4_ss<128, 16>(tm, kd, sdesc(tile + BOX, 128, 1024), id, 0u);
+            mma4_ss<128, 16>(tm, kd, sdesc(tile + 3 * BOX, 128, 1024), id, 1u);
             mma_commit_w(done);
             if (!wait(done, 1)) mbar_wait(done, 1, DRAIN_NS);
         }
@@ -342,12 +344,12 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         uint8_t* dst = sm + (tid / 64) * BOX + (tid % 8) * 2;
         const int piece = (tid % 64) / 8;
 #pragma unroll 1
-        for (int col = 0; col < C; col += 32) {
-            float x[32];
-            tmem_ld32(tm + ((uint32_t)(32 * warp) << 16) + col, x);
+        for (int col = 0; col < C; col += 16) {
+            float x[16];
+            tmem_ld16(tm + ((uint32_t)(32 * warp) << 16) + col, x);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
                 float hi, lo;
                 split_bf16(x[i], x[i + 1], hi, lo);
                 uint8_t* a = dst + (col + i) * 128 + ((piece ^ (i & 7)) * 16);
@@ -369,7 +371,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     if (warp == 1) {
         fence_after_sync();
-        tmem_dealloc(tm, 128);
+        tmem_dealloc(tm, C);
     }
 }
 
