@@ -446,7 +446,9 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 // ------------------------------------------------------------------- local --
 
 namespace lo {
-constexpr int LNT = 256;
+constexpr int LNT = 256, LALL = LNT + 128;            // threads that compute; and a warpgroup whose first warp loads and issues
+// registers per thread of the two kinds: 168 at launch, 256 x 216 + 128 x 72 = 384 x 168
+constexpr int REGS_COMPUTE = 216, REGS_ISSUE = 72;
 // dV and U (two planes each), then boxes of 64 tokens x 64 channels: dO0 dO1 K0 Q0 K1 Q1
 constexpr uint32_t O_V = 0, O_U = 2 * UPLANE, O_X = 4 * UPLANE;
 constexpr int X_DO = 0, X_K = 2, X_Q = 3, BOXES = 6;
@@ -454,17 +456,18 @@ constexpr int X_DO = 0, X_K = 2, X_Q = 3, BOXES = 6;
 constexpr uint32_t O_ST = O_X + BOXES * BOX;
 // the pair gradients [dkk; dqk] (128 rows of 64, swizzled as a box), two planes; the gates
 constexpr uint32_t O_L = O_ST + 4 * HALF, O_G = O_L + 4 * BOX;
-constexpr uint32_t SMEM = O_G + 1024 + 1024;
+constexpr uint32_t SMEM = O_G + 2 * 1024 + 1024;     // two sets of gates
 constexpr uint32_t O_OUT = 0;                        // dk and dq [64][128] bf16, at the end
 // tensor memory: S0 [dV; dO]^T, dS1 U^T, [dkk; dqk] with K and the rest of dk, dV U^T (lanes 0-63), dO U^T (lanes
 // 64-127), [K; Q] K^T
 constexpr uint32_t T_A = 0, T_B = 128, T_C = 192, T_G = 320, T_G2 = 384, T_KK = 448;
 
-// Sum over the warp's lanes of each of 32 values: lane l gets that of x[l].
-__device__ __forceinline__ float lane_sums(float (&x)[32], int lane)
+// Sum over the warp's lanes of each of N values: lane l gets that of x[l % N].
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&x)[N], int lane)
 {
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) {
+    for (int w = N / 2; w > 0; w >>= 1) {
         const bool up = (lane & w) != 0;
 #pragma unroll
         for (int i = 0; i < w; ++i) {
@@ -472,8 +475,11 @@ __device__ __forceinline__ float lane_sums(float (&x)[32], int lane)
             x[i] = keep + __shfl_xor_sync(0xffffffffu, give, w);
         }
     }
-    return x[0];
+    return N == 32 ? x[0] : x[0] + __shfl_xor_sync(0xffffffffu, x[0], 16);
 }
+
+enum { L_FULL, L_FULL2, L_PAIRS, L_HALF, L_ALL, L_DRAIN, L_ROWS, L_DOT, L_GRADS, L_READ, L_FREE, NBARS };
+__device__ __forceinline__ void computing_sync() { asm volatile("bar.sync 1, %0;" :: "n"(LNT) : "memory"); }
 }  // namespace lo
 
 struct LocalArgs {
@@ -494,13 +500,13 @@ struct LocalMaps {
     CUtensorMap q, k, dO;
 };
 
-__global__ void __launch_bounds__(lo::LNT, 1)
+__global__ void __launch_bounds__(lo::LALL, 1)
 local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ LocalArgs p)
 {
     using namespace lo;
     using namespace tc;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t bars[5];
+    __shared__ __align__(8) uint64_t bars[NBARS];
     __shared__ __align__(16) float sGh[C], sGl[C];
     __shared__ float sDB[C], sA[4][C], sB[4][C], sW[4][C], sTot[2 * C], sDot[8];
     __shared__ uint32_t s_tmem;
@@ -512,12 +518,14 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     int n, chunk, begin, end;
     if (!slot_chunk(p.seqs, slot, n, chunk, begin, end)) return;
     const int t0 = begin + chunk * C, nv = min(C, end - t0);
-    const uint32_t base = smem_u32(sm), full = smem_u32(&bars[0]), full2 = smem_u32(&bars[1]);
-    // products complete: pairs, the states' first half, the second half and the rest (a barrier each: two may
-    // complete before a thread looks)
-    const uint32_t done[3] = {smem_u32(&bars[2]), smem_u32(&bars[3]), smem_u32(&bars[4])};
+    const uint32_t base = smem_u32(sm);
+    // From the loads and products: L_FULL and L_FULL2 a value head's operands and its states' second halves are here;
+    // L_PAIRS, L_HALF, L_ALL the products of the pairs, of the states' first halves, and all are done.  From the
+    // computing warps: L_ROWS rows behind the sequence are zero, L_DOT the states' first halves have been read, L_GRADS
+    // the pair gradients are in place, L_READ the second halves and dV have been read, L_FREE the sums of all products.
+    auto bar = [&](int b) { return smem_u32(&bars[b]); };
     if (tid == 0) {
-        for (int b = 0; b < 5; ++b) mbar_init(smem_u32(&bars[b]), 1);
+        for (int b = 0; b < NBARS; ++b) mbar_init(bar(b), b < L_ROWS ? 1 : LNT / 32);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -529,7 +537,8 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = s_tmem;
-    const Waits wait = {&s_abort, &g_back_status, p.wait_ns};
+    const Waits waits = {&s_abort, &g_back_status, p.wait_ns};
+    auto wait = [&](uint32_t b, uint32_t parity) { return waits.inlined(b, parity); };
     // this thread in tensor memory: lane 32 sp + lane, and the first or second half of the columns
     const int sp = warp & 3, half = warp >> 2, row = 32 * sp + lane;
     const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
@@ -542,18 +551,30 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     };
     // a plane of dV or U, half h of d_v
     auto up = [&](uint32_t off, int h) { return sdesc(base + off + h * 1024, U_LBO, U_SBO); };
-    auto finish = [&](int which, int m) {            // every thread waits for the products
-        if (!wait(done[which], m & 1) && warp == 0) mbar_wait(done[which], m & 1, DRAIN_NS);
-        fence_after_sync();
-    };
-    auto land = [&](uint32_t b, uint32_t parity) {
-        if (!wait(b, parity)) mbar_wait(b, parity, DRAIN_NS);
-    };
     // the states' half h: S0 and dS1, upper and lower plane
     auto load_states = [&](int64_t unit, int h, uint32_t b) {
         for (int x = 0; x < 2; ++x)
             for (int pl = 0; pl < 2; ++pl)
                 bulk_load(base + O_ST + (2 * x + pl) * HALF, (x ? p.dS1 : p.S0) + unit * (2 * (int64_t)PLANE) + pl * PLANE + h * HALF, HALF, b);
+    };
+    // everything of value head m but the states' second halves; K and Q stay for the group
+    auto load_head = [&](int m) {
+        const int hv = hk * group + m;
+        const int64_t unit = slot * p.HV + hv;
+        mbar_arrive_expect_tx(bar(L_FULL), (m == 0 ? 6 : 2) * BOX + 4 * UPLANE + 4 * HALF + 1024);
+        bulk_load(base + O_V, p.dvp + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, bar(L_FULL));
+        bulk_load(base + O_U, p.u + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, bar(L_FULL));
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+            const int x = hv * D + 64 * b, y = hk * D + 64 * b;
+            tma_load_2d(base + O_X + (X_DO + b) * BOX, &maps.dO, x, t0, bar(L_FULL));
+            if (m == 0) {
+                tma_load_2d(base + O_X + (X_K + 2 * b) * BOX, &maps.k, y, t0, bar(L_FULL));
+                tma_load_2d(base + O_X + (X_Q + 2 * b) * BOX, &maps.q, y, t0, bar(L_FULL));
+            }
+        }
+        bulk_load(base + O_G + 1024 * (m & 1), p.rec + unit * REC_BYTES + REC_NGAM, 1024, bar(L_FULL));
+        load_states(unit, 0, bar(L_FULL));
     };
     // products with the states' half in shared memory: S0 [dV; dO]^T and dS1 U^T (d_k as M)
     auto state_products = [&](int h) {
@@ -569,7 +590,6 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         mma4_ss<16, 16>(tm + T_B, ds, up(O_U, h), idm, more);
         mma4_ss<16, 16>(tm + T_B, dsl, up(O_U, h), idm, 1u);
         mma4_ss<16, 16>(tm + T_B, ds, up(O_U + UPLANE, h), idm, 1u);
-        mma_commit_w(done[1 + h]);
     };
     // <dS1, S0> over the half in shared memory
     auto state_dot = [&]() {
@@ -592,26 +612,85 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         return dot;
     };
 
+    if (warp >= LNT / 32) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(REGS_ISSUE));
+        if (warp > LNT / 32) {
+            __syncthreads();
+            return;
+        }
+        auto ok = [&](int b, int m) {
+            const bool r = wait(bar(b), m & 1);
+            fence_after_sync();
+            return __all_sync(0xffffffffu, r && *(volatile int*)&s_abort == 0);
+        };
+        bool loaded2 = false;
+        int m = 0;
+        if (lane == 0) load_head(0);
+        __syncwarp();
+#pragma unroll 1
+        for (; m < group; ++m) {
+            loaded2 = false;
+            if (!ok(nv < C ? L_ROWS : L_FULL, m)) break;
+            // an operand of 64 rows is taken as 128 with its neighbours in shared memory, whose results are not read
+            const uint32_t id = idesc_bf16(128, 64), idm = idesc_bf16(128, 64, true, true), idb = idesc_bf16(128, 64, false, true);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t more = h > 0 ? 1u : 0u;
+                if (m == 0) mma4_ss<2, 2>(tm + T_KK, xb(X_K + 2 * h), xb(X_K + 2 * h), id, more);
+                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U, h), idm, more);
+                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U + UPLANE, h), idm, 1u);
+                mma4_ss<16, 16>(tm + T_G, up(O_V + UPLANE, h), up(O_U, h), idm, 1u);
+                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U, h), idb, more);
+                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U + UPLANE, h), idb, 1u);
+            }
+            mma_commit_w(bar(L_PAIRS));
+            if (m > 0 && !ok(L_FREE, m - 1)) break;
+            state_products(0);
+            mma_commit_w(bar(L_HALF));
+            if (!ok(L_HALF, m) || !ok(L_DOT, m)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar(L_FULL2), 4 * HALF);
+                load_states(slot * p.HV + hk * group + m, 1, bar(L_FULL2));
+            }
+            __syncwarp();
+            loaded2 = true;
+            if (!ok(L_FULL2, m)) break;
+            state_products(1);
+            if (!ok(L_GRADS, m)) break;
+            const uint32_t id128 = idesc_bf16(128, 128, true, false), idmn = idesc_bf16(128, 64, true, true);
+            const uint64_t l = sdesc_sw128(base + O_L), k = xb_mn(X_K), q = xb_mn(X_Q);
+            constexpr uint64_t LO = 2 * BOX >> 4, Q_ROWS = BOX >> 4;
+            // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk
+            mma4_ss<128, 2>(tm + T_C, k, l, id128, 0u);
+            mma4_ss<128, 2>(tm + T_C, k, l + LO, id128, 1u);
+            mma4_ss<128, 128>(tm + T_C, k, l, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, k, l + LO, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, q, l + Q_ROWS, idmn, 1u);
+            mma4_ss<128, 128>(tm + T_C, q, l + LO + Q_ROWS, idmn, 1u);
+            mma_commit_w(bar(L_ALL));
+            if (!ok(L_ALL, m) || !ok(L_READ, m)) break;
+            if (m + 1 < group && lane == 0) load_head(m + 1);
+            __syncwarp();
+        }
+        if (m < group) {                              // gave up: what is in flight ends before its space is used again
+            mbar_wait(bar(L_FULL), m & 1, DRAIN_NS);
+            if (loaded2) mbar_wait(bar(L_FULL2), m & 1, DRAIN_NS);
+            mma_commit_w(bar(L_DRAIN));
+            mbar_wait(bar(L_DRAIN), 0, DRAIN_NS);
+        }
+        __syncthreads();
+        return;
+    }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(REGS_COMPUTE));
 #pragma unroll 1
     for (int m = 0; m < group; ++m) {
         const int hv = hk * group + m;
-        const int64_t unit = slot * p.HV + hv;
-        if (tid == 0) {
-            mbar_arrive_expect_tx(full, (m == 0 ? 6 : 2) * BOX + 4 * UPLANE + 4 * HALF + 1024);
-            bulk_load(base + O_V, p.dvp + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, full);
-            bulk_load(base + O_U, p.u + unit * (2 * (int64_t)UPLANE), 2 * UPLANE, full);
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                const int x = hv * D + 64 * b, y = hk * D + 64 * b;
-                tma_load_2d(base + O_X + (X_DO + b) * BOX, &maps.dO, x, t0, full);
-                if (m == 0) {
-                    tma_load_2d(base + O_X + (X_K + 2 * b) * BOX, &maps.k, y, t0, full);
-                    tma_load_2d(base + O_X + (X_Q + 2 * b) * BOX, &maps.q, y, t0, full);
-                }
-            }
-            load_states(unit, 0, full);
-            bulk_load(base + O_G, p.rec + unit * REC_BYTES + REC_NGAM, 1024, full);
-        }
+        auto give = [&](int b) {                      // this warp's part of what the issuer waits for
+            fence_smem_to_async();
+            fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(b));
+        };
         if (warp == 2) {                              // the running sum of g in units of log 2
             double x[2];
             for (int i = 0; i < 2; ++i) {
@@ -630,34 +709,20 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 sGl[2 * lane + i] = (float)(G - (double)(float)G);
             }
         }
-        land(full, m & 1);
+        wait(bar(L_FULL), m & 1);
         if (nv < C) {                                 // rows behind the sequence (U's and dV's are zero)
-            for (int e = tid; e < (C - nv) * BOXES * 8; e += LNT) {
-                const int piece = e & 7, box = (e >> 3) % BOXES, rr = nv + (e >> 3) / BOXES;
+            const int boxes = m == 0 ? BOXES : 2;
+            for (int e = tid; e < (C - nv) * boxes * 8; e += LNT) {
+                const int piece = e & 7, box = (e >> 3) % boxes, rr = nv + (e >> 3) / boxes;
                 *reinterpret_cast<uint4*>(sm + O_X + box * BOX + rr * 128 + piece * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
-            fence_smem_to_async();
+            give(L_ROWS);
         }
-        __syncthreads();
-        bool issued = false;
-        if (warp == 0 && (issued = !__any_sync(0xffffffffu, *(volatile int*)&s_abort != 0))) {
-            // an operand of 64 rows is taken as 128 with its neighbours in shared memory, whose results are not read
-            const uint32_t id = idesc_bf16(128, 64), idm = idesc_bf16(128, 64, true, true), idb = idesc_bf16(128, 64, false, true);
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t more = h > 0 ? 1u : 0u;
-                if (m == 0) mma4_ss<2, 2>(tm + T_KK, xb(X_K + 2 * h), xb(X_K + 2 * h), id, more);
-                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U, h), idm, more);
-                mma4_ss<16, 16>(tm + T_G, up(O_V, h), up(O_U + UPLANE, h), idm, 1u);
-                mma4_ss<16, 16>(tm + T_G, up(O_V + UPLANE, h), up(O_U, h), idm, 1u);
-                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U, h), idb, more);
-                mma4_ss<2, 16>(tm + T_G2, xb(X_DO + h - 1), up(O_U + UPLANE, h), idb, 1u);
-            }
-            mma_commit_w(done[0]);
-            state_products(0);
-        }
+        computing_sync();
         float dot = state_dot();
-        finish(0, m);
+        give(L_DOT);
+        wait(bar(L_PAIRS), m & 1);
+        fence_after_sync();
         {   // pair gradients: dkk_ri = -D_ri dV_r . U_i (i < r), dqk_ri = scale D_ri dO_r . U_i (i <= r)
             float x[32], y[32];
             const int r = row % C;
@@ -694,75 +759,12 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 *reinterpret_cast<float4*>(dst + 2 * BOX) = make_float4(lw[0], lw[1], lw[2], lw[3]);
             }
         }
-        finish(1, m);                                 // the states' first half has been read
-        fence_smem_to_async();
-        fence_before_sync();
-        __syncthreads();
-        fence_after_sync();
-        if (tid == 0) {
-            mbar_arrive_expect_tx(full2, 4 * HALF);
-            load_states(unit, 1, full2);
-        }
-        if (warp == 0 && issued) {
-            __syncwarp();
-            const uint32_t id128 = idesc_bf16(128, 128, true, false), idmn = idesc_bf16(128, 64, true, true);
-            const uint64_t l = sdesc_sw128(base + O_L), k = xb_mn(X_K), q = xb_mn(X_Q);
-            constexpr uint64_t LO = 2 * BOX >> 4, Q_ROWS = BOX >> 4;
-            // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk
-            mma4_ss<128, 2>(tm + T_C, k, l, id128, 0u);
-            mma4_ss<128, 2>(tm + T_C, k, l + LO, id128, 1u);
-            mma4_ss<128, 128>(tm + T_C, k, l, idmn, 1u);
-            mma4_ss<128, 128>(tm + T_C, k, l + LO, idmn, 1u);
-            mma4_ss<128, 128>(tm + T_C, q, l + Q_ROWS, idmn, 1u);
-            mma4_ss<128, 128>(tm + T_C, q, l + LO + Q_ROWS, idmn, 1u);
-        }
-        land(full2, m & 1);
-        if (warp == 0 && issued) {
-            __syncwarp();
-            state_products(1);
-        }
+        give(L_GRADS);
+        wait(bar(L_FULL2), m & 1);
         dot += state_dot();
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
         if (lane == 0) sDot[warp] = dot;
-        finish(2, m);
-        const float* gates = reinterpret_cast<const float*>(sm + O_G);       // -gam, eta, scale gam, beta: 64 each
-        {   // channel `row`, tokens 32 half .. + 31
-            float a[32], b[32], pa[32];
-            const uint8_t* kp = sm + O_X + (X_K + 2 * (row / 64)) * BOX + (row % 8) * 2;
-            const int piece = (row % 64) / 8;
-            auto at = [&](const uint8_t* x, int tok) {
-                return to_f32(*reinterpret_cast<const __nv_bfloat16*>(x + tok * 128 + ((piece ^ (tok & 7)) * 16)));
-            };
-            tmem_ld32(t + T_A + 32 * half, a);        // dV S0^T
-            tmem_ld32(t + T_C + 32 * half, b);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float z = gates[32 * half + i] * a[i];
-                pa[i] = z * at(kp, 32 * half + i);
-                ak[i] += z + b[i];
-            }
-            tmem_ld32(t + T_A + 64 + 32 * half, a);   // dO S0^T
-            tmem_ld32(t + T_C + 64 + 32 * half, b);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float z = gates[2 * C + 32 * half + i] * a[i];
-                pa[i] = fmaf(z, at(kp + BOX, 32 * half + i), pa[i]);
-                aq[i] += z + b[i];
-            }
-            sA[sp][32 * half + lane] = lane_sums(pa, lane);
-            tmem_ld32(t + T_B + 32 * half, a);        // U dS1^T
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float z = gates[C + 32 * half + i] * a[i];
-                b[i] = z * at(kp, 32 * half + i);
-                ak[i] += z;
-            }
-            sB[sp][32 * half + lane] = lane_sums(b, lane);
-        }
         {   // dv: dV's upper plane, token by token
             const int tok = tid / 4, j0 = 32 * (tid % 4);
             const uint8_t* src = sm + O_V + (tok / 8) * U_SBO + (tok % 8) * 2;
@@ -779,11 +781,74 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                     *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
         }
-        fence_smem_to_async();                        // the next loads write where these threads did
-        fence_before_sync();
-        __syncthreads();                              // everything of this value head has been read
+        give(L_READ);
+        wait(bar(L_ALL), m & 1);
         fence_after_sync();
-        if (warp == 0) {                              // dg and dbeta, two tokens per lane
+        const float* gates = reinterpret_cast<const float*>(sm + O_G + 1024 * (m & 1));       // -gam, eta, scale gam, beta: 64 each
+        {   // channel `row`, tokens 32 half .. + 31 in two parts
+            const uint8_t* kp = sm + O_X + (X_K + 2 * (row / 64)) * BOX + (row % 8) * 2;
+            const int piece = (row % 64) / 8;
+            auto at = [&](const uint8_t* x, int i) {
+                return to_f32(*reinterpret_cast<const __nv_bfloat16*>(x + i * 128 + ((piece ^ (i & 7)) * 16)));
+            };
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                float a[16], b[16], pa[16];
+                const int tok0 = 32 * half + 16 * part;
+                const uint8_t* kt = kp + tok0 * 128;
+                auto gate4 = [&](int which, int i) { return *reinterpret_cast<const float4*>(gates + which * C + tok0 + i); };
+                tmem_ld16(t + T_A + tok0, a);         // dV S0^T
+                tmem_ld16(t + T_C + tok0, b);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 g4 = gate4(0, i);
+                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = f[e] * a[i + e];
+                        pa[i + e] = z * at(kt, i + e);
+                        ak[16 * part + i + e] += z + b[i + e];
+                    }
+                }
+                tmem_ld16(t + T_A + 64 + tok0, a);    // dO S0^T
+                tmem_ld16(t + T_C + 64 + tok0, b);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 g4 = gate4(2, i);
+                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = f[e] * a[i + e];
+                        pa[i + e] = fmaf(z, at(kt + BOX, i + e), pa[i + e]);
+                        aq[16 * part + i + e] += z + b[i + e];
+                    }
+                }
+                tmem_ld16(t + T_B + tok0, a);         // U dS1^T
+                const float as = lane_sums(pa, lane);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 g4 = gate4(1, i);
+                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = f[e] * a[i + e];
+                        b[i + e] = z * at(kt, i + e);
+                        ak[16 * part + i + e] += z;
+                    }
+                }
+                const float bs = lane_sums(b, lane);
+                if (lane < 16) {
+                    sA[sp][tok0 + lane] = as;
+                    sB[sp][tok0 + lane] = bs;
+                }
+            }
+        }
+        give(L_FREE);
+        computing_sync();
+        if (warp == LNT / 32 - 1) {                   // dg and dbeta, two tokens per lane
             float a[2], b[2], w[2], tot[2], dd = lane < 8 ? sDot[lane] : 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -819,8 +884,8 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 }
             }
         }
-        __syncthreads();
     }
+    __syncthreads();                                  // no load is in flight
     {   // dk, dq: channel-major in registers, token-major in memory
         __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + O_OUT);
         const bool bad = *(volatile int*)&s_abort != 0;
@@ -830,7 +895,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             so[tok * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : ak[i]);
             so[(C + tok) * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : aq[i]);
         }
-        __syncthreads();
+        computing_sync();
 #pragma unroll 4
         for (int e = tid; e < 2 * C * D / 8; e += LNT) {
             const int r = (e / (D / 8)) % C, c8 = e % (D / 8);
@@ -840,7 +905,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         }
     }
     fence_before_sync();
-    __syncthreads();
+    computing_sync();
     if (warp == 1) {
         fence_after_sync();
         tmem_dealloc(tm, 512);
@@ -982,7 +1047,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         e = cudaGetLastError();
     }
     if (e == cudaSuccess && N > 0) {
-        local_kernel<<<(unsigned)(slot_count(a.seqs) * HK), lo::LNT, lo::SMEM, stream>>>(maps, l);
+        local_kernel<<<(unsigned)(slot_count(a.seqs) * HK), lo::LALL, lo::SMEM, stream>>>(maps, l);
         e = cudaGetLastError();
     }
     if (N > 0) note_launches(2);

@@ -220,7 +220,13 @@ struct Waits {
         if (ns != 0 && tc::mbar_try_wait(bar, parity)) return true;
         return slow(bar, parity);
     }
-    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const
+    // The same without a call: kernels that move registers between their warps may not make one.
+    __device__ __forceinline__ bool inlined(uint32_t bar, uint32_t parity) const
+    {
+        return (ns != 0 && tc::mbar_try_wait(bar, parity)) || expire(bar, parity);
+    }
+    __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const { return expire(bar, parity); }
+    __device__ __forceinline__ bool expire(uint32_t bar, uint32_t parity) const
     {
         if (ns == 0 && tc::mbar_test_wait(bar, parity)) return true;
         // by the SM's clock (2 cycles per ns at most): reading the global timer takes about as long as its 1 us step,
