@@ -542,7 +542,8 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     // this thread in tensor memory: lane 32 sp + lane, and the first or second half of the columns
     const int sp = warp & 3, half = warp >> 2, row = 32 * sp + lane;
     const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-    float ak[32], aq[32];                            // dk, dq at channel `row`, 32 tokens, over the group
+    // dk, dq at channel `row`, 32 tokens, over the group: what comes from the states
+    float ak[32], aq[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) ak[i] = aq[i] = 0.f;
     auto xb = [&](int b) { return sdesc_sw128(base + O_X + b * BOX); };
@@ -660,8 +661,8 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             const uint32_t id128 = idesc_bf16(128, 128, true, false), idmn = idesc_bf16(128, 64, true, true);
             const uint64_t l = sdesc_sw128(base + O_L), k = xb_mn(X_K), q = xb_mn(X_Q);
             constexpr uint64_t LO = 2 * BOX >> 4, Q_ROWS = BOX >> 4;
-            // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk
-            mma4_ss<128, 2>(tm + T_C, k, l, id128, 0u);
+            // K^T [dkk; dqk]^T, then the columns of dk: K^T dkk + Q^T dqk; summed over the group
+            mma4_ss<128, 2>(tm + T_C, k, l, id128, m > 0 ? 1u : 0u);
             mma4_ss<128, 2>(tm + T_C, k, l + LO, id128, 1u);
             mma4_ss<128, 128>(tm + T_C, k, l, idmn, 1u);
             mma4_ss<128, 128>(tm + T_C, k, l + LO, idmn, 1u);
@@ -766,7 +767,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
         for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
         if (lane == 0) sDot[warp] = dot;
         {   // dv: dV's upper plane, token by token
-            const int tok = tid / 4, j0 = 32 * (tid % 4);
+            const int tok = tid / 4, q = tid & 3, j0 = 32 * q;
             const uint8_t* src = sm + O_V + (tok / 8) * U_SBO + (tok % 8) * 2;
             __nv_bfloat16* out = p.dv + ((int64_t)(t0 + tok) * p.HV + hv) * D + j0;
             if (tok < nv)
@@ -774,11 +775,12 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
                 for (int i = 0; i < 32; i += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint8_t* a = src + (j0 + i + 2 * e) * 16;
+                    for (int e = 0; e < 4; ++e) {     // pair (e + q) & 3: neighbouring threads in different banks
+                        const uint8_t* a = src + (j0 + i + 2 * ((e + q) & 3)) * 16;
                         w[e] = *reinterpret_cast<const uint16_t*>(a) | ((uint32_t)*reinterpret_cast<const uint16_t*>(a + 16) << 16);
                     }
-                    *reinterpret_cast<uint4*>(out + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                    const uint4 x = q & 1 ? make_uint4(w[3], w[0], w[1], w[2]) : make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(out + i) = q & 2 ? make_uint4(x.z, x.w, x.x, x.y) : x;
                 }
         }
         give(L_READ);
@@ -793,53 +795,29 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             };
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                float a[16], b[16], pa[16];
                 const int tok0 = 32 * half + 16 * part;
                 const uint8_t* kt = kp + tok0 * 128;
+                float a[16], b[16], c[16], pa[16];
                 auto gate4 = [&](int which, int i) { return *reinterpret_cast<const float4*>(gates + which * C + tok0 + i); };
                 tmem_ld16(t + T_A + tok0, a);         // dV S0^T
-                tmem_ld16(t + T_C + tok0, b);
+                tmem_ld16(t + T_A + 64 + tok0, b);    // dO S0^T
+                tmem_ld16(t + T_B + tok0, c);         // U dS1^T
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
-                    const float4 g4 = gate4(0, i);
-                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
+                    const float4 g4 = gate4(0, i), h4 = gate4(1, i), q4 = gate4(2, i);
+                    const float fa[4] = {g4.x, g4.y, g4.z, g4.w}, fb[4] = {q4.x, q4.y, q4.z, q4.w}, fc[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float z = f[e] * a[i + e];
-                        pa[i + e] = z * at(kt, i + e);
-                        ak[16 * part + i + e] += z + b[i + e];
+                        const float x = at(kt, i + e), y = at(kt + BOX, i + e);
+                        const float za = fa[e] * a[i + e], zb = fb[e] * b[i + e], zc = fc[e] * c[i + e];
+                        pa[i + e] = fmaf(za, x, zb * y);
+                        c[i + e] = zc * x;
+                        ak[16 * part + i + e] += za + zc;
+                        aq[16 * part + i + e] += zb;
                     }
                 }
-                tmem_ld16(t + T_A + 64 + tok0, a);    // dO S0^T
-                tmem_ld16(t + T_C + 64 + tok0, b);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 g4 = gate4(2, i);
-                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float z = f[e] * a[i + e];
-                        pa[i + e] = fmaf(z, at(kt + BOX, i + e), pa[i + e]);
-                        aq[16 * part + i + e] += z + b[i + e];
-                    }
-                }
-                tmem_ld16(t + T_B + tok0, a);         // U dS1^T
-                const float as = lane_sums(pa, lane);
-                wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const float4 g4 = gate4(1, i);
-                    const float f[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float z = f[e] * a[i + e];
-                        b[i + e] = z * at(kt, i + e);
-                        ak[16 * part + i + e] += z;
-                    }
-                }
-                const float bs = lane_sums(b, lane);
+                const float as = lane_sums(pa, lane), bs = lane_sums(c, lane);
                 if (lane < 16) {
                     sA[sp][tok0 + lane] = as;
                     sB[sp][tok0 + lane] = bs;
@@ -889,11 +867,15 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
     {   // dk, dq: channel-major in registers, token-major in memory
         __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + O_OUT);
         const bool bad = *(volatile int*)&s_abort != 0;
+        float x[32], y[32];
+        tmem_ld32(t + T_C + 32 * half, x);
+        tmem_ld32(t + T_C + 64 + 32 * half, y);
+        wait_ld();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             const int tok = 32 * half + i;
-            so[tok * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : ak[i]);
-            so[(C + tok) * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : aq[i]);
+            so[tok * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : ak[i] + x[i]);
+            so[(C + tok) * D + row] = __float2bfloat16_rn(bad ? __int_as_float(0x7fc00000) : aq[i] + y[i]);
         }
         computing_sync();
 #pragma unroll 4

@@ -223,6 +223,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         const float* from_h = warp < 2 ? sGh : sCh;
         const float* from_l = warp < 2 ? sGl : sCl;
         const int last = warp < 2 ? r - 1 : r;        // the row's last column
+        const float2 minus = make_float2(-1.f, -1.f);
 #pragma unroll 1
         for (int col = 0; col < C; col += 16) {
             float x[16];
@@ -239,11 +240,15 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
                 const float4 ch = *reinterpret_cast<const float4*>(from_h + col + i), cl = *reinterpret_cast<const float4*>(from_l + col + i);
-                const float dh[4] = {ch.x, ch.y, ch.z, ch.w}, dl[4] = {cl.x, cl.y, cl.z, cl.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = exp2_fast((gh - dh[e]) + (gl - dl[e]));
-                    x[i + e] = col + i + e <= last ? f * d * x[i + e] : 0.f;
+                for (int e = 0; e < 4; e += 2) {
+                    const float2 h = e ? make_float2(ch.z, ch.w) : make_float2(ch.x, ch.y);
+                    const float2 l = e ? make_float2(cl.z, cl.w) : make_float2(cl.x, cl.y);
+                    const float2 d = add2(fma2(h, minus, make_float2(gh, gh)), fma2(l, minus, make_float2(gl, gl)));
+                    const float2 y = mul2(mul2(make_float2(exp2_fast(d.x), exp2_fast(d.y)), make_float2(f, f)),
+                                          make_float2(x[i + e], x[i + e + 1]));
+                    x[i + e] = col + i + e <= last ? y.x : 0.f;
+                    x[i + e + 1] = col + i + e + 1 <= last ? y.y : 0.f;
                 }
             }
             if (warp < 2) {
