@@ -5,10 +5,13 @@
 //
 // Bound by HBM: the fp32 state is read once and written once (128 KB per
 // request and head at d_k = d_v = 128), everything else is 1 % of that.  The
-// state's columns are independent, so a CTA of 256 threads takes NCOL of them:
+// state's columns are independent, but a CTA of 256 threads takes all of them:
 // thread (rg, cg) owns columns 4 cg .. 4 cg + 3 of rows rg, rg + RSTEP, ... ,
 // every access a 16-byte vector of a full 128-byte line, all loads of the
-// state issued before any arithmetic.  The two column sums over d_k go through
+// state issued before any arithmetic: more bytes in flight per thread.  Four
+// CTAs of 32 columns each took as long at 32 states of 128 x 128 (5.6 us) and
+// longer at all other counts (8.0 against 5.9 us at 128, 41 against 25 us at
+// 1184).  176 us for 256 requests x 32 heads: 6.1 TB/s.  The two column sums over d_k go through
 // shuffles where lanes of a warp share a column group and one shared-memory
 // pass.
 #include "gdn_common.cuh"
@@ -18,46 +21,45 @@ namespace gdn {
 
 constexpr int STEP_NT = 256;
 
-template <int DK, int NCOL>
+template <int DK, int DV>
 struct StepMap {
-    static constexpr int CG = NCOL / 4;              // float4 column groups
+    static constexpr int CG = DV / 4;                // float4 column groups
     static constexpr int RSTEP = STEP_NT / CG;       // rows covered per pass
     static constexpr int ROWS = (DK + RSTEP - 1) / RSTEP;
     static_assert(DK % RSTEP == 0, "rows per thread");
 };
 
-template <int DK, int NCOL>
+template <int DK, int DV>
 __global__ void __launch_bounds__(STEP_NT)
 step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
             const __nv_bfloat16* __restrict__ v, const void* __restrict__ g, const void* __restrict__ beta,
             float* __restrict__ state, __nv_bfloat16* __restrict__ o, const int* __restrict__ slots, int n_slots,
-            float scale, int HK, int HV, int dv, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32)
+            float scale, int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32)
 {
-    using M = StepMap<DK, NCOL>;
+    using M = StepMap<DK, DV>;
     constexpr int CG = M::CG, RSTEP = M::RSTEP, ROWS = M::ROWS;
     __shared__ float sh_k[DK], sh_q[DK], sh_qk;
     __shared__ float4 red[2][RSTEP][CG];
     const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
     const int hv = blockIdx.y;
     const int64_t n = blockIdx.x;
-    const int j0 = blockIdx.z * NCOL;
     const int64_t row = slots ? slots[n] : n;
-    __nv_bfloat16* on = o + (n * HV + hv) * dv + j0 + 4 * cg;
+    __nv_bfloat16* on = o + (n * HV + hv) * DV + 4 * cg;
     if (row < 0 || row >= n_slots) {                 // a padded row of the batch: no state, o = 0
         if (rg == 0) *reinterpret_cast<uint2*>(on) = make_uint2(0u, 0u);
         return;
     }
-    float* S = state + (row * HV + hv) * (int64_t)DK * dv + j0 + 4 * cg;
+    float* S = state + (row * HV + hv) * (int64_t)(DK * DV) + 4 * cg;
     float4 s[ROWS];
 #pragma unroll
     for (int m = 0; m < ROWS; ++m)
-        s[m] = __ldcs(reinterpret_cast<const float4*>(S + (int64_t)(rg + m * RSTEP) * dv));
+        s[m] = __ldcs(reinterpret_cast<const float4*>(S + (rg + m * RSTEP) * DV));
     const int hk = hv / (HV / HK);
     if (tid < DK) {
         sh_k[tid] = to_f32(k[n * k_stride + hk * DK + tid]);
         sh_q[tid] = to_f32(q[n * q_stride + hk * DK + tid]);
     }
-    const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(v + n * v_stride + (int64_t)hv * dv + j0 + 4 * cg);
+    const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(v + n * v_stride + (int64_t)hv * DV + 4 * cg);
     const float2 v01 = __bfloat1622float2(v2[0]), v23 = __bfloat1622float2(v2[1]);
     const float a = expf(gate(g, n * HV + hv, gate_f32)), b = gate(beta, n * HV + hv, gate_f32);
     __syncthreads();
@@ -93,7 +95,7 @@ step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
         float4 x;
         x.x = fmaf(ki, u.x, a * s[m].x); x.y = fmaf(ki, u.y, a * s[m].y);
         x.z = fmaf(ki, u.z, a * s[m].z); x.w = fmaf(ki, u.w, a * s[m].w);
-        __stcs(reinterpret_cast<float4*>(S + (int64_t)(rg + m * RSTEP) * dv), x);
+        __stcs(reinterpret_cast<float4*>(S + (rg + m * RSTEP) * DV), x);
     }
     if (rg == 0) {
         for (int w = 0; w < RSTEP; ++w) {
@@ -116,17 +118,16 @@ cudaError_t gdn_step_launch(const void* q, const void* k, const void* v, const v
 {
     using namespace gdn;
     using bf = __nv_bfloat16;
-#define GDN_STEP(DK_, NCOL_)                                                                                    \
-    step_kernel<DK_, NCOL_><<<dim3((unsigned)N, (unsigned)HV, (unsigned)(dv / NCOL_)), STEP_NT, 0, stream>>>(    \
-        (const bf*)q, (const bf*)k, (const bf*)v, g, beta, state, (bf*)o, slots, n_slots, scale, HK, HV, dv,     \
+#define GDN_STEP(DK_, DV_)                                                                                      \
+    step_kernel<DK_, DV_><<<dim3((unsigned)N, (unsigned)HV), STEP_NT, 0, stream>>>(                              \
+        (const bf*)q, (const bf*)k, (const bf*)v, g, beta, state, (bf*)o, slots, n_slots, scale, HK, HV,         \
         q_stride, k_stride, v_stride, gate_f32)
-    if (dk == 128) {
-        if (dv % 128 == 0) GDN_STEP(128, 128); else GDN_STEP(128, 32);
-    } else if (dk == 64) {
-        GDN_STEP(64, 32);
-    } else {
-        GDN_STEP(32, 32);
-    }
+#define GDN_STEP_DV(DK_) \
+    if (dv == 128) GDN_STEP(DK_, 128); else if (dv == 64) GDN_STEP(DK_, 64); else GDN_STEP(DK_, 32)
+    if (dk == 128) { GDN_STEP_DV(128); }
+    else if (dk == 64) { GDN_STEP_DV(64); }
+    else { GDN_STEP_DV(32); }
+#undef GDN_STEP_DV
 #undef GDN_STEP
     note_launches(1);
     return cudaGetLastError();
