@@ -1,0 +1,216 @@
+"""How the calls of the gated delta rule with one decay per head are made:
+waits that run out, two calls at once, rows named twice, offsets past 32 bits.
+
+A wait that runs out (KDA_WAIT_LIMIT_NS=0 makes every wait a single check)
+faults nothing: the kernels end by themselves, everything that they write is
+NaN, kda_device_status says KDA_ERR_TIMEOUT once, and the next call is right.
+Tolerances are those of the forward's and the backward's own tests.
+"""
+import pytest
+import torch
+
+import linear_attention_07_b200 as kda
+from test_gdn import D, TOL_O, TOL_S, TOL_STEP, batch, cu_of, on_gpu, reference, rel, tokens
+from test_gdn_backward import check, cotangents, run
+from test_gdn_backward import reference as gradients
+
+pytestmark = pytest.mark.gpu
+
+LENS = (100, 1, 64)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from linear_attention_07_b200 import build
+    build.build()
+    kda.load_library()
+    torch.cuda.init()
+
+
+def expired():
+    torch.cuda.synchronize()
+    assert kda.device_status() == kda.KDA_ERR_TIMEOUT
+    assert kda.device_status() == kda.KDA_OK             # read and cleared
+
+
+def test_forward_waits_expire(monkeypatch):
+    x, h0 = tokens(165, 2, 4, seed=70), torch.randn(3, 4, D, D)
+    call = lambda: kda.gdn_chunk_fwd(*batch(on_gpu(x)), h0.cuda(), cu_seqlens=cu_of(LENS).cuda())
+    assert kda.device_status() == kda.KDA_OK
+    monkeypatch.setenv("KDA_WAIT_LIMIT_NS", "0")
+    o, S = call()
+    expired()
+    assert torch.isnan(o.float()).all() and torch.isnan(S).all()
+    monkeypatch.delenv("KDA_WAIT_LIMIT_NS")
+    o, S = call()
+    ro, rS = reference(x, LENS, h0)
+    assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= TOL_S
+    assert kda.device_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_backward_waits_expire(monkeypatch, eight):
+    x, h0 = tokens(165, 2, 4, seed=71), torch.randn(3, 4, D, D)
+    dO, dhT = cotangents(165, 4, 3)
+    assert kda.device_status() == kda.KDA_OK
+    monkeypatch.setenv("KDA_WAIT_LIMIT_NS", "0")
+    if eight:
+        q, k, v, g, b = batch(on_gpu(x))
+        got = kda.gdn_chunk_bwd(*kda.act_pack8(q, k, v), g, b, h0.cuda(), dO[None].cuda(), dhT.cuda(),
+                                cu_seqlens=cu_of(LENS).cuda())
+    else:
+        got = run(x, LENS, dO, h0, dhT)
+    expired()
+    for name, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got):
+        assert torch.isnan(t.float()).all(), name
+    monkeypatch.delenv("KDA_WAIT_LIMIT_NS")
+    check(run(x, LENS, dO, h0, dhT), gradients(x, LENS, dO, h0, dhT))
+
+
+def test_two_calls_at_once():
+    """Each call has its own workspace: calls on two streams leave one another's results alone."""
+    a, b = tokens(1500, 2, 4, seed=72), tokens(1500, 2, 4, seed=73)
+    dO, dhT = cotangents(1500, 4, 1)
+    xs = [batch(on_gpu(t)) for t in (a, b)]
+    dOg, dhTg = dO[None].cuda(), dhT.cuda()
+
+    def both(x):
+        o, S = kda.gdn_chunk_fwd(*x)
+        return [o, S, *kda.gdn_chunk_bwd(*x, None, dOg, dhTg)]
+
+    want = [both(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(4):
+        for i, (x, s) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(both(x))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert all(torch.equal(y, z) for y, z in zip(w, r))
+    assert kda.device_status() == kda.KDA_OK
+
+
+def test_two_graphs_of_calls():
+    """Captured calls own their workspace too: two graphs replayed in turn and at once."""
+    xs = [batch(on_gpu(tokens(700, 2, 2, seed=s))) for s in (74, 75)]
+    want = [kda.gdn_chunk_fwd(*x) for x in xs]
+    graphs, outs = [], []
+    for x in xs:
+        s = torch.cuda.Stream()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(kda.gdn_chunk_fwd(*x))
+        graphs.append(g)
+    for at_once in (False, True):
+        for o, S in outs:
+            o.zero_()
+            S.zero_()
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.stream(torch.cuda.Stream() if at_once else torch.cuda.current_stream()):
+                g.replay()
+        torch.cuda.synchronize()
+        for w, r in zip(want, outs):
+            assert all(torch.equal(y, z) for y, z in zip(w, r))
+
+
+def test_state_in_place_and_on_a_side_stream():
+    x, h0 = tokens(130, 2, 6, seed=76), torch.randn(1, 6, D, D)
+    ro, rS = reference(x, [130], h0)
+    S = h0.cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        o, out = kda.gdn_chunk_fwd(*batch(on_gpu(x)), S, hT=S)
+        torch.cuda.current_stream().synchronize()
+    assert out is S
+    assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= TOL_S
+
+
+def test_a_row_named_twice():
+    """Which of two requests a shared row's last state is from is not specified; nothing else is touched."""
+    N, HK, HV = 4, 2, 4
+    x = tokens(N, HK, HV, seed=77)
+    pool = torch.randn(6, HV, D, D)
+    slots = torch.tensor([1, 1, 4, 7], dtype=torch.int32)
+    S = pool.cuda()
+    o = kda.gdn_decode_step(*on_gpu(x), S, slots=slots.cuda())
+    assert torch.isfinite(S).all() and torch.isfinite(o.float()).all()
+    assert torch.equal(S[[0, 2, 3, 5]].cpu(), pool[[0, 2, 3, 5]])
+    assert not o[3].any()
+    ro, rS = reference([t[2:3] for t in x], [1], pool[4:5])
+    assert rel(o[2], ro[0]) <= TOL_O and rel(S[4:5], rS) <= TOL_STEP
+    S = pool.cuda()
+    kda.gdn_chunk_fwd(*batch(on_gpu(x)), S, cu_seqlens=cu_of([1] * N).cuda(), slots=slots.cuda())
+    assert torch.isfinite(S).all()
+    assert torch.equal(S[[0, 2, 3, 5]].cpu(), pool[[0, 2, 3, 5]])
+    assert rel(S[4:5], rS) <= TOL_S
+    assert kda.device_status() == kda.KDA_OK
+
+
+def test_pool_past_32_bits():
+    """Rows behind the 2^31st element of a pool."""
+    HK, HV, rows = 2, 32, 4099
+    assert (rows - 1) * HV * D * D > 2 ** 31
+    pool = torch.empty(rows, HV, D, D, device="cuda")
+    S0 = torch.randn(2, HV, D, D)
+    rws = torch.tensor([rows - 1, rows - 3])
+    pool[rws] = S0.cuda()
+    slots = rws.int().cuda()
+    x = tokens(2, HK, HV, seed=78)
+    o = kda.gdn_decode_step(*on_gpu(x), pool, slots=slots)
+    ro, rS = reference(x, [1, 1], S0)
+    assert rel(o, ro) <= TOL_O and rel(pool[rws], rS) <= TOL_STEP
+    pool[rws] = S0.cuda()
+    x = tokens(80, HK, HV, seed=79)
+    o, _ = kda.gdn_chunk_fwd(*batch(on_gpu(x)), pool, cu_seqlens=cu_of([70, 10]).cuda(), slots=slots)
+    ro, rS = reference(x, [70, 10], S0)
+    assert rel(o[0], ro) <= TOL_O and rel(pool[rws], rS) <= TOL_S
+
+
+def test_tokens_past_32_bits():
+    """A sequence whose values lie behind the 2^31st element of v and o."""
+    HK, HV, L = 1, 64, 100
+    T = 2 ** 31 // (HV * D) + 200
+    x = tokens(L, HK, HV, seed=80)
+    big = []
+    for t in x:
+        y = torch.zeros(1, T, *t.shape[1:], dtype=t.dtype, device="cuda")
+        y[0, T - L:] = t.cuda()
+        big.append(y)
+    cu = torch.tensor([T - L - 30, T - L, T], dtype=torch.int32, device="cuda")
+    o, S = kda.gdn_chunk_fwd(*big, cu_seqlens=cu)
+    ro, rS = reference(x, [L])
+    assert rel(o[0, T - L:], ro) <= TOL_O and rel(S[1:], rS) <= TOL_S
+    del o
+    back = kda.act_unpack8(kda.act_pack8(big[2]))
+    small = kda.act_unpack8(kda.act_pack8(x[2].cuda().contiguous()))
+    assert torch.equal(back[0, T - L:], small) and not back[0, :T - L].any()
+
+
+def test_strides_past_32_bits():
+    """Tokens so far apart that the last ones lie behind the 2^31st element of their tensor."""
+    HK, HV, T = 2, 4, 130
+    x = tokens(T, HK, HV, seed=81)
+    dO, dhT = cotangents(T, HV, 1)
+    stride = 2 ** 24 + 2 ** 19
+    assert (T - 1) * stride > 2 ** 31
+    wide = torch.empty(1, T, stride, dtype=torch.bfloat16, device="cuda")
+    far, at = [], stride - (2 * HK + HV) * D
+    for t in x[:3]:
+        heads = t.shape[1]
+        y = wide[..., at:at + heads * D].unflatten(-1, (heads, D))
+        y.copy_(t[None].cuda())
+        far.append(y)
+        at += heads * D
+    gates = batch([t.cuda() for t in x[3:]])
+    near = batch(on_gpu(x))
+    for a, b in zip(kda.gdn_chunk_fwd(*far, *gates), kda.gdn_chunk_fwd(*near)):
+        assert torch.equal(a, b)
+    back = lambda y: kda.gdn_chunk_bwd(*y, *gates, None, dO[None].cuda(), dhT.cuda())
+    for a, b in zip(back(far), back(near[:3])):
+        assert torch.equal(a, b)
+    for a, b in zip(kda.act_pack8(*far), kda.act_pack8(*near[:3])):
+        assert torch.equal(a.data.view(torch.uint8), b.data.view(torch.uint8)) and torch.equal(a.scales, b.scales)
