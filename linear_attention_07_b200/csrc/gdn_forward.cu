@@ -12,6 +12,10 @@
 // shared memory.  Sums are fp32; the state is updated in fp32 registers (never
 // accumulated in tensor memory, whose additions need not round to nearest).
 //
+// Long sequences of few heads run in segments, as the chunks of one head are a
+// chain: every segment from zero and its transition at the same time, the start
+// states joined, and every segment again with its outputs.
+//
 // Roles (22 warps):
 //   warps 0-15  chain: thread (j, part) holds S[dk][j] for 16 + 16 values of
 //               dk and takes 16 of the chunk's tokens; eta U, the state
@@ -27,6 +31,9 @@
 // cores would be idle.  The state goes in two halves of d_k, so that a product
 // runs on one while the other is converted (halves of the tokens gain nothing:
 // an MMA of N = 32 takes as long as one of N = 64).
+#include <algorithm>
+#include <cmath>
+
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -67,12 +74,26 @@ constexpr uint32_t T_UE = 192;                       // (eta U)^T
 constexpr uint32_t T_XQ = 256, T_O = 320;
 constexpr uint32_t T_D = 384;                        // (K^T eta U)^T
 
+// A sequence in one piece; or in segments, of which the first of two launches
+// runs segment 0 and, for each of the segments between it and the last, the
+// state that it reaches from zero and its transition (from the identity with V =
+// 0; neither has outputs), and the second launch runs all but segment 0 from
+// their start states.
+enum Pass { WHOLE, FIRST, SECOND };
+// Segment 0 counts 8 of the others' 10: its outputs are made while theirs are not.
+constexpr int SEG_FIRST = 8, SEG_OTHER = 10;
+constexpr int MIN_CHUNKS = 40;                       // of a sequence in segments
+
 struct Args {
     Seqs seqs;
     const uint8_t* rec;
     const float* h0;
     float* hT;
     __nv_bfloat16* o;
+    // [n_seq][HV][D][D] the state behind segment 0 and that before the last; [n_seq][segments - 2][HV][D][D] the
+    // transitions, the states reached from zero and the start states of those between
+    float *end0, *before_last, *M, *N, *start;
+    int pass, segments;
     int HK, HV;
     float scale;
     uint64_t wait_ns;
@@ -93,13 +114,45 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     __shared__ int s_abort;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hv = blockIdx.x % p.HV, n = blockIdx.x / p.HV;
+    const int hv = blockIdx.x % p.HV, between = p.segments - 2;
+    const int tasks = p.pass == WHOLE ? 1 : p.pass == FIRST ? 1 + 2 * between : between + 1;
+    const int task = (blockIdx.x / p.HV) % tasks, n = blockIdx.x / (p.HV * tasks);
     const int hk = hv / (p.HV / p.HK);
     int begin, end;
     seq_range(p.seqs, n, begin, end);
-    const int chunks = (end - begin + C - 1) / C;
+    int chunks = (end - begin + C - 1) / C;
+    int64_t slot0 = (int64_t)(begin / C) + n;
     const int row = state_row(p.seqs, n);
-    const int64_t slot0 = (int64_t)(begin / C) + n;
+    const int64_t head = ((int64_t)n * p.HV + hv) * D * D, pool = ((int64_t)row * p.HV + hv) * D * D;
+    // where the state comes from and goes to; whether outputs are made, and whether V counts as zero and the state
+    // begins as the identity
+    const float* from = p.h0 && row >= 0 ? p.h0 + pool : nullptr;
+    float* to = p.hT && row >= 0 ? p.hT + pool : nullptr;
+    bool outputs = true, transition = false;
+    if (p.pass != WHOLE) {
+        const int seg = p.pass == SECOND ? 1 + task : (task + 1) / 2;
+        const int64_t mid = (((int64_t)n * between + seg - 1) * p.HV + hv) * D * D;
+        if (p.pass == SECOND) {
+            from = seg <= between ? p.start + mid : p.before_last + head;
+            if (seg <= between) to = nullptr;
+        } else if (seg == 0) {
+            to = p.end0 + head;
+        } else {
+            outputs = false;
+            transition = task % 2 == 0;
+            from = nullptr;
+            to = (transition ? p.M : p.N) + mid;
+        }
+        auto first_chunk = [&](int x) {
+            constexpr int less = SEG_OTHER - SEG_FIRST;
+            return x == 0 ? 0 : (int)((int64_t)chunks * (SEG_OTHER * x - less) / (SEG_OTHER * p.segments - less));
+        };
+        const int c0 = first_chunk(seg), c1 = first_chunk(seg + 1);
+        end = min(end, begin + c1 * C);
+        begin += c0 * C;
+        slot0 += c0;
+        chunks = c1 - c0;
+    }
     auto bar = [&](int b) { return smem_u32(&bars[b]); };
 
     if (tid == 0) {
@@ -124,11 +177,13 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
-        const float* h = p.h0 && row >= 0 ? p.h0 + ((int64_t)row * p.HV + hv) * D * D + j : nullptr;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 16 * part + i) * D] : 0.f;
+            for (int i = 0; i < 16; ++i) {
+                const int dk = 64 * b + 16 * part + i;
+                S[b][i] = from ? from[dk * D + j] : transition && dk == j ? 1.f : 0.f;
+            }
         auto put = [&](uint32_t col, const float (&x)[16]) {     // this part's 16 values of an operand
             float w[16];
             tmem_put16(t + col + 16 * part, x, w);
@@ -186,20 +241,18 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 }
             }
         }
-        if (p.hT && row >= 0) {
-            float* hT = p.hT + ((int64_t)row * p.HV + hv) * D * D + j;
+        if (to)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) hT[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
-        }
+                for (int i = 0; i < 16; ++i) to[(64 * b + 16 * part + i) * D + j] = S[b][i];
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
         const int ot = tid - 32 * N_CHAIN;
         __nv_bfloat16* so = reinterpret_cast<__nv_bfloat16*>(sm + S_OUT);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < chunks && outputs; ++c) {
             const float2* gq = reinterpret_cast<const float2*>(sm + S_GATE + (c % GATE_SLOTS) * GATE_BYTES + (REC_GQ - REC_NGAM));
             wait(bar(B_GATE + c % GATE_SLOTS), (c / GATE_SLOTS) & 1);
             wait(bar(B_MO), c & 1);
@@ -268,6 +321,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 __syncwarp();
             }
             const uint32_t base = smem_u32(st);
+            if (transition) return true;
             const uint64_t vd = (sdesc_sw128(base + S_V) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(BOX >> 4) << 16);
             mma4_ss<128, 16>(tm + T_U, vd, sdesc(base + S_REC + REC_TH, 128, 1024), id_v, 0u);
             mma4_ss<128, 16>(tm + T_U, vd, sdesc(base + S_REC + REC_TL, 128, 1024), id_v, 1u);
@@ -280,7 +334,7 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const uint64_t kq = sdesc_sw128(base), wd = sdesc_sw128(base + S_REC + REC_WH);
             auto w_product = [&](int b) {             // -(W S)^T over half b of d_k
                 const uint64_t h = wd + (uint64_t)(b * (BOX >> 4)), l = h + (uint64_t)(2 * BOX >> 4);
-                mma4_ts<2>(tm + T_U, tm + T_S + 64 * b, h, id_n64, 1u);
+                mma4_ts<2>(tm + T_U, tm + T_S + 64 * b, h, id_n64, transition && b == 0 ? 0u : 1u);
                 mma4_ts<2>(tm + T_U, tm + T_S + 64 * b + LOWER, h, id_n64, 1u);
                 mma4_ts<2>(tm + T_U, tm + T_S + 64 * b, l, id_n64, 1u);
             };
@@ -291,13 +345,15 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             fence_after_sync();
             w_product(1);
             mma_commit_w(bar(B_MU));
-            if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
-            fence_after_sync();
+            if (outputs) {
+                if (c > 0 && !ok(B_OFREE, (c - 1) & 1)) break;
+                fence_after_sync();
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {             // (Q S)^T, before a new state replaces the old one
-                const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
-                mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b, qd, id_n64, b > 0 ? 1u : 0u);
-                mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b + LOWER, qd, id_n64, 1u);
+                for (int b = 0; b < 2; ++b) {         // (Q S)^T, before a new state replaces the old one
+                    const uint64_t qd = kq + (uint64_t)((2 * b + 1) * (BOX >> 4));
+                    mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b, qd, id_n64, b > 0 ? 1u : 0u);
+                    mma4_ts<2>(tm + T_XQ, tm + T_S + 64 * b + LOWER, qd, id_n64, 1u);
+                }
             }
             if (!ok(B_U, c & 1)) break;               // eta U, and P has landed
             fence_after_sync();
@@ -308,10 +364,12 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE + LOWER, kd, id_d, 1u);
                 mma_commit_w(bar(B_MD + b));
             }
-            const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
-            mma4_ts<16>(tm + T_O, tm + T_UE, ph, id_n64, 0u);
-            mma4_ts<16>(tm + T_O, tm + T_UE + LOWER, ph, id_n64, 1u);
-            mma4_ts<16>(tm + T_O, tm + T_UE, pl, id_n64, 1u);
+            if (outputs) {
+                const uint64_t ph = sdesc(smem_u32(sm + S_P), 128, 1024), pl = ph + (uint64_t)(BOX >> 4);
+                mma4_ts<16>(tm + T_O, tm + T_UE, ph, id_n64, 0u);
+                mma4_ts<16>(tm + T_O, tm + T_UE + LOWER, ph, id_n64, 1u);
+                mma4_ts<16>(tm + T_O, tm + T_UE, pl, id_n64, 1u);
+            }
             mma_commit_w(bar(B_MO));
             // T_U is free: the next chunk's U^T = V^T T^T
             if (c + 1 < chunks && !begin_chunk(c + 1)) break;
@@ -324,32 +382,39 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const uint8_t* rec = p.rec + (slot0 * p.HV + hv) * REC_BYTES;
         const int64_t rec_step = (int64_t)p.HV * REC_BYTES;
         int loaded = 0, loaded_p = 0;
+        auto load_p = [&](int cp) {                   // one of the arrivals that chunk cp's U waits for
+            loaded_p = cp + 1;
+            if (!outputs) {
+                mbar_arrive(bar(B_U));
+                return;
+            }
+            mbar_arrive_expect_tx(bar(B_U), P_BYTES);
+            bulk_load(smem_u32(sm + S_P), rec + cp * rec_step + REC_PH, P_BYTES, bar(B_U));
+        };
+        // Q is for the outputs; V is not for the transition
+        const uint32_t stage_bytes = STAGE - (outputs ? 0 : 2 * BOX) - (transition ? 2 * BOX : 0);
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
             // chunk c - 2's products (O's is the last) are complete: its stage is free, and P's buffer for chunk c - 1.
             // Its gates slot is that of chunk c + 2, which waits for a later output.
             if (c >= 2 && !wait(bar(B_MO), c & 1)) break;
             if (*(volatile int*)&s_abort) break;
-            auto load_p = [&](int cp) {
-                mbar_arrive_expect_tx(bar(B_U), P_BYTES);    // one of the arrivals that chunk cp's U waits for
-                bulk_load(smem_u32(sm + S_P), rec + cp * rec_step + REC_PH, P_BYTES, bar(B_U));
-                loaded_p = cp + 1;
-            };
             if (c >= 2) load_p(c - 1);
             const uint32_t base = smem_u32(sm + (c & 1) * STAGE), full = bar(B_FULL + (c & 1));
             const int y = begin + c * C;
             const uint8_t* r = rec + c * rec_step;
-            mbar_arrive_expect_tx(full, STAGE);
+            mbar_arrive_expect_tx(full, stage_bytes);
             const uint32_t gate = bar(B_GATE + c % GATE_SLOTS);
             mbar_arrive_expect_tx(gate, GATE_BYTES);
             bulk_load(smem_u32(sm + S_GATE) + (c % GATE_SLOTS) * GATE_BYTES, r + REC_NGAM, GATE_BYTES, gate);
+            if (!transition)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
+                for (int b = 0; b < 2; ++b) tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
             bulk_load(base + S_REC, r, REC_NGAM, full);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
-                tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
+                if (outputs) tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
             }
             loaded = c + 1;
             if (c == 0) load_p(0);
@@ -358,17 +423,15 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const int yn = begin + cn * C;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
+                    if (!transition) tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
                     tma_prefetch_2d(&mk, hk * D + 64 * b, yn);
-                    tma_prefetch_2d(&mq, hk * D + 64 * b, yn);
+                    if (outputs) tma_prefetch_2d(&mq, hk * D + 64 * b, yn);
                 }
-                bulk_prefetch(rec + cn * rec_step, REC_BYTES);
+                bulk_prefetch(rec + cn * rec_step, outputs ? REC_BYTES : REC_PH);
             }
         }
         if (loaded == chunks && chunks > 1 && wait(bar(B_MO), chunks & 1)) {     // the last chunk's P
-            mbar_arrive_expect_tx(bar(B_U), P_BYTES);
-            bulk_load(smem_u32(sm + S_P), rec + (chunks - 1) * rec_step + REC_PH, P_BYTES, bar(B_U));
-            loaded_p = chunks;
+            load_p(chunks - 1);
         }
         // everything loaded has landed before the end
         for (int c = max(0, loaded - STAGES); c < loaded; ++c)
@@ -385,16 +448,37 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     }
     if (s_abort) {             // a wait expired: no partial result passes for a real one
         const __nv_bfloat16 nan = __float2bfloat16_rn(__int_as_float(0x7fc00000));
-        for (int64_t e = tid; e < (int64_t)(end - begin) * D; e += NT)
-            p.o[((int64_t)(begin + e / D) * p.HV + hv) * D + e % D] = nan;
-        if (p.hT && row >= 0)
-            for (int e = tid; e < D * D; e += NT) p.hT[((int64_t)row * p.HV + hv) * D * D + e] = __int_as_float(0x7fc00000);
+        if (outputs)
+            for (int64_t e = tid; e < (int64_t)(end - begin) * D; e += NT)
+                p.o[((int64_t)(begin + e / D) * p.HV + hv) * D + e % D] = nan;
+        if (to)
+            for (int e = tid; e < D * D; e += NT) to[e] = __int_as_float(0x7fc00000);
     }
 }
 
 static DeviceFlags g_fwd_attr_done;
 
+// Segments per sequence.  A CTA of this kernel fills an SM, so at most as many
+// as make the first launch one wave; and the square root of the sequence's
+// chunks, as a segment costs about 4.5 us (its transition is joined to the
+// others in turn) and a chunk 2.5 us.  Whole call, one sequence, in one piece
+// and so, us: 8192 tokens 413 -> 335 at 32 heads, 348 -> 156 at 8, 325 -> 132
+// at 1 (8 segments 138, 16 141); 32768 tokens, 1 head 1236 -> 248.  At 2048
+// tokens 121 -> 124 at 32 heads and 102 -> 83 at 8, at 1024 70 -> 86 and
+// 62 -> 65: in one piece below 40 chunks.  Lengths are on the device: sequences
+// count by their average.
+static int segment_count(int64_t heads, int64_t tokens, int n_seq)
+{
+    const int64_t per_head = current_sm_count() / heads;         // CTAs of the first launch: 1 + 2 (segments - 2)
+    const int64_t chunks = tokens / n_seq / C;
+    const int64_t segments = std::min((per_head + 3) / 2, (int64_t)std::sqrt((double)chunks));
+    return chunks >= fw::MIN_CHUNKS && segments >= 3 ? (int)segments : 1;
+}
+
 }  // namespace gdn
+
+cudaError_t state_chain_launch(const float* M, const float* N, const float* h0, float* S_start, float* hT, int B, int P,
+                               int H, cudaStream_t stream);
 
 cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
@@ -430,15 +514,35 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
             !make_token_map(&mo, o, tokens, (int64_t)HV * D, (int64_t)HV * D, true))
             return cudaErrorInvalidValue;
         keep_pool_memory();
-        e = cudaMallocAsync(reinterpret_cast<void**>(&rec), (size_t)slot_count(a.seqs) * HV * REC_BYTES, stream);
+        const int64_t heads = (int64_t)N * HV, state = (int64_t)D * D;
+        a.segments = segment_count(heads, tokens, N);
+        const int64_t between = a.segments - 2;
+        const size_t rec_bytes = (size_t)slot_count(a.seqs) * HV * REC_BYTES;
+        const size_t states = a.segments > 1 ? (size_t)(heads * (2 + 3 * between) * state) : 0;
+        e = cudaMallocAsync(reinterpret_cast<void**>(&rec), rec_bytes + states * sizeof(float), stream);
         if (e != cudaSuccess) return e;
+        if (states) {
+            a.end0 = reinterpret_cast<float*>(rec + rec_bytes);
+            a.before_last = a.end0 + heads * state;
+            a.M = a.before_last + heads * state;
+            a.N = a.M + heads * between * state;
+            a.start = a.N + heads * between * state;
+        }
         e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, false, stream);
     }
     a.rec = rec;
-    if (e == cudaSuccess) {
-        forward_kernel<<<(unsigned)((int64_t)N * HV), fw::NT, fw::SMEM, stream>>>(mq, mk, mv, mo, a);
+    auto launch = [&](int pass, int64_t tasks) {
+        a.pass = pass;
+        forward_kernel<<<(unsigned)((int64_t)N * HV * tasks), fw::NT, fw::SMEM, stream>>>(mq, mk, mv, mo, a);
         note_launches(1);
-        e = cudaGetLastError();
+        return cudaGetLastError();
+    };
+    if (e == cudaSuccess && !a.end0) e = launch(fw::WHOLE, 1);
+    else if (e == cudaSuccess) {
+        const int between = a.segments - 2;
+        e = launch(fw::FIRST, 1 + 2 * between);
+        if (e == cudaSuccess) e = state_chain_launch(a.M, a.N, a.end0, a.start, a.before_last, N, between, HV, stream);
+        if (e == cudaSuccess) e = launch(fw::SECOND, between + 1);
     }
     if (rec) {
         const cudaError_t ef = cudaFreeAsync(rec, stream);

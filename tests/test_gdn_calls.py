@@ -67,6 +67,40 @@ def test_backward_waits_expire(monkeypatch, eight):
     check(run(x, LENS, dO, h0, dhT), gradients(x, LENS, dO, h0, dhT))
 
 
+@pytest.mark.parametrize("lens, heads", [((2600,), (16, 32)), ((5000,), (3, 3)), ((11000, 0, 1, 130), (2, 4)),
+                                         ((8300,), (1, 2))], ids=str)
+@pytest.mark.parametrize("decay", ["trained", "none"])
+def test_long_sequences_of_few_heads(lens, heads, decay):
+    """Sequences cut into segments that run at the same time, two or more per sequence."""
+    T, N = sum(lens), len(lens)
+    x, h0 = tokens(T, *heads, seed=82, decay=decay, beta=0.05 if decay == "none" else None), torch.randn(N, heads[1], D, D)
+    n0 = kda.launch_count()
+    S = h0.cuda()
+    o, _ = kda.gdn_chunk_fwd(*batch(on_gpu(x)), S, cu_seqlens=cu_of(lens).cuda(), hT=S, scale=D ** -0.5)
+    assert kda.launch_count() - n0 == 4                  # chunks, first segments, their states joined, the others
+    ro, rS = reference(x, lens, h0, scale=D ** -0.5)
+    # the start states add the rounding of a transition and of the product with it to the chunks' own
+    assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= 2 * TOL_S
+    assert kda.device_status() == kda.KDA_OK
+
+
+def test_segments_in_a_pool_and_expired(monkeypatch):
+    T, HK, HV = 4100, 2, 4
+    x, pool = tokens(T, HK, HV, seed=83), torch.randn(3, HV, D, D)
+    ro, rS = reference(x, [T], pool[2:])
+    for slot in (2, 3):
+        S = pool.cuda()
+        o, _ = kda.gdn_chunk_fwd(*batch(on_gpu(x)), S, cu_seqlens=cu_of([T]).cuda(), slots=torch.tensor([slot], dtype=torch.int32).cuda())
+        if slot == 2:
+            assert rel(o[0], ro) <= TOL_O and rel(S[2:], rS) <= 2 * TOL_S
+        assert torch.equal(S[:slot].cpu(), pool[:slot])
+    assert rel(o[0], reference(x, [T])[0]) <= TOL_O
+    monkeypatch.setenv("KDA_WAIT_LIMIT_NS", "0")
+    o, S = kda.gdn_chunk_fwd(*batch(on_gpu(x)))
+    expired()
+    assert torch.isnan(o.float()).all() and torch.isnan(S).all()
+
+
 def test_two_calls_at_once():
     """Each call has its own workspace: calls on two streams leave one another's results alone."""
     a, b = tokens(1500, 2, 4, seed=72), tokens(1500, 2, 4, seed=73)
