@@ -348,12 +348,15 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * Tokens behind a sequence's end inside its last 64-token chunk count as zero
  * whatever they hold.  Two launches: every chunk's state-free part for all
  * chunks at once, then one CTA per sequence and value head along the chunks.
- * K and Q enter the products as bf16, the state and what is computed as pairs
- * of bf16 with fp32 sums: hT is accurate to about 1e-5 of its norm.
- * Supported: d_k == d_v == 128.  Stream-ordered workspace of 66,560 bytes per
- * value head and 64-token chunk (at most tokens / 64 + N chunks);
- * KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in the prefill
- * (kda_device_status).
+ * Long sequences of few heads (40 chunks on average, at least three CTAs per
+ * sequence and head at once) are cut into segments instead: four launches, as
+ * kda_chunk_transition and kda_state_chain join segments.  K, Q and V enter
+ * the products as bf16, the state and what is computed as pairs of bf16 with
+ * fp32 sums: hT is accurate to about 1e-5 of its norm.  Supported: d_k == d_v
+ * == 128.  Stream-ordered workspace of 66,560 bytes per value head and
+ * 64-token chunk (at most tokens / 64 + N chunks), with segments up to 16.2 MB
+ * more on 148 SMs; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
+ * the prefill (kda_device_status).
  */
 int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                       const float* h0, void* o, float* hT, const int32_t* cu_seqlens, const int32_t* slots,
@@ -373,8 +376,8 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
  * atomics: the same inputs give the same bits.  Three launches (one more with
  * cu_seqlens); stream-ordered workspace of 263,168 bytes per value head and
- * 64-token chunk (KDA_ERR_NO_MEMORY if
- * it cannot be had).  Supported: d_k == d_v == 128.
+ * 64-token chunk (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
+ * the forward.  Supported: d_k == d_v == 128.
  *
  * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits
  * (kda_act_pack8, dense [tokens][HK or HV][128] and [..][4] scales): the

@@ -15,6 +15,12 @@ Raw C functions are exposed under their C names (every name in
 per request with the state after each) and ``chunk_bwd`` (the gradients).  They accept only contiguous CUDA
 tensors of the documented dtypes and shapes.
 
+The gated delta rule with one decay per head: ``gdn_chunk_fwd`` (packed
+sequences, grouped heads, pools of states), ``gdn_chunk_bwd`` and
+``gdn_decode_step``; their q, k and v may be slices of one projection's
+output.  ``act_pack8`` and ``act_unpack8`` keep activations in 8 bits
+(``Packed8``), which ``gdn_chunk_bwd`` also takes as they are.
+
 If the library is missing or cannot be loaded, every call raises
 ``KdaLibraryError``: there is no fallback implementation.
 """
@@ -37,7 +43,8 @@ KDA_ERR_NO_MEMORY = -5
 EXPORTED = ("kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_states", "kda_chunk_fwd_f32",
             "kda_chunk_transition", "kda_state_chain", "kda_chunk_fwd_raw", "kda_decode_step",
             "kda_decode_step_raw", "kda_verify_fwd", "kda_chunk_bwd", "kda_chunk_bwd_raw",
-            "kda_gdn_chunk_fwd", "kda_gdn_chunk_bwd", "kda_gdn_chunk_bwd_packed8", "kda_gdn_decode_step", "kda_act_pack8", "kda_act_unpack8",
+            "kda_gdn_chunk_fwd", "kda_gdn_chunk_bwd", "kda_gdn_chunk_bwd_packed8", "kda_gdn_decode_step",
+            "kda_act_pack8", "kda_act_unpack8",
             "kda_device_status", "kda_selftest_bounded_wait",
             "kda_status_string", "kda_launch_count", "kda_prefill_path", "kda_version")
 

@@ -65,13 +65,18 @@ __device__ __forceinline__ int64_t first_slot(const Seqs& s, int n)
     return (int64_t)(a / C) + n;
 }
 
-// Sequence and chunk of a slot; false if the slot belongs to none.
+// Sequence and chunk of a slot; false if the slot belongs to none.  Called by
+// whole warps: 32 sequences are looked at at once, a trip to memory for each
+// factor of 32 in their number.
 __device__ __forceinline__ bool slot_chunk(const Seqs& s, int64_t slot, int& n, int& chunk, int& begin, int& end)
 {
-    int lo = 0, hi = s.n_seq - 1;                    // the last n with first_slot(n) <= slot
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_slot(s, mid) <= slot) lo = mid; else hi = mid - 1;
+    int lo = 0;                                      // the last n with first_slot(n) <= slot
+    for (int count = s.n_seq; count > 1;) {
+        const int step = (count + 31) / 32, at = (int)(threadIdx.x & 31) * step;
+        const bool before = at < count && first_slot(s, lo + at) <= slot;
+        const int last = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0) * step;
+        lo += last;
+        count = min(step, count - last);
     }
     n = lo;
     seq_range(s, n, begin, end);

@@ -48,6 +48,25 @@ __device__ __forceinline__ void store_split(uint8_t* hi_dst, uint8_t* lo_dst, in
     }
 }
 
+// Warps 0 and 1.
+__device__ __forceinline__ void front_sync() { asm volatile("bar.sync 1, 64;" ::: "memory"); }
+
+// 16 lanes x 32 columns of tensor memory as matrix fragments: x[4 k ..] are the
+// lanes l / 4 (two columns 8 k + 2 (l % 4) ..) and l / 4 + 8 (likewise) of thread l.
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, float (&x)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]),
+                   "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+                 : "r"(taddr));
+}
+// Four 8 x 8 matrices of 16-bit values, transposed; thread l has the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_transposed(uint32_t addr, float a, float b, float c, float d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 :: "r"(addr), "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)) : "memory");
+}
+
 // fp32 products on the tensor cores: x = hi + lo with 11 significant bits in
 // hi, and hi hi + hi lo + lo hi.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
@@ -143,55 +162,22 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     uint8_t* rec = rec_all + (slot * HV + hv) * REC_BYTES;
     const uint32_t tile = smem_u32(sm), full = smem_u32(&bars[0]), done = smem_u32(&bars[1]);
 
-    if (tid == 0) {
-        mbar_init(full, 1);
-        mbar_init(done, 1);
-        fence_mbar_init();
-        s_abort = 0;
-        mbar_arrive_expect_tx(full, 4 * BOX);
-        for (int b = 0; b < 2; ++b) {
-            tma_load_2d(tile + 2 * b * BOX, &mk, hk * D + 64 * b, t0, full);
-            tma_load_2d(tile + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, t0, full);
-        }
-    }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(&s_tmem), C);
-        tmem_relinquish();
-    }
-    if (warp == 2) {                                  // running sum of g in 64 bits, two tokens per lane
-        double x[2];
-        for (int i = 0; i < 2; ++i) {
-            const int r = 2 * lane + i;
-            const int64_t at = (int64_t)(t0 + r) * HV + hv;
-            x[i] = r < nv ? (double)cut_decay(gate(g, at, gate_f32)) : 0.0;
-            const float b = r < nv ? gate(beta, at, gate_f32) : 0.f;
-            // the backward divides by beta: not below 2^-30
-            sB[r] = backward && r < nv && fabsf(b) < 0x1p-30f ? copysignf(0x1p-30f, b) : b;
-        }
-        double sum = x[0] + x[1];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += y;
-        }
-        for (int i = 0; i < 2; ++i) {
-            const double G = (i == 0 ? sum - x[1] : sum) * 1.4426950408889634;
-            const double last = __shfl_sync(0xffffffffu, sum, 31) * 1.4426950408889634;
-            // P / eta: exp(G_r - G_i) / exp(G_last - G_i), the latter not below its floor
-            const double c = backward ? G : last - G > (double)ETA_FLOOR_LOG2 ? last : G + (double)ETA_FLOOR_LOG2;
-            sGh[2 * lane + i] = (float)G;
-            sGl[2 * lane + i] = (float)(G - (double)(float)G);
-            sCh[2 * lane + i] = (float)c;
-            sCl[2 * lane + i] = (float)(c - (double)(float)c);
-        }
-    }
-    fence_before_sync();
-    __syncthreads();
-    fence_after_sync();
-    const uint32_t tm = s_tmem;
-    const Waits wait = {&s_abort, &g_prep_status, wait_ns};
     bool issued = false;
-    if (warp == 0) {
+    const Waits wait = {&s_abort, &g_prep_status, wait_ns};
+    if (warp == 0) {                                  // [K; Q] K^T, while warp 2 has the gates
+        if (lane == 0) {
+            mbar_init(full, 1);
+            mbar_init(done, 1);
+            fence_mbar_init();
+            s_abort = 0;
+            mbar_arrive_expect_tx(full, 4 * BOX);
+            for (int b = 0; b < 2; ++b) {
+                tma_load_2d(tile + 2 * b * BOX, &mk, hk * D + 64 * b, t0, full);
+                tma_load_2d(tile + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, t0, full);
+            }
+        }
+        front_sync();                                 // tensor memory is there
+        fence_after_sync();
         const bool here = wait(full, 0);
         if (!here) mbar_wait(full, 0, DRAIN_NS);      // the loads land before their space is used again
         if (nv < C) {                                 // rows behind the sequence: whatever is there counts as zero
@@ -202,18 +188,56 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             fence_smem_to_async();
             __syncwarp();
         }
-        if (__all_sync(0xffffffffu, here)) {
-            // [K; Q] K^T: K K^T in lanes 0-63, Q K^T in lanes 64-127
+        if (__all_sync(0xffffffffu, here)) {          // K K^T in lanes 0-63, Q K^T in lanes 64-127
             constexpr uint32_t id = idesc_bf16(128, C);
-            mma4_ss<2, 2>(tm, sdesc_sw128(tile), sdesc_sw128(tile), id, 0u);
-            mma4_ss<2, 2>(tm, sdesc_sw128(tile + 2 * BOX), sdesc_sw128(tile + 2 * BOX), id, 1u);
+            const uint32_t d = s_tmem;
+            mma4_ss<2, 2>(d, sdesc_sw128(tile), sdesc_sw128(tile), id, 0u);
+            mma4_ss<2, 2>(d, sdesc_sw128(tile + 2 * BOX), sdesc_sw128(tile + 2 * BOX), id, 1u);
             mma_commit_w(done);
             if (!wait(done, 0)) mbar_wait(done, 0, DRAIN_NS);
             issued = true;
         }
+    } else if (warp == 1) {
+        tmem_alloc(smem_u32(&s_tmem), C);
+        tmem_relinquish();
+        fence_before_sync();
+        front_sync();
+    } else if (warp == 2) {                           // running sum of g in 64 bits, two tokens per lane
+        const int64_t at = (int64_t)(t0 + 2 * lane) * HV + hv;
+        const bool real[2] = {2 * lane < nv, 2 * lane + 1 < nv};
+        float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
+        auto load = [&](bool f32) {                   // all loads at once, whatever the type
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (real[i]) gi[i] = gate(g, at + i * HV, f32), bi[i] = gate(beta, at + i * HV, f32);
+        };
+        if (gate_f32) load(true); else load(false);
+        const double x0 = (double)cut_decay(gi[0]), x1 = (double)cut_decay(gi[1]);
+        double sum = x0 + x1;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += y;
+        }
+        const double last = __shfl_sync(0xffffffffu, sum, 31) * 1.4426950408889634;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 2 * lane + i;
+            const double G = (i == 0 ? sum - x1 : sum) * 1.4426950408889634;
+            // P / eta: exp(G_r - G_i) / exp(G_last - G_i), the latter not below its floor
+            const double c = backward ? G : last - G > (double)ETA_FLOOR_LOG2 ? last : G + (double)ETA_FLOOR_LOG2;
+            sGh[r] = (float)G;
+            sGl[r] = (float)(G - (double)(float)G);
+            sCh[r] = (float)c;
+            sCl[r] = (float)(c - (double)(float)c);
+            // the backward divides by beta: not below 2^-30
+            sB[r] = backward && real[i] && fabsf(bi[i]) < 0x1p-30f ? copysignf(0x1p-30f, bi[i]) : bi[i];
+        }
     }
+    fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    const uint32_t tm = s_tmem;
     float* x00 = reinterpret_cast<float*>(sm + B00);
     float* x10 = reinterpret_cast<float*>(sm + B10);
     float* x11 = reinterpret_cast<float*>(sm + B11);
@@ -261,31 +285,23 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             }
         }
     }
-    if (tid < C) {
-        const float gh = sGh[tid], gl = sGl[tid], gam = exp2f(gh + gl);
-        const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
-        // a wait that expired leaves NaN in the state, the outputs and the gradients
-        const bool bad = s_abort != 0;
-        const float nan = __int_as_float(0x7fc00000);
-        reinterpret_cast<float*>(rec + REC_NGAM)[tid] = bad ? nan : -gam;
-        reinterpret_cast<float*>(rec + REC_ETA)[tid] = bad ? nan : exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
-        reinterpret_cast<float*>(rec + REC_GQ)[tid] = bad ? nan : scale * gam;
-        reinterpret_cast<float*>(rec + REC_BETA)[tid] = sB[tid];
-        sNG[tid] = -gam;
-    }
-    fence_before_sync();
-    __syncthreads();
-    {   // the 16 x 16 diagonal blocks, one per warp: forward substitution, one column per thread (lanes 16-31 repeat
-        // lanes 0-15), its values in registers and the rows of A as broadcast reads
-        float* blk = warp < 2 ? x00 : x11;
-        const int o = 16 * (warp & 1), j = lane & 15;
+    if (warp < 2) {
+        // the 16 x 16 diagonal blocks of this warp's rows: forward substitution, one column per lane, its values in
+        // registers and the rows of A as broadcast reads (half h is 16 rows and 16 columns on, where the groups of
+        // columns are permuted by 4 more)
+        __syncwarp();
+        float* blk = warp ? x11 : x00;
+        const int h = lane >> 4, j = lane & 15;
+        const float* up = blk + h * (16 * 32 + 16);
+        const float* down = blk + h * (16 * 32 - 16);
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < r; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(blk + at(o + r, o + i));
+                const int piece = (i >> 2) ^ swz(r);
+                const float4 v = *reinterpret_cast<const float4*>((piece & 4 ? down : up) + r * 32 + 4 * piece);
                 s[0] = fmaf(v.x, x[i], s[0]);
                 if (i + 1 < r) s[1] = fmaf(v.y, x[i + 1], s[1]);
                 if (i + 2 < r) s[2] = fmaf(v.z, x[i + 2], s[2]);
@@ -294,10 +310,22 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             x[r] = r == j ? 1.f : r > j ? -((s[0] + s[1]) + (s[2] + s[3])) : 0.f;
         }
         __syncwarp();
-        if (lane < 16)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) blk[at(o + r, o + j)] = x[r];
+        for (int r = 0; r < 16; ++r) blk[at(16 * h + r, 16 * h + j)] = x[r];
+    } else {
+        const int r = tid - C;
+        const float gh = sGh[r], gl = sGl[r], gam = exp2f(gh + gl);
+        const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
+        // a wait that expired leaves NaN in the state, the outputs and the gradients
+        const bool bad = s_abort != 0;
+        const float nan = __int_as_float(0x7fc00000);
+        reinterpret_cast<float*>(rec + REC_NGAM)[r] = bad ? nan : -gam;
+        reinterpret_cast<float*>(rec + REC_ETA)[r] = bad ? nan : exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
+        reinterpret_cast<float*>(rec + REC_GQ)[r] = bad ? nan : scale * gam;
+        reinterpret_cast<float*>(rec + REC_BETA)[r] = sB[r];
+        sNG[r] = -gam;
     }
+    fence_before_sync();
     __syncthreads();
     // blocks next to one another: X10 = -X11 (A10 X00), of 16 and then of 32; every warp takes 8 columns
     {
@@ -345,24 +373,22 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     __syncthreads();
     fence_after_sync();
-    {   // thread: channel `tid`, all 64 rows, as two planes of swizzled boxes
-        uint8_t* dst = sm + (tid / 64) * BOX + (tid % 8) * 2;
-        const int piece = (tid % 64) / 8;
+    {   // -W^T to two planes of swizzled boxes, 8 channels x 8 tokens at a time through transposing matrix stores: a
+        // thread has two neighbouring tokens of a channel, of one 8 channels on, and of both the lower plane
+        const int token = lane & 7, octet = (lane >> 3) & 1, plane = lane >> 4;
 #pragma unroll 1
-        for (int col = 0; col < C; col += 16) {
+        for (int q = 0; q < 4; ++q) {
+            const int ch = 32 * warp + 16 * (q >> 1), col = 32 * (q & 1);
+            const uint32_t dst = tile + (2 * plane + ch / 64) * BOX + (col + token) * 128 + ((((ch % 64) / 8 + octet) ^ token) * 16);
             float x[16];
-            tmem_ld16(tm + ((uint32_t)(32 * warp) << 16) + col, x);
+            tmem_ld_16x256b(tm + ((uint32_t)ch << 16) + col, x);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float hi, lo;
-                split_bf16(x[i], x[i + 1], hi, lo);
-                uint8_t* a = dst + (col + i) * 128 + ((piece ^ (i & 7)) * 16);
-                uint8_t* b = dst + (col + i + 1) * 128 + ((piece ^ ((i + 1) & 7)) * 16);
-                *reinterpret_cast<uint16_t*>(a) = (uint16_t)__float_as_uint(hi);
-                *reinterpret_cast<uint16_t*>(b) = (uint16_t)(__float_as_uint(hi) >> 16);
-                *reinterpret_cast<uint16_t*>(a + 2 * BOX) = (uint16_t)__float_as_uint(lo);
-                *reinterpret_cast<uint16_t*>(b + 2 * BOX) = (uint16_t)(__float_as_uint(lo) >> 16);
+            for (int k = 0; k < 4; ++k) {
+                float hi[2], lo[2];
+                split_bf16(x[4 * k], x[4 * k + 1], hi[0], lo[0]);
+                split_bf16(x[4 * k + 2], x[4 * k + 3], hi[1], lo[1]);
+                store_transposed(dst + k * 8 * 128, hi[0], hi[1], lo[0], lo[1]);
             }
         }
     }
