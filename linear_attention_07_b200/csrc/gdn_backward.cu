@@ -28,6 +28,15 @@
 // All that passes between products is a pair of bf16, as in the forward: a
 // single rounding would show in dg and dbeta, which are few numbers each from
 // a long sum.
+//
+// 8192 tokens x 32 heads (16 query/key heads): chains 550 us (4.2 us a chunk;
+// the reverse chain is the longer one, two products in turn, one of them over
+// dU in two steps, and 96 KB to store, which an SM does at about 32 bytes a
+// cycle), local 338 us (10 us per value head: the pair products and the states'
+// read shared memory at its rate, 128 bytes a cycle, for 7,000 of 18,000 cycles,
+// and the sums over the results take the rest).  The local kernel with one role
+// that did everything in turn took 410 us; with 16 computing warps of 16 columns
+// each in place of 8 of 32, 390 against 364 us at that time.
 #include "gdn_chunk.cuh"
 
 namespace kda {

@@ -58,17 +58,17 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(x);
 }
 
-// The 8-bit form (act8.cu): a block's scale 2^(s - 127) (s = 255: NaN), and 16
-// e4m3 values times it as 16 bf16, exact (e4m3 has 4 significant bits).
+// The 8-bit form (act8.cu): a block's scale 2^(s - 127) (s = 255: NaN), and 8
+// e4m3 values times it as 8 bf16, exact (e4m3 has 4 significant bits).
 __device__ __forceinline__ float act8_scale(uint32_t s)
 {
     return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7fc00000u : s << 23);
 }
-__device__ __forceinline__ void act8_expand(const uint4& x, float scale, uint32_t (&out)[8])
+__device__ __forceinline__ void act8_expand(const uint2& x, float scale, uint32_t (&out)[4])
 {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint32_t w[2] = {x.x, x.y};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e / 2] >> (16 * (e & 1))), __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
         const __nv_bfloat162 b = __floats2bfloat162_rn(f.x * scale, f.y * scale);
