@@ -323,12 +323,9 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         const int r = tid - C;
         const float gh = sGh[r], gl = sGl[r], gam = exp2f(gh + gl);
         const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
-        // a wait that expired leaves NaN in the state, the outputs and the gradients
-        const bool bad = s_abort != 0;
-        const float nan = __int_as_float(0x7fc00000);
-        reinterpret_cast<float*>(rec + REC_NGAM)[r] = bad ? nan : -gam;
-        reinterpret_cast<float*>(rec + REC_ETA)[r] = bad ? nan : exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
-        reinterpret_cast<float*>(rec + REC_GQ)[r] = bad ? nan : scale * gam;
+        reinterpret_cast<float*>(rec + REC_NGAM)[r] = -gam;
+        reinterpret_cast<float*>(rec + REC_ETA)[r] = exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
+        reinterpret_cast<float*>(rec + REC_GQ)[r] = scale * gam;
         reinterpret_cast<float*>(rec + REC_BETA)[r] = sB[r];
         sNG[r] = -gam;
     }
@@ -406,6 +403,10 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         bulk_store(rec + REC_WH, tile, 4 * BOX);
         bulk_commit();
         bulk_wait_read_all();
+    }
+    // a wait that expired leaves NaN in the state, the outputs and the gradients
+    if (s_abort && tid >= C) {
+        for (uint32_t at : {REC_NGAM, REC_ETA, REC_GQ}) reinterpret_cast<float*>(rec + at)[tid - C] = __int_as_float(0x7fc00000);
     }
     if (warp == 1) {
         fence_after_sync();
