@@ -348,14 +348,14 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * Tokens behind a sequence's end inside its last 64-token chunk count as zero
  * whatever they hold.  Two launches: every chunk's state-free part for all
  * chunks at once, then one CTA per sequence and value head along the chunks.
- * Long sequences of few heads (40 chunks on average, at least three CTAs per
- * sequence and head at once) are cut into segments instead: four launches, as
- * kda_chunk_transition and kda_state_chain join segments.  K, Q and V enter
+ * Long sequences of few heads (32 chunks on average, at least three CTAs per
+ * sequence and head at once) are cut into segments instead, joined as
+ * kda_state_chain joins them: four launches.  K, Q and V enter
  * the products as bf16, the state and what is computed as pairs of bf16 with
  * fp32 sums: hT is accurate to about 1e-5 of its norm.  Supported: d_k == d_v
  * == 128.  Stream-ordered workspace of 66,560 bytes per value head and
- * 64-token chunk (at most tokens / 64 + N chunks), with segments up to 16.2 MB
- * more on 148 SMs; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
+ * 64-token chunk (at most tokens / 64 + N chunks), with segments up to half as
+ * much again; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
  * the prefill (kda_device_status).
  */
 int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,

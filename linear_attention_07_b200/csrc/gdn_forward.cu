@@ -81,15 +81,17 @@ constexpr uint32_t T_UE = 192;                       // (eta U)^T
 constexpr uint32_t T_XQ = 256, T_O = 320;
 constexpr uint32_t T_D = 384;                        // (K^T eta U)^T
 
-// A sequence in one piece; or in segments, of which the first of two launches
-// runs segment 0 and, for each of the segments between it and the last, the
-// state that it reaches from zero and its transition (from the identity with V =
-// 0; neither has outputs), and the second launch runs all but segment 0 from
-// their start states.
+// A sequence runs in one piece; or, if it has min_chunks chunks, in segments, of
+// which the first of two launches runs segment 0 and, for each of the segments
+// between it and the last, the state that it reaches from zero and its
+// transition (from the identity with V = 0; neither has outputs).
+// join_kernel makes the start states of these, and the second launch runs all
+// but segment 0 from them.  The first launch has the sequences in one piece
+// behind those in segments.
 enum Pass { WHOLE, FIRST, SECOND };
 // Segment 0 counts 8 of the others' 10: its outputs are made while theirs are not.
 constexpr int SEG_FIRST = 8, SEG_OTHER = 10;
-constexpr int MIN_CHUNKS = 40;                       // of a sequence in segments
+constexpr int MIN_CHUNKS = 32;                       // of a sequence in segments
 
 struct Args {
     Seqs seqs;
@@ -97,14 +99,105 @@ struct Args {
     const float* h0;
     float* hT;
     __nv_bfloat16* o;
-    // [n_seq][HV][D][D] the state behind segment 0 and that before the last; [n_seq][segments - 2][HV][D][D] the
+    // [n_long][HV][D][D] the state behind segment 0 and that before the last; [n_long][segments - 2][HV][D][D] the
     // transitions, the states reached from zero and the start states of those between
     float *end0, *before_last, *M, *N, *start;
-    int pass, segments;
+    int pass, segments, min_chunks, n_long;          // at most n_long sequences are in segments
     int HK, HV;
     float scale;
     uint64_t wait_ns;
 };
+
+__device__ __forceinline__ int chunk_count(const Seqs& s, int n)
+{
+    int begin, end;
+    seq_range(s, n, begin, end);
+    return (end - begin + C - 1) / C;
+}
+
+// The l-th sequence of min_chunks chunks or more, or -1; by whole warps.
+__device__ __forceinline__ int long_sequence(const Seqs& s, int min_chunks, int l)
+{
+    for (int first = 0; first < s.n_seq; first += 32) {
+        const int n = first + (int)(threadIdx.x & 31);
+        uint32_t m = __ballot_sync(0xffffffffu, n < s.n_seq && chunk_count(s, n) >= min_chunks);
+        const int count = __popc(m);
+        if (l < count) {
+            for (; l > 0; --l) m &= m - 1;
+            return first + __ffs(m) - 1;
+        }
+        l -= count;
+    }
+    return -1;
+}
+
+// start_{p+1} = M_p start_p + N_p in fp32 for 32 columns of one head, a step
+// after the other; M_{p+1} is on its way in registers meanwhile.  Thread: rows
+// tid / 8 + 32 r, columns 4 (tid % 8) .. + 3.
+constexpr int JOIN_NT = 256, JOIN_COLS = 32, JOIN_LD = D + 4;
+constexpr uint32_t JOIN_SMEM = (D * JOIN_LD + D * JOIN_COLS) * 4;
+
+__global__ void __launch_bounds__(JOIN_NT)
+join_kernel(const Args p)
+{
+    extern __shared__ __align__(16) float jsm[];
+    float* m = jsm;                                  // [D][JOIN_LD]
+    float* st = jsm + D * JOIN_LD;                   // [D][JOIN_COLS]
+    const int tid = threadIdx.x, l = blockIdx.y / p.HV, hv = blockIdx.y % p.HV, between = p.segments - 2;
+    if (long_sequence(p.seqs, p.min_chunks, l) < 0) return;
+    const int row = tid / 8, cs = 4 * (tid % 8), col = blockIdx.x * JOIN_COLS + cs;
+    const int64_t head = ((int64_t)l * p.HV + hv) * D * D;
+    auto mid = [&](int k) { return (((int64_t)l * between + k) * p.HV + hv) * D * D; };
+    float4 next[D * D / 4 / JOIN_NT], cur[4];
+    auto load = [&](int k) {
+        const float4* src = reinterpret_cast<const float4*>(p.M + mid(k));
+#pragma unroll
+        for (int u = 0; u < D * D / 4 / JOIN_NT; ++u) next[u] = src[u * JOIN_NT + tid];
+    };
+    load(0);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) cur[r] = *reinterpret_cast<const float4*>(p.end0 + head + (row + 32 * r) * D + col);
+#pragma unroll 1
+    for (int k = 0; k < between; ++k) {
+        float4 acc[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int64_t at = mid(k) + (row + 32 * r) * D + col;
+            acc[r] = *reinterpret_cast<const float4*>(p.N + at);
+            *reinterpret_cast<float4*>(p.start + at) = cur[r];
+        }
+        __syncthreads();                             // the last step has read m and st
+#pragma unroll
+        for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(st + (row + 32 * r) * JOIN_COLS + cs) = cur[r];
+#pragma unroll
+        for (int u = 0; u < D * D / 4 / JOIN_NT; ++u) {
+            const int e = 4 * (u * JOIN_NT + tid);
+            *reinterpret_cast<float4*>(m + e / D * JOIN_LD + e % D) = next[u];
+        }
+        __syncthreads();
+        if (k + 1 < between) load(k + 1);
+#pragma unroll 4
+        for (int i = 0; i < D; i += 4) {
+            float4 x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float4*>(st + (i + e) * JOIN_COLS + cs);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 a = *reinterpret_cast<const float4*>(m + (row + 32 * r) * JOIN_LD + i);
+                const float f[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[r].x = fmaf(f[e], x[e].x, acc[r].x); acc[r].y = fmaf(f[e], x[e].y, acc[r].y);
+                    acc[r].z = fmaf(f[e], x[e].z, acc[r].z); acc[r].w = fmaf(f[e], x[e].w, acc[r].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) cur[r] = acc[r];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(p.before_last + head + (row + 32 * r) * D + col) = cur[r];
+}
 
 }  // namespace fw
 
@@ -122,23 +215,27 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int hv = blockIdx.x % p.HV, between = p.segments - 2;
-    const int tasks = p.pass == WHOLE ? 1 : p.pass == FIRST ? 1 + 2 * between : between + 1;
-    const int task = (blockIdx.x / p.HV) % tasks, n = blockIdx.x / (p.HV * tasks);
+    const int tasks = p.pass == WHOLE ? 0 : p.pass == FIRST ? 1 + 2 * between : between + 1;
+    const int in_segments = p.n_long * tasks, at = blockIdx.x / p.HV - in_segments;
+    const bool whole = at >= 0;
+    const int l = whole ? 0 : (at + in_segments) / tasks, task = whole ? 0 : (at + in_segments) % tasks;
+    const int n = whole ? at : long_sequence(p.seqs, p.min_chunks, l);
+    if (n < 0 || (whole && p.pass == FIRST && chunk_count(p.seqs, n) >= p.min_chunks)) return;
     const int hk = hv / (p.HV / p.HK);
     int begin, end;
     seq_range(p.seqs, n, begin, end);
     int chunks = (end - begin + C - 1) / C;
     int64_t slot0 = (int64_t)(begin / C) + n;
     const int row = state_row(p.seqs, n);
-    const int64_t head = ((int64_t)n * p.HV + hv) * D * D, pool = ((int64_t)row * p.HV + hv) * D * D;
+    const int64_t head = ((int64_t)l * p.HV + hv) * D * D, pool = ((int64_t)row * p.HV + hv) * D * D;
     // where the state comes from and goes to; whether outputs are made, and whether V counts as zero and the state
     // begins as the identity
     const float* from = p.h0 && row >= 0 ? p.h0 + pool : nullptr;
     float* to = p.hT && row >= 0 ? p.hT + pool : nullptr;
     bool outputs = true, transition = false;
-    if (p.pass != WHOLE) {
+    if (!whole) {
         const int seg = p.pass == SECOND ? 1 + task : (task + 1) / 2;
-        const int64_t mid = (((int64_t)n * between + seg - 1) * p.HV + hv) * D * D;
+        const int64_t mid = (((int64_t)l * between + seg - 1) * p.HV + hv) * D * D;
         if (p.pass == SECOND) {
             from = seg <= between ? p.start + mid : p.before_last + head;
             if (seg <= between) to = nullptr;
@@ -465,27 +562,30 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 
 static DeviceFlags g_fwd_attr_done;
 
-// Segments per sequence.  A CTA of this kernel fills an SM, so at most as many
-// as make the first launch one wave; and the square root of the sequence's
-// chunks, as a segment costs about 4.5 us (its transition is joined to the
+// Segments of a call's long sequences: where all SMs take three CTAs and more
+// per sequence and head (a CTA of this kernel fills one), as many as make the
+// first launch one wave; and at most the square root of the sequences' average
+// of chunks, as a segment costs about 4 us (its transition is joined to the
 // others in turn) and a chunk 2.5 us.  Whole call, one sequence, in one piece
-// and so, us: 8192 tokens 413 -> 335 at 32 heads, 348 -> 156 at 8, 325 -> 132
-// at 1 (8 segments 138, 16 141); 32768 tokens, 1 head 1236 -> 248.  At 2048
-// tokens 121 -> 124 at 32 heads and 102 -> 83 at 8, at 1024 70 -> 86 and
-// 62 -> 65: in one piece below 40 chunks.  Lengths are on the device: sequences
-// count by their average.
-static int segment_count(int64_t heads, int64_t tokens, int n_seq)
+// and so, us: 8192 tokens 404 -> 313 at 32 heads, 345 -> 152 at 8, 324 -> 129 at
+// 1 (8 segments 136, 16 139); 32768 tokens of 1 head 1233 -> 240; 2048 tokens
+// 117 -> 110 at 32 heads, 101 -> 83 at 8; 1024 tokens 68 -> 74 and 63 -> 67: in
+// one piece below 32 chunks on average (lengths are on the device).  With
+// more heads a batch's longest sequences gained nothing so, even where they
+// took most of the call (16 prompts x 16 heads with one of 4096 tokens, the next
+// of 2500 and 2047: 173 us of this kernel in one piece, 220 in four segments).
+static void choose_segments(fw::Args& a, int64_t heads, bool ragged)
 {
-    const int64_t per_head = current_sm_count() / heads;         // CTAs of the first launch: 1 + 2 (segments - 2)
-    const int64_t chunks = tokens / n_seq / C;
-    const int64_t segments = std::min((per_head + 3) / 2, (int64_t)std::sqrt((double)chunks));
-    return chunks >= fw::MIN_CHUNKS && segments >= 3 ? (int)segments : 1;
+    const int64_t chunks = a.seqs.tokens / C / a.seqs.n_seq;
+    const int64_t segments = std::min((current_sm_count() / heads + 3) / 2, (int64_t)std::sqrt((double)chunks));
+    if (chunks < fw::MIN_CHUNKS || segments < 3) return;
+    a.segments = (int)segments;
+    a.min_chunks = fw::MIN_CHUNKS;
+    // all of equal lengths, or as many as the tokens can make
+    a.n_long = ragged ? (int)std::min<int64_t>(a.seqs.n_seq, a.seqs.tokens / ((fw::MIN_CHUNKS - 1) * C + 1)) : a.seqs.n_seq;
 }
 
 }  // namespace gdn
-
-cudaError_t state_chain_launch(const float* M, const float* N, const float* h0, float* S_start, float* hT, int B, int P,
-                               int H, cudaStream_t stream);
 
 cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
@@ -508,7 +608,9 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
     a.scale = scale;
     a.wait_ns = bounded_wait_limit_ns();
     cudaError_t e = once_per_device(g_fwd_attr_done, [](int) {
-        return cudaFuncSetAttribute(forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fw::SMEM);
+        const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
+        const cudaError_t r = cudaFuncSetAttribute(forward_kernel, at, (int)fw::SMEM);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(fw::join_kernel, at, (int)fw::JOIN_SMEM);
     });
     if (e != cudaSuccess) return e;
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
@@ -521,11 +623,10 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
             !make_token_map(&mo, o, tokens, (int64_t)HV * D, (int64_t)HV * D, true))
             return cudaErrorInvalidValue;
         keep_pool_memory();
-        const int64_t heads = (int64_t)N * HV, state = (int64_t)D * D;
-        a.segments = segment_count(heads, tokens, N);
-        const int64_t between = a.segments - 2;
+        choose_segments(a, (int64_t)N * HV, cu != nullptr);
+        const int64_t heads = (int64_t)a.n_long * HV, state = (int64_t)D * D, between = a.segments - 2;
         const size_t rec_bytes = (size_t)slot_count(a.seqs) * HV * REC_BYTES;
-        const size_t states = a.segments > 1 ? (size_t)(heads * (2 + 3 * between) * state) : 0;
+        const size_t states = heads > 0 ? (size_t)(heads * (2 + 3 * between) * state) : 0;
         e = cudaMallocAsync(reinterpret_cast<void**>(&rec), rec_bytes + states * sizeof(float), stream);
         if (e != cudaSuccess) return e;
         if (states) {
@@ -538,18 +639,23 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, false, stream);
     }
     a.rec = rec;
-    auto launch = [&](int pass, int64_t tasks) {
+    auto launch = [&](int pass, int64_t blocks) {
         a.pass = pass;
-        forward_kernel<<<(unsigned)((int64_t)N * HV * tasks), fw::NT, fw::SMEM, stream>>>(mq, mk, mv, mo, a);
+        forward_kernel<<<(unsigned)blocks, fw::NT, fw::SMEM, stream>>>(mq, mk, mv, mo, a);
         note_launches(1);
         return cudaGetLastError();
     };
-    if (e == cudaSuccess && !a.end0) e = launch(fw::WHOLE, 1);
-    else if (e == cudaSuccess) {
-        const int between = a.segments - 2;
-        e = launch(fw::FIRST, 1 + 2 * between);
-        if (e == cudaSuccess) e = state_chain_launch(a.M, a.N, a.end0, a.start, a.before_last, N, between, HV, stream);
-        if (e == cudaSuccess) e = launch(fw::SECOND, between + 1);
+    if (e == cudaSuccess && a.n_long == 0) {
+        e = launch(fw::WHOLE, (int64_t)N * HV);
+    } else if (e == cudaSuccess) {
+        const int64_t between = a.segments - 2, heads = (int64_t)a.n_long * HV;
+        e = launch(fw::FIRST, heads * (1 + 2 * between) + (cu ? (int64_t)N * HV : 0));
+        if (e == cudaSuccess) {
+            fw::join_kernel<<<dim3(D / fw::JOIN_COLS, (unsigned)heads), fw::JOIN_NT, fw::JOIN_SMEM, stream>>>(a);
+            note_launches(1);
+            e = cudaGetLastError();
+        }
+        if (e == cudaSuccess) e = launch(fw::SECOND, heads * (between + 1));
     }
     if (rec) {
         const cudaError_t ef = cudaFreeAsync(rec, stream);

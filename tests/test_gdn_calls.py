@@ -84,6 +84,26 @@ def test_long_sequences_of_few_heads(lens, heads, decay):
     assert kda.device_status() == kda.KDA_OK
 
 
+@pytest.mark.parametrize("lens, heads", [((30, 9000, 1, 4000), (2, 4)), ((5200, 0, 40, 5300), (1, 2))], ids=str)
+def test_long_sequences_in_a_ragged_batch(lens, heads):
+    """The long ones go in segments, the others in one piece; a pool in another order, with a row missing."""
+    T, N = sum(lens), len(lens)
+    x, pool = tokens(T, *heads, seed=84), torch.randn(N + 2, heads[1], D, D)
+    slots = torch.randperm(N + 2, generator=torch.Generator().manual_seed(85))[:N].int()
+    slots[2] = -1
+    kept = [n for n in range(N) if n != 2]
+    h0 = torch.where((slots >= 0)[:, None, None, None], pool[slots.long()], 0.0)
+    n0 = kda.launch_count()
+    S = pool.cuda()
+    o, _ = kda.gdn_chunk_fwd(*batch(on_gpu(x)), S, cu_seqlens=cu_of(lens).cuda(), slots=slots.cuda())
+    assert kda.launch_count() - n0 == 4
+    ro, rS = reference(x, lens, h0)
+    assert rel(o[0], ro) <= TOL_O and rel(S[slots.long()[kept]], rS[kept]) <= 2 * TOL_S
+    rest = [r for r in range(N + 2) if r not in slots.tolist()]
+    assert torch.equal(S[rest].cpu(), pool[rest])
+    assert kda.device_status() == kda.KDA_OK
+
+
 def test_segments_in_a_pool_and_expired(monkeypatch):
     T, HK, HV = 4100, 2, 4
     x, pool = tokens(T, HK, HV, seed=83), torch.randn(3, HV, D, D)
