@@ -547,7 +547,7 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slot
     starts from row slots[n] and its last state is written there; a slot
     outside the pool starts from zero and keeps none.  Rows of o that belong to
     no sequence are not written.  Returns (o, hT), hT the pool with slots."""
-    torch = _types()
+    _types()
     B, T, HK, dk = q.shape
     HV, dv = v.shape[-2:]
     dev = _require_cuda(q)
@@ -568,9 +568,9 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slot
     state = (rows, HV, dk, dv)
     hp = None if h0 is None else _dense(h0, "h0", _F32, state, dev)
     if o is None:
-        o = torch.empty((B, T, HV, dv), dtype=_BF16, device=dev)
+        o = v.new_empty((B, T, HV, dv))
     if hT is None and output_final_state:
-        hT = torch.empty(state, dtype=_F32, device=dev)
+        hT = v.new_empty(state, dtype=_F32)
     _call("kda_gdn_chunk_fwd", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp, hp,
           _dense(o, "o", _BF16, (B, T, HV, dv), dev), None if hT is None else _dense(hT, "hT", _F32, state, dev),
           None if cu_seqlens is None else cu_seqlens.data_ptr(), sp, rows, scale, N, Tc, HK, HV, dk, dv, qs, ks, vs, gf)
@@ -587,7 +587,7 @@ def gdn_chunk_bwd(q, k, v, g, beta, h0, dO, dhT=None, *, scale=1.0, cu_seqlens=N
     dk (summed over the value heads of a group), dv, dg, dbeta are bf16, dh0 is
     fp32 (None if want_dh0 is False).  Tokens that belong to no sequence get
     zero gradients."""
-    torch = _types()
+    _types()
     eight = isinstance(q, Packed8)
     if isinstance(k, Packed8) != eight or isinstance(v, Packed8) != eight:
         raise TypeError("q, k and v must all be tensors or all be Packed8")
@@ -604,10 +604,9 @@ def gdn_chunk_bwd(q, k, v, g, beta, h0, dO, dhT=None, *, scale=1.0, cu_seqlens=N
     gp, bp, gf = _check_gates(g, beta, (B, T, HV), dev)
     N, Tc = _gdn_sequences(B, T, cu_seqlens, dev)
     state = (N, HV, dk, dv)
-    bf = dict(dtype=_BF16, device=dev)
-    gq, gk = torch.empty((B, T, HK, dk), **bf), torch.empty((B, T, HK, dk), **bf)
-    gv, gg, gb = torch.empty((B, T, HV, dv), **bf), torch.empty((B, T, HV), **bf), torch.empty((B, T, HV), **bf)
-    gh = torch.empty(state, dtype=_F32, device=dev) if want_dh0 else None
+    gq, gk, gv, gg, gb = (dO.new_empty(shape, dtype=_BF16) for shape in
+                          ((B, T, HK, dk), (B, T, HK, dk), (B, T, HV, dv), (B, T, HV), (B, T, HV)))
+    gh = dO.new_empty(state, dtype=_F32) if want_dh0 else None
     rest = (gp, bp, None if h0 is None else _dense(h0, "h0", _F32, state, dev), _dense(dO, "dO", _BF16, (B, T, HV, dv), dev),
             None if dhT is None else _dense(dhT, "dhT", _F32, state, dev), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(),
             gg.data_ptr(), gb.data_ptr(), None if gh is None else gh.data_ptr(),
@@ -628,7 +627,7 @@ def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):
     [N, HV, dk, dv], or a pool [rows, HV, dk, dv] with slots [N] (int32, on the
     device) naming each request's row; a slot outside the pool marks a padded
     request (o = 0, no state).  Returns o [N, HV, dv] bf16."""
-    torch = _types()
+    _types()
     N, HK, dk = q.shape
     HV, dv = v.shape[-2:]
     dev = _require_cuda(q)
@@ -638,7 +637,7 @@ def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):
     gp, bp, gf = _check_gates(g, beta, (N, HV), dev)
     rows, sp = (N, None) if slots is None else (state.shape[0], _dense(slots, "slots", _I32, (N,), dev))
     if o is None:
-        o = torch.empty((N, HV, dv), dtype=_BF16, device=dev)
+        o = v.new_empty((N, HV, dv))
     _call("kda_gdn_decode_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), gp, bp,
           _dense(state, "state", _F32, (rows, HV, dk, dv), dev), _dense(o, "o", _BF16, (N, HV, dv), dev), sp, rows,
           scale, N, HK, HV, dk, dv, qs, ks, vs, gf)
@@ -684,8 +683,8 @@ def act_pack8(*tensors):
         strides.append(_check_tokens(x, "tensor %d" % i, x.shape[:-2], heads, d, dev))
         cols.append(heads * d)
         rows.append(t.numel() // (heads * d) if heads * d else 0)
-        out.append(Packed8(torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev),
-                           torch.empty((*shape[:-1], shape[-1] // 32), dtype=torch.uint8, device=dev)))
+        out.append(Packed8(t.new_empty(shape, dtype=torch.float8_e4m3fn),
+                           t.new_empty((*shape[:-1], shape[-1] // 32), dtype=torch.uint8)))
     _call("kda_act_pack8", dev, n, _PTRS[n](*[t.data_ptr() for t in tensors]), _PTRS[n](*[p.data.data_ptr() for p in out]),
           _PTRS[n](*[p.scales.data_ptr() for p in out]), _SIZES[n](*rows), _SIZES[n](*cols), _SIZES[n](*strides))
     return out[0] if n == 1 else tuple(out)
@@ -701,12 +700,12 @@ def _packed8(p, name, shape, dev):
 
 def act_unpack8(packed, *, out=None):
     """The bf16 values that a Packed8 stands for, exactly (kda_act_unpack8)."""
-    torch = _types()
+    _types()
     dev = _require_cuda(packed.data)
     shape = packed.data.shape
     data, scales = _packed8(packed, "packed", shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
+        out = packed.data.new_empty(shape, dtype=_BF16)
     last = shape[-1]
     _call("kda_act_unpack8", dev, 1, _PTRS[1](data), _PTRS[1](scales), _PTRS[1](_dense(out, "out", _BF16, shape, dev)),
           _SIZES[1](packed.data.numel() // last if last else 0), _SIZES[1](last))
