@@ -37,6 +37,9 @@
 // and the sums over the results take the rest).  The local kernel with one role
 // that did everything in turn took 410 us; with 16 computing warps of 16 columns
 // each in place of 8 of 32, 390 against 364 us at that time.
+#include <algorithm>
+#include <cmath>
+
 #include "gdn_chunk.cuh"
 
 namespace kda {
@@ -87,12 +90,27 @@ constexpr uint32_t T_PO = 256;                       // reverse: (P^T dO)^T
 constexpr uint32_t T_OG = 320;                       // reverse: (gam dO~)^T
 constexpr uint32_t T_D = 384;
 
+// Sequences of min_chunks chunks run in segments, of which those between the
+// first and the last count SEG_OTHER and these two SEG_END.  The first launch
+// has, per value head, the forward chain's first segment and the reverse chain's
+// last in full, and for each segment between them the state that either chain
+// reaches from zero and the transition M (M^T for the reverse chain), which leave
+// nothing else.  join_launch makes the start states, the second launch runs the
+// other segments.  With fwd_parts the forward chain instead goes in two parts one
+// after the other, FWD_FIRST % of it in the first launch.
+enum Pass { WHOLE, FIRST, SECOND };
+constexpr int SEG_END = 8, SEG_OTHER = 10, FWD_FIRST = 50;
+
 struct Args {
     Seqs seqs;
     const uint8_t* rec;
     const float* h0;
     const float* dhT;
     float* dh0;
+    // forward, reverse: as JoinSet, first the state (gradient) at the end of what the first launch runs in full
+    float *first[2], *before_last[2], *M[2], *N[2], *start[2];
+    int pass, segments, min_chunks, n_long;
+    bool fwd_parts;
     uint8_t* S0;            // per (slot, value head): the chunk's start state, two planes
     uint8_t* dS1;           // and its end state's gradient
     uint8_t* u;             // U, two planes
@@ -101,18 +119,97 @@ struct Args {
     uint64_t wait_ns;
 };
 
+// What a CTA runs: chunks [c0, c1) of a sequence's head, from a state (gradient)
+// (null: zero, or the identity for the transition, where V counts as zero) to
+// one (null: not kept), and for the transition also its transpose.
+struct Piece {
+    int n, hv, c0, c1;
+    bool rev, full, transition;
+    const float* from;
+    float *to, *to_t;
+};
+
+// False if there is nothing to run.
+__device__ __forceinline__ bool find_piece(const Args& p, Piece& pc)
+{
+    const int between = p.segments - 2, fwd_others = p.fwd_parts ? 1 : between + 1;
+    const int tasks = p.pass == WHOLE ? 0 : p.pass == FIRST ? 2 + between * (p.fwd_parts ? 2 : 3) : between + 1 + fwd_others;
+    const int64_t in_segments = (int64_t)p.n_long * p.HV * tasks, at = (int64_t)blockIdx.x - in_segments;
+    pc.full = true;
+    pc.transition = false;
+    pc.to = pc.to_t = nullptr;
+    if (at >= 0) {                                   // the two chains of a head next to one another: they share loads
+        pc.rev = (at & 1) != 0;
+        pc.hv = (int)((at >> 1) % p.HV);
+        pc.n = (int)((at >> 1) / p.HV);
+        pc.c0 = 0;
+        pc.c1 = chunk_count(p.seqs, pc.n);
+        const int64_t head = ((int64_t)pc.n * p.HV + pc.hv) * D * D;
+        pc.from = pc.rev ? (p.dhT ? p.dhT + head : nullptr) : p.h0 ? p.h0 + head : nullptr;
+        if (pc.rev && p.dh0) pc.to = p.dh0 + head;
+        return p.pass == WHOLE || pc.c1 < p.min_chunks;
+    }
+    const int task = (int)(blockIdx.x / p.HV) % tasks, l = (int)(blockIdx.x / p.HV) / tasks;
+    pc.hv = (int)(blockIdx.x % p.HV);
+    pc.n = long_sequence(p.seqs, p.min_chunks, l);
+    if (pc.n < 0) return false;
+    const int chunks = chunk_count(p.seqs, pc.n);
+    const int64_t head = ((int64_t)pc.n * p.HV + pc.hv) * D * D, kept = ((int64_t)l * p.HV + pc.hv) * D * D;
+    auto bound = [&](int x) {
+        return x == 0 ? 0 : x == p.segments ? chunks
+                          : (int)((int64_t)chunks * (SEG_END + SEG_OTHER * (x - 1)) / (2 * SEG_END + SEG_OTHER * between));
+    };
+    // segment x between the ends, as the forward (0) and the reverse chain (1) count it
+    auto mid = [&](int dir, int x) { return (((int64_t)l * between + (dir ? between - x : x - 1)) * p.HV + pc.hv) * D * D; };
+    int seg;
+    if (p.pass == FIRST) {
+        const int kinds = p.fwd_parts ? 2 : 3;
+        const int kind = task < 2 ? task : (task - 2) % kinds;           // 0 reverse, 1 forward or transition, 2 forward
+        seg = task == 0 ? p.segments - 1 : task == 1 ? 0 : 1 + (task - 2) / kinds;
+        pc.rev = kind == 0;
+        if (task < 2) {
+            const float* h = pc.rev ? p.dhT : p.h0;
+            pc.from = h ? h + head : nullptr;
+            pc.to = p.first[pc.rev] + kept;
+        } else {
+            pc.full = false;
+            pc.from = nullptr;
+            pc.transition = kind == 1;
+            pc.to = pc.transition ? (p.fwd_parts ? nullptr : p.M[0] + mid(0, seg)) : p.N[pc.rev] + mid(pc.rev, seg);
+            if (pc.transition) pc.to_t = p.M[1] + mid(1, seg);
+        }
+    } else {
+        pc.rev = task <= between;
+        seg = pc.rev ? task : p.fwd_parts ? 1 : task - between;
+        const bool is_mid = seg >= 1 && seg <= between;
+        pc.from = !pc.rev && p.fwd_parts ? p.first[0] + kept
+               : is_mid ? p.start[pc.rev] + mid(pc.rev, seg) : p.before_last[pc.rev] + kept;
+        if (pc.rev && seg == 0 && p.dh0) pc.to = p.dh0 + head;
+    }
+    pc.c0 = bound(seg);
+    pc.c1 = bound(seg + 1);
+    if (!pc.rev && pc.full && p.fwd_parts) {
+        const int half = (int)((int64_t)chunks * FWD_FIRST / 100);
+        pc.c0 = p.pass == FIRST ? 0 : half;
+        pc.c1 = p.pass == FIRST ? half : chunks;
+    }
+    return true;
+}
+
 template <bool REV>
 __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& p,
-                                      uint8_t* sm, uint64_t* bars, volatile int* s_abort, int n, int hv)
+                                      uint8_t* sm, uint64_t* bars, volatile int* s_abort, const Piece& pc)
 {
     using namespace tc;
     constexpr uint32_t tm = 0;                       // all of tensor memory is this CTA's
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int hk = hv / (p.HV / p.HK);
+    const int hv = pc.hv, hk = hv / (p.HV / p.HK), chunks = pc.c1 - pc.c0;
     int begin, end;
-    seq_range(p.seqs, n, begin, end);
-    const int chunks = (end - begin + C - 1) / C;
-    const int64_t slot0 = (int64_t)(begin / C) + n;
+    seq_range(p.seqs, pc.n, begin, end);
+    const int64_t slot0 = (int64_t)(begin / C) + pc.n + pc.c0;
+    end = min(end, begin + pc.c1 * C);
+    begin += pc.c0 * C;
+    const bool full = pc.full, transition = !REV && pc.transition;
     auto bar = [&](int b) { return smem_u32(&bars[b]); };
     auto chunk_at = [&](int c) { return REV ? chunks - 1 - c : c; };
     auto u_cols = [](int c) { return REV || (c & 1) == 0 ? T_U : T_U2; };
@@ -121,13 +218,14 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
     if (warp < N_CHAIN) {
         const int sp = warp & 3, part = warp >> 2, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
-        const float* init = REV ? p.dhT : p.h0;
-        const float* h = init ? init + ((int64_t)n * p.HV + hv) * D * D + j : nullptr;
         float S[2][16];                              // S[b][i]: d_k = 64 b + 16 part + i
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) S[b][i] = h ? h[(int64_t)(64 * b + 16 * part + i) * D] : 0.f;
+            for (int i = 0; i < 16; ++i) {
+                const int dk = 64 * b + 16 * part + i;
+                S[b][i] = pc.from ? pc.from[dk * D + j] : transition && dk == j ? 1.f : 0.f;
+            }
         auto arrive = [&](int b) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(b));
@@ -182,7 +280,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 tmem_put16(t + T_OG + 16 * part, x, w);
                 give(B_DO);
             }
-            store_state(0, c);
+            if (full) store_state(0, c);
             wait(bar(B_MU), c & 1);                  // U, or K dS1 and P^T dO
             fence_after_sync();
             tmem_ld16(t + u_cols(c) + 16 * part, x);
@@ -210,7 +308,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 tmem_put16(t + T_UE + 16 * part, x, w);
             }
             give(B_U);
-            store_state(1, c);
+            if (full) store_state(1, c);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 wait(bar(B_MD + b), c & 1);
@@ -226,18 +324,22 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 if (c + 1 < chunks) give_state(b);
             }
         }
-        if (REV && p.dh0) {
-            float* out = p.dh0 + ((int64_t)n * p.HV + hv) * D * D + j;
+        if (pc.to)
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) out[(int64_t)(64 * b + 16 * part + i) * D] = S[b][i];
-        }
+                for (int i = 0; i < 16; ++i) pc.to[(64 * b + 16 * part + i) * D + j] = S[b][i];
+        if (transition)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(pc.to_t + j * D + 64 * b + 16 * part + i) = make_float4(S[b][i], S[b][i + 1], S[b][i + 2], S[b][i + 3]);
     } else if (warp < W_MMA) {
         const int sp = warp & 3, j = 32 * sp + lane;
         const uint32_t t = tm + ((uint32_t)(32 * sp) << 16);
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < chunks && full; ++c) {
             const int s = c & 1;
             wait(bar(B_MV + s), (c >> 1) & 1);
             fence_after_sync();
@@ -292,7 +394,8 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 mma4_ss<128, 128>(tm + T_PO, vd, ph, id_v, 0u);
                 mma4_ss<128, 128>(tm + T_PO, vd, ph + (uint64_t)(BOX >> 4), id_v, 1u);
             } else {                                 // U^T = V^T T^T
-                if (c > 1 && !ok(B_OFREE + (c & 1), ((c >> 1) - 1) & 1)) return false;      // chunk c - 2's U has been read
+                if (transition) return true;
+                if (full && c > 1 && !ok(B_OFREE + (c & 1), ((c >> 1) - 1) & 1)) return false;     // chunk c - 2's U has been read
                 fence_after_sync();
                 mma4_ss<128, 16>(tm + u_cols(c), vd, sdesc(base + S_REC + REC_TH, 128, 1024), id_v, 0u);
                 mma4_ss<128, 16>(tm + u_cols(c), vd, sdesc(base + S_REC + REC_TL, 128, 1024), id_v, 1u);
@@ -309,11 +412,11 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             auto s_product = [&](int b) {
                 const uint64_t h = REV ? kq + (uint64_t)(2 * b * (BOX >> 4)) : wd + (uint64_t)(b * (BOX >> 4));
                 const uint32_t u = tm + u_cols(c);
-                mma4_ts<2>(u, tm + T_S + 64 * b, h, id_n64, REV && b == 0 ? 0u : 1u);
+                mma4_ts<2>(u, tm + T_S + 64 * b, h, id_n64, (REV || transition) && b == 0 ? 0u : 1u);
                 mma4_ts<2>(u, tm + T_S + 64 * b + LOWER, h, id_n64, 1u);
                 if (!REV) mma4_ts<2>(u, tm + T_S + 64 * b, h + LO, id_n64, 1u);
             };
-            if (REV && c > 0 && !ok(B_OFREE + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
+            if (REV && full && c > 0 && !ok(B_OFREE + ((c - 1) & 1), ((c - 1) >> 1) & 1)) break;
             if (!ok(B_S, c & 1)) break;
             fence_after_sync();
             s_product(0);
@@ -342,7 +445,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 if (REV) mma4_ts<128>(tm + T_D + 64 * b, tm + T_UE, h + LO, id_bmn, 1u);
                 mma_commit_w(bar(B_MD + b));
             }
-            if constexpr (REV) {                     // dV^T = dU^T T
+            if (REV && full) {                       // dV^T = dU^T T
                 const uint64_t th = sdesc(base + S_REC + REC_TH, 1024, 128), tl = th + (uint64_t)(BOX >> 4);
                 mma4_ts<128>(tm + T_U, tm + T_UE, th, id_bmn, 0u);
                 mma4_ts<128>(tm + T_U, tm + T_UE + LOWER, th, id_bmn, 1u);
@@ -357,7 +460,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             mbar_wait(bar(B_DRAIN), 0, DRAIN_NS);
         }
     } else if (lane == 0) {
-        constexpr uint32_t bytes = REV ? STAGE : 4 * BOX + REC_W_BYTES;
+        const uint32_t bytes = REV ? STAGE : (transition ? 2 : 4) * BOX + REC_W_BYTES;
         int loaded = 0, loaded_p = 0;
 #pragma unroll 1
         for (int c = 0; c < chunks; ++c) {
@@ -366,17 +469,17 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
             // before a product that this one waits for)
             if (c >= 2 && !wait(bar(B_FREE + s), ((c >> 1) - 1) & 1)) break;
             if (*s_abort) break;
-            const uint32_t base = smem_u32(sm + s * STAGE), full = bar(B_FULL + s);
+            const uint32_t base = smem_u32(sm + s * STAGE), landed = bar(B_FULL + s);
             const int y = begin + chunk_at(c) * C;
             const uint8_t* rec = p.rec + ((slot0 + chunk_at(c)) * p.HV + hv) * REC_BYTES;
-            mbar_arrive_expect_tx(full, bytes);
+            mbar_arrive_expect_tx(landed, bytes);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, full);
-                if (REV) tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, full);
-                tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, full);
+                tma_load_2d(base + 2 * b * BOX, &mk, hk * D + 64 * b, y, landed);
+                if (REV) tma_load_2d(base + (2 * b + 1) * BOX, &mq, hk * D + 64 * b, y, landed);
+                if (!transition) tma_load_2d(base + S_V + b * BOX, &mv, hv * D + 64 * b, y, landed);
             }
-            bulk_load(base + S_REC, rec, REC_W_BYTES, full);
+            bulk_load(base + S_REC, rec, REC_W_BYTES, landed);
             loaded = c + 1;
             if (c + 2 < chunks) {                     // on its way to L2
                 const int yn = begin + chunk_at(c + 2) * C;
@@ -384,7 +487,7 @@ __device__ __forceinline__ void chain(const CUtensorMap& mq, const CUtensorMap& 
                 for (int b = 0; b < 2; ++b) {
                     tma_prefetch_2d(&mk, hk * D + 64 * b, yn);
                     if (REV) tma_prefetch_2d(&mq, hk * D + 64 * b, yn);
-                    tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
+                    if (!transition) tma_prefetch_2d(&mv, hv * D + 64 * b, yn);
                 }
                 bulk_prefetch(p.rec + ((slot0 + chunk_at(c + 2)) * p.HV + hv) * REC_BYTES, REV ? REC_BYTES : REC_W_BYTES);
             }
@@ -412,8 +515,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __shared__ int s_abort;
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const bool rev = (blockIdx.x & 1) != 0;          // the two chains of a head next to one another: they share loads
-    const int hv = (blockIdx.x >> 1) % p.HV, n = (blockIdx.x >> 1) / p.HV;
+    Piece pc;
+    if (!find_piece(p, pc)) return;
     if (tid == 0) {
         for (int b = 0; b < N_BAR; ++b) {
             const int count = b == B_S || b == B_S + 1 || b == B_U || b == B_DO ? N_CHAIN
@@ -431,8 +534,8 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     __syncthreads();
     fence_after_sync();
     const uint32_t tm = s_tmem;
-    if (rev) chain<true>(mq, mk, mdo, p, sm, bars, &s_abort, n, hv);
-    else chain<false>(mq, mk, mv, p, sm, bars, &s_abort, n, hv);
+    if (pc.rev) chain<true>(mq, mk, mdo, p, sm, bars, &s_abort, pc);
+    else chain<false>(mq, mk, mv, p, sm, bars, &s_abort, pc);
     fence_before_sync();
     __syncthreads();
     if (warp == W_MMA) {
@@ -440,15 +543,15 @@ chains_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
         tmem_dealloc(tm, 512);
     }
     if (*(volatile int*)&s_abort) {                  // a wait expired: no partial result passes for a real one
-        int begin, end;
-        seq_range(p.seqs, n, begin, end);
-        const int64_t first = (int64_t)(begin / C) + n;
-        uint8_t* out = rev ? p.dv : p.u;             // the local kernel reads both: its gradients become NaN
-        for (int c = 0; c * C < end - begin; ++c)
+        const int64_t first = first_slot(p.seqs, pc.n);
+        uint8_t* out = pc.rev ? p.dv : p.u;           // the local kernel reads both: its gradients become NaN
+        for (int c = pc.c0; c < pc.c1 && pc.full; ++c)
             for (int e = tid; e < (int)UPLANE / 4; e += NT)
-                reinterpret_cast<uint32_t*>(out + ((first + c) * p.HV + hv) * (2 * (int64_t)UPLANE))[e] = 0x7fc07fc0u;
-        if (rev && p.dh0)
-            for (int e = tid; e < D * D; e += NT) p.dh0[((int64_t)n * p.HV + hv) * D * D + e] = __int_as_float(0x7fc00000);
+                reinterpret_cast<uint32_t*>(out + ((first + c) * p.HV + pc.hv) * (2 * (int64_t)UPLANE))[e] = 0x7fc07fc0u;
+        float* to[2] = {pc.to, pc.to_t};
+        for (int i = 0; i < 2; ++i)
+            if (to[i])
+                for (int e = tid; e < D * D; e += NT) to[i][e] = __int_as_float(0x7fc00000);
     }
 }
 
@@ -933,6 +1036,20 @@ __global__ void outside_kernel(const Outside z, const int* __restrict__ cu, int 
 
 static DeviceFlags g_back_attr_done;
 
+// Segments of a call's long sequences, as in the forward.  The first launch has
+// 3 segments - 4 CTAs per sequence and value head; with the forward chain in two
+// parts 4 for three segments.
+static void choose_segments(bk::Args& a, int64_t heads, bool ragged)
+{
+    if (heads == 0) return;
+    const int64_t chunks = a.seqs.tokens / C / a.seqs.n_seq, per_head = current_sm_count() / heads;
+    if (chunks < MIN_CHUNKS || per_head < 4) return;
+    a.segments = (int)std::max<int64_t>(3, std::min((per_head + 4) / 3, (int64_t)std::sqrt((double)chunks)));
+    a.fwd_parts = per_head < 5;
+    a.min_chunks = MIN_CHUNKS;
+    a.n_long = ragged ? (int)std::min<int64_t>(a.seqs.n_seq, a.seqs.tokens / ((MIN_CHUNKS - 1) * C + 1)) : a.seqs.n_seq;
+}
+
 }  // namespace gdn
 
 cudaError_t act8_launch(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
@@ -968,7 +1085,10 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     if (e != cudaSuccess) return e;
     const size_t units = (size_t)slot_count(a.seqs) * HV;
     const size_t u_bytes = (size_t)tokens * HV * D * 2, qk_bytes = (size_t)tokens * HK * D * 2;
-    size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE + 4 * (size_t)UPLANE);
+    choose_segments(a, (int64_t)N * HV, cu != nullptr);
+    const int64_t heads = (int64_t)a.n_long * HV, between = a.segments - 2;
+    const size_t kept = (size_t)heads * D * D, mids = kept * (heads > 0 ? between : 0);
+    size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE + 4 * (size_t)UPLANE) + (4 * kept + (a.fwd_parts ? 3 : 6) * mids) * sizeof(float);
     if (scales) bytes += 2 * qk_bytes + u_bytes;
     uint8_t* ws = nullptr;
     keep_pool_memory();
@@ -981,6 +1101,15 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     a.dS1 = take(units * 2 * PLANE);
     a.u = take(units * 2 * UPLANE);
     a.dv = take(units * 2 * UPLANE);
+    for (int r = 0; r < 2 && heads > 0; ++r) {
+        auto floats = [&](size_t n) { return reinterpret_cast<float*>(take(n * sizeof(float))); };
+        a.first[r] = floats(kept);
+        a.before_last[r] = floats(kept);
+        if (r == 0 && a.fwd_parts) continue;
+        a.M[r] = floats(mids);
+        a.N[r] = floats(mids);
+        a.start[r] = floats(mids);
+    }
     if (scales) {
         void* out[3] = {take(qk_bytes), take(qk_bytes), take(u_bytes)};
         const void* src[3] = {q, k, v};
@@ -1033,15 +1162,27 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     }
     if (e == cudaSuccess && N > 0)
         e = prep_launch(maps.q, maps.k, g, beta, a.seqs, const_cast<uint8_t*>(a.rec), scale, HK, HV, gate_f32, true, stream);
-    if (e == cudaSuccess && N > 0) {
-        chains_kernel<<<(unsigned)(2 * (int64_t)N * HV), NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);
-        e = cudaGetLastError();
+    auto chains = [&](int pass, int64_t blocks) {
+        a.pass = pass;
+        chains_kernel<<<(unsigned)blocks, NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);
+        note_launches(1);
+        return cudaGetLastError();
+    };
+    if (e == cudaSuccess && N > 0 && heads == 0) {
+        e = chains(WHOLE, 2 * (int64_t)N * HV);
+    } else if (e == cudaSuccess && N > 0) {
+        e = chains(FIRST, heads * (2 + between * (a.fwd_parts ? 2 : 3)) + (cu ? 2 * (int64_t)N * HV : 0));
+        JoinArgs j = {a.seqs, {}, HV, (int)between, a.min_chunks};
+        int sets = 0;
+        for (int r = a.fwd_parts ? 1 : 0; r < 2; ++r) j.set[sets++] = {a.M[r], a.N[r], a.first[r], a.start[r], a.before_last[r]};
+        if (e == cudaSuccess) e = join_launch(j, sets, heads, stream);
+        if (e == cudaSuccess) e = chains(SECOND, heads * (between + 1 + (a.fwd_parts ? 1 : between + 1)));
     }
     if (e == cudaSuccess && N > 0) {
+        note_launches(1);
         local_kernel<<<(unsigned)(slot_count(a.seqs) * HK), lo::LALL, lo::SMEM, stream>>>(maps, l);
         e = cudaGetLastError();
     }
-    if (N > 0) note_launches(2);
     const cudaError_t ef = cudaFreeAsync(ws, stream);
     return e == cudaSuccess ? ef : e;
 }

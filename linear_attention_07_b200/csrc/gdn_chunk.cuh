@@ -86,6 +86,46 @@ __device__ __forceinline__ bool slot_chunk(const Seqs& s, int64_t slot, int& n, 
     return true;
 }
 
+__device__ __forceinline__ int chunk_count(const Seqs& s, int n)
+{
+    int begin, end;
+    seq_range(s, n, begin, end);
+    return (end - begin + C - 1) / C;
+}
+
+// The l-th sequence of min_chunks chunks or more, or -1; by whole warps.
+__device__ __forceinline__ int long_sequence(const Seqs& s, int min_chunks, int l)
+{
+    for (int first = 0; first < s.n_seq; first += 32) {
+        const int n = first + (int)(threadIdx.x & 31);
+        uint32_t m = __ballot_sync(0xffffffffu, n < s.n_seq && chunk_count(s, n) >= min_chunks);
+        const int count = __popc(m);
+        if (l < count) {
+            for (; l > 0; --l) m &= m - 1;
+            return first + __ffs(m) - 1;
+        }
+        l -= count;
+    }
+    return -1;
+}
+
+// Long sequences of few heads run in segments at the same time: from MIN_CHUNKS
+// chunks on.  The start states follow from the states that the segments reach
+// from zero (N) and their transitions (M), start_{k+1} = M_k start_k + N_k with
+// start_0 = first; before_last is what the last step gives.  All [n_long]
+// [between][HV][D][D] fp32, first and before_last [n_long][HV][D][D].
+constexpr int MIN_CHUNKS = 32;
+struct JoinSet {
+    const float *M, *N, *first;
+    float *start, *before_last;
+};
+struct JoinArgs {
+    Seqs seqs;
+    JoinSet set[2];
+    int HV, between, min_chunks;
+};
+cudaError_t join_launch(const JoinArgs& a, int sets, int64_t heads, cudaStream_t stream);
+
 // Descriptor of a 128-byte-swizzled tile of 128-byte rows (as a TMA box of 64
 // bf16 columns leaves it, 1024-byte aligned): groups of 8 rows are 1024 bytes
 // apart.  K-major (the row is a vector along K): 16 elements of K further are

@@ -85,13 +85,12 @@ constexpr uint32_t T_D = 384;                        // (K^T eta U)^T
 // which the first of two launches runs segment 0 and, for each of the segments
 // between it and the last, the state that it reaches from zero and its
 // transition (from the identity with V = 0; neither has outputs).
-// join_kernel makes the start states of these, and the second launch runs all
+// join_launch makes the start states of these, and the second launch runs all
 // but segment 0 from them.  The first launch has the sequences in one piece
 // behind those in segments.
 enum Pass { WHOLE, FIRST, SECOND };
 // Segment 0 counts 8 of the others' 10: its outputs are made while theirs are not.
 constexpr int SEG_FIRST = 8, SEG_OTHER = 10;
-constexpr int MIN_CHUNKS = 32;                       // of a sequence in segments
 
 struct Args {
     Seqs seqs;
@@ -107,97 +106,6 @@ struct Args {
     float scale;
     uint64_t wait_ns;
 };
-
-__device__ __forceinline__ int chunk_count(const Seqs& s, int n)
-{
-    int begin, end;
-    seq_range(s, n, begin, end);
-    return (end - begin + C - 1) / C;
-}
-
-// The l-th sequence of min_chunks chunks or more, or -1; by whole warps.
-__device__ __forceinline__ int long_sequence(const Seqs& s, int min_chunks, int l)
-{
-    for (int first = 0; first < s.n_seq; first += 32) {
-        const int n = first + (int)(threadIdx.x & 31);
-        uint32_t m = __ballot_sync(0xffffffffu, n < s.n_seq && chunk_count(s, n) >= min_chunks);
-        const int count = __popc(m);
-        if (l < count) {
-            for (; l > 0; --l) m &= m - 1;
-            return first + __ffs(m) - 1;
-        }
-        l -= count;
-    }
-    return -1;
-}
-
-// start_{p+1} = M_p start_p + N_p in fp32 for 32 columns of one head, a step
-// after the other; M_{p+1} is on its way in registers meanwhile.  Thread: rows
-// tid / 8 + 32 r, columns 4 (tid % 8) .. + 3.
-constexpr int JOIN_NT = 256, JOIN_COLS = 32, JOIN_LD = D + 4;
-constexpr uint32_t JOIN_SMEM = (D * JOIN_LD + D * JOIN_COLS) * 4;
-
-__global__ void __launch_bounds__(JOIN_NT)
-join_kernel(const Args p)
-{
-    extern __shared__ __align__(16) float jsm[];
-    float* m = jsm;                                  // [D][JOIN_LD]
-    float* st = jsm + D * JOIN_LD;                   // [D][JOIN_COLS]
-    const int tid = threadIdx.x, l = blockIdx.y / p.HV, hv = blockIdx.y % p.HV, between = p.segments - 2;
-    if (long_sequence(p.seqs, p.min_chunks, l) < 0) return;
-    const int row = tid / 8, cs = 4 * (tid % 8), col = blockIdx.x * JOIN_COLS + cs;
-    const int64_t head = ((int64_t)l * p.HV + hv) * D * D;
-    auto mid = [&](int k) { return (((int64_t)l * between + k) * p.HV + hv) * D * D; };
-    float4 next[D * D / 4 / JOIN_NT], cur[4];
-    auto load = [&](int k) {
-        const float4* src = reinterpret_cast<const float4*>(p.M + mid(k));
-#pragma unroll
-        for (int u = 0; u < D * D / 4 / JOIN_NT; ++u) next[u] = src[u * JOIN_NT + tid];
-    };
-    load(0);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) cur[r] = *reinterpret_cast<const float4*>(p.end0 + head + (row + 32 * r) * D + col);
-#pragma unroll 1
-    for (int k = 0; k < between; ++k) {
-        float4 acc[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int64_t at = mid(k) + (row + 32 * r) * D + col;
-            acc[r] = *reinterpret_cast<const float4*>(p.N + at);
-            *reinterpret_cast<float4*>(p.start + at) = cur[r];
-        }
-        __syncthreads();                             // the last step has read m and st
-#pragma unroll
-        for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(st + (row + 32 * r) * JOIN_COLS + cs) = cur[r];
-#pragma unroll
-        for (int u = 0; u < D * D / 4 / JOIN_NT; ++u) {
-            const int e = 4 * (u * JOIN_NT + tid);
-            *reinterpret_cast<float4*>(m + e / D * JOIN_LD + e % D) = next[u];
-        }
-        __syncthreads();
-        if (k + 1 < between) load(k + 1);
-#pragma unroll 4
-        for (int i = 0; i < D; i += 4) {
-            float4 x[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float4*>(st + (i + e) * JOIN_COLS + cs);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 a = *reinterpret_cast<const float4*>(m + (row + 32 * r) * JOIN_LD + i);
-                const float f[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[r].x = fmaf(f[e], x[e].x, acc[r].x); acc[r].y = fmaf(f[e], x[e].y, acc[r].y);
-                    acc[r].z = fmaf(f[e], x[e].z, acc[r].z); acc[r].w = fmaf(f[e], x[e].w, acc[r].w);
-                }
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) cur[r] = acc[r];
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(p.before_last + head + (row + 32 * r) * D + col) = cur[r];
-}
 
 }  // namespace fw
 
@@ -578,11 +486,11 @@ static void choose_segments(fw::Args& a, int64_t heads, bool ragged)
 {
     const int64_t chunks = a.seqs.tokens / C / a.seqs.n_seq;
     const int64_t segments = std::min((current_sm_count() / heads + 3) / 2, (int64_t)std::sqrt((double)chunks));
-    if (chunks < fw::MIN_CHUNKS || segments < 3) return;
+    if (chunks < MIN_CHUNKS || segments < 3) return;
     a.segments = (int)segments;
-    a.min_chunks = fw::MIN_CHUNKS;
+    a.min_chunks = MIN_CHUNKS;
     // all of equal lengths, or as many as the tokens can make
-    a.n_long = ragged ? (int)std::min<int64_t>(a.seqs.n_seq, a.seqs.tokens / ((fw::MIN_CHUNKS - 1) * C + 1)) : a.seqs.n_seq;
+    a.n_long = ragged ? (int)std::min<int64_t>(a.seqs.n_seq, a.seqs.tokens / ((MIN_CHUNKS - 1) * C + 1)) : a.seqs.n_seq;
 }
 
 }  // namespace gdn
@@ -608,9 +516,7 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
     a.scale = scale;
     a.wait_ns = bounded_wait_limit_ns();
     cudaError_t e = once_per_device(g_fwd_attr_done, [](int) {
-        const cudaFuncAttribute at = cudaFuncAttributeMaxDynamicSharedMemorySize;
-        const cudaError_t r = cudaFuncSetAttribute(forward_kernel, at, (int)fw::SMEM);
-        return r != cudaSuccess ? r : cudaFuncSetAttribute(fw::join_kernel, at, (int)fw::JOIN_SMEM);
+        return cudaFuncSetAttribute(forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fw::SMEM);
     });
     if (e != cudaSuccess) return e;
     CUtensorMap mq = {}, mk = {}, mv = {}, mo = {};
@@ -651,9 +557,8 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         const int64_t between = a.segments - 2, heads = (int64_t)a.n_long * HV;
         e = launch(fw::FIRST, heads * (1 + 2 * between) + (cu ? (int64_t)N * HV : 0));
         if (e == cudaSuccess) {
-            fw::join_kernel<<<dim3(D / fw::JOIN_COLS, (unsigned)heads), fw::JOIN_NT, fw::JOIN_SMEM, stream>>>(a);
-            note_launches(1);
-            e = cudaGetLastError();
+            JoinArgs j = {a.seqs, {{a.M, a.N, a.end0, a.start, a.before_last}}, HV, (int)between, a.min_chunks};
+            e = join_launch(j, 1, heads, stream);
         }
         if (e == cudaSuccess) e = launch(fw::SECOND, heads * (between + 1));
     }

@@ -11,7 +11,7 @@ import torch
 
 import linear_attention_07_b200 as kda
 from test_gdn import D, TOL_O, TOL_S, TOL_STEP, batch, cu_of, on_gpu, reference, rel, tokens
-from test_gdn_backward import check, cotangents, run
+from test_gdn_backward import TOL_DG, TOL_GRAD, check, cotangents, run
 from test_gdn_backward import reference as gradients
 
 pytestmark = pytest.mark.gpu
@@ -82,6 +82,36 @@ def test_long_sequences_of_few_heads(lens, heads, decay):
     # the start states add the rounding of a transition and of the product with it to the chunks' own
     assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= 2 * TOL_S
     assert kda.device_status() == kda.KDA_OK
+
+
+@pytest.mark.parametrize("lens, heads", [((2200,), (16, 32)), ((2500,), (5, 5)), ((4500, 0, 1, 130, 6000), (2, 4)), ((5000,), (1, 1))],
+                         ids=str)
+@pytest.mark.parametrize("ends", [False, True])
+def test_gradients_of_long_sequences_of_few_heads(lens, heads, ends):
+    """Both chains in segments (32 heads: the forward chain in two parts)."""
+    T, N = sum(lens), len(lens)
+    x = tokens(T, *heads, seed=86)
+    h0 = torch.randn(N, heads[1], D, D) if ends else None
+    dO, dhT = cotangents(T, heads[1], N)
+    dhT = dhT if ends else None
+    n0 = kda.launch_count()
+    got = run(x, lens, dO, h0, dhT)
+    assert kda.launch_count() - n0 == 6                  # outside, chunks, two of the chains, joined, local
+    want = gradients(x, lens, dO, h0, dhT)
+    # the start states add the rounding of a transition and of the product with it to the chunks' own
+    check(got, want, (TOL_GRAD, TOL_GRAD, TOL_GRAD, TOL_DG, TOL_GRAD, 2 * TOL_S))
+    for a, b in zip(got, run(x, lens, dO, h0, dhT)):
+        assert torch.equal(a, b)
+
+
+def test_gradients_in_segments_expired(monkeypatch):
+    x = tokens(4100, 2, 4, seed=87)
+    dO, dhT = cotangents(4100, 4, 1)
+    monkeypatch.setenv("KDA_WAIT_LIMIT_NS", "0")
+    got = run(x, [4100], dO, None, dhT)
+    expired()
+    for name, t in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got):
+        assert torch.isnan(t.float()).all(), name
 
 
 @pytest.mark.parametrize("lens, heads", [((30, 9000, 1, 4000), (2, 4)), ((5200, 0, 40, 5300), (1, 2))], ids=str)
