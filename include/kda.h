@@ -375,8 +375,9 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * Tokens before the first sequence and behind the last get zero gradients.  A
  * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
  * atomics: the same inputs give the same bits.  Three launches (one more with
- * cu_seqlens); stream-ordered workspace of 263,168 bytes per value head and
- * 64-token chunk (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
+ * cu_seqlens, two more where long sequences of few heads run in segments);
+ * stream-ordered workspace of 263,168 bytes per value head and 64-token chunk,
+ * with segments up to a fifth more (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
  * the forward.  Supported: d_k == d_v == 128.
  *
  * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits

@@ -19,20 +19,20 @@
 // A write strength of zero would make dbeta 0 / 0: the backward takes |beta|
 // as at least 2^-30 (below fp32's resolution of the state).
 //
-// Two launches after the prep:
+// Two launches after the prep (four where sequences run in segments):
 //   1. chains_kernel: per sequence and value head two CTAs side by side, the
 //      forward chain (states at the chunks' starts, U) and the reverse chain
-//      (state gradients at the chunks' ends, dV, dh0);
+//      (state gradients at the chunks' ends, dV, dh0); its transition over chunks
+//      is the forward chain's, transposed;
 //   2. local_kernel: per chunk and query/key head, dq, dk (summed over the
 //      value heads of the group), dg, dbeta.
 // All that passes between products is a pair of bf16, as in the forward: a
 // single rounding would show in dg and dbeta, which are few numbers each from
 // a long sum.
 //
-// 8192 tokens x 32 heads (16 query/key heads): chains 550 us (4.2 us a chunk;
-// the reverse chain is the longer one, two products in turn, one of them over
-// dU in two steps, and 96 KB to store, which an SM does at about 32 bytes a
-// cycle), local 338 us (10 us per value head: the pair products and the states'
+// 8192 tokens x 32 heads (16 query/key heads): chains 433 us (210 + 9 + 214; in
+// one piece 560: 3.3 us a forward chunk, 4.2 us a reverse one, which has 96 KB
+// to store, and an SM stores about 32 bytes a cycle), local 338 us (10 us per value head: the pair products and the states'
 // read shared memory at its rate, 128 bytes a cycle, for 7,000 of 18,000 cycles,
 // and the sums over the results take the rest).  The local kernel with one role
 // that did everything in turn took 410 us; with 16 computing warps of 16 columns
@@ -1036,16 +1036,22 @@ __global__ void outside_kernel(const Outside z, const int* __restrict__ cu, int 
 
 static DeviceFlags g_back_attr_done;
 
-// Segments of a call's long sequences, as in the forward.  The first launch has
-// 3 segments - 4 CTAs per sequence and value head; with the forward chain in two
-// parts 4 for three segments.
+// Segments of a call's long sequences, as in the forward: the first launch has
+// 3 segments - 4 CTAs per sequence and value head, or 4 for three segments with
+// the forward chain in two parts.  Whole call, one sequence, in one piece and so,
+// us: 8192 tokens 926 -> 833 at 32 heads (in parts), 840 -> 719 at 24, 644 -> 344
+// at 8, 530 -> 184 at 1 (6 segments 234, 8 203, 16 183, 24 205); 2048 tokens 274
+// -> 279 at 32 heads, 258 -> 247 at 24, 183 -> 136 at 8; 1024 tokens 159 -> 172,
+// 159 -> 169 and 111 -> 109: in one piece below 32 chunks on average, in parts
+// below 40 unless a batch is ragged, whose longest sequence has more.
 static void choose_segments(bk::Args& a, int64_t heads, bool ragged)
 {
     if (heads == 0) return;
     const int64_t chunks = a.seqs.tokens / C / a.seqs.n_seq, per_head = current_sm_count() / heads;
-    if (chunks < MIN_CHUNKS || per_head < 4) return;
-    a.segments = (int)std::max<int64_t>(3, std::min((per_head + 4) / 3, (int64_t)std::sqrt((double)chunks)));
     a.fwd_parts = per_head < 5;
+    const int64_t least = a.fwd_parts && !(ragged && a.seqs.n_seq > 1) ? MIN_CHUNKS + 8 : MIN_CHUNKS;
+    if (chunks < least || per_head < 4) return;
+    a.segments = (int)std::max<int64_t>(3, std::min((per_head + 4) / 3, (int64_t)std::sqrt((double)chunks)));
     a.min_chunks = MIN_CHUNKS;
     a.n_long = ragged ? (int)std::min<int64_t>(a.seqs.n_seq, a.seqs.tokens / ((MIN_CHUNKS - 1) * C + 1)) : a.seqs.n_seq;
 }

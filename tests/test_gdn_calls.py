@@ -84,7 +84,7 @@ def test_long_sequences_of_few_heads(lens, heads, decay):
     assert kda.device_status() == kda.KDA_OK
 
 
-@pytest.mark.parametrize("lens, heads", [((2200,), (16, 32)), ((2500,), (5, 5)), ((4500, 0, 1, 130, 6000), (2, 4)), ((5000,), (1, 1))],
+@pytest.mark.parametrize("lens, heads", [((2600,), (16, 32)), ((2500,), (5, 5)), ((4500, 0, 1, 130, 6000), (2, 4)), ((5000,), (1, 1))],
                          ids=str)
 @pytest.mark.parametrize("ends", [False, True])
 def test_gradients_of_long_sequences_of_few_heads(lens, heads, ends):
