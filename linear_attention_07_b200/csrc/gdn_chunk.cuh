@@ -146,8 +146,9 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn = fals
 // Four K steps of one product by a converged warp (one elected lane issues).
 // A from tensor memory (16 columns per step: 8 of the upper and 8 of the lower
 // plane, written by one store) or shared memory, B from shared memory, its steps
-// in descriptor units (16 bytes), which change a descriptor's lower word only.  Issuing is close to what bounds the chains, so
-// it is kept to few instructions: warp-uniform operands, one election for four.
+// in descriptor units (16 bytes), which change a descriptor's lower word only.
+// Issuing is close to what bounds the chains, so it is kept to few instructions:
+// warp-uniform operands, one election for four.
 template <uint32_t B_STEP>
 __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t more)
 {

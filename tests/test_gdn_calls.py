@@ -104,6 +104,24 @@ def test_gradients_of_long_sequences_of_few_heads(lens, heads, ends):
         assert torch.equal(a, b)
 
 
+def test_segments_of_a_batch():
+    """Sequences of equal lengths, without cu_seqlens."""
+    B, T, HK, HV = 2, 2600, 4, 8
+    x, h0 = tokens(B * T, HK, HV, seed=88), torch.randn(B, HV, D, D)
+    dO, dhT = cotangents(B * T, HV, B)
+    split = [t.unflatten(0, (B, T)) for t in on_gpu(x)]
+    n0 = kda.launch_count()
+    o, S = kda.gdn_chunk_fwd(*split, h0.cuda())
+    assert kda.launch_count() - n0 == 4
+    ro, rS = reference(x, [T] * B, h0)
+    assert rel(o.flatten(0, 1), ro) <= TOL_O and rel(S, rS) <= 2 * TOL_S
+    n0 = kda.launch_count()
+    got = kda.gdn_chunk_bwd(*split, h0.cuda(), dO.unflatten(0, (B, T)).cuda(), dhT.cuda())
+    assert kda.launch_count() - n0 == 5
+    check([t.flatten(0, 1)[None] for t in got[:5]] + [got[5]], gradients(x, [T] * B, dO, h0, dhT),
+          (TOL_GRAD, TOL_GRAD, TOL_GRAD, TOL_DG, TOL_GRAD, 2 * TOL_S))
+
+
 def test_gradients_in_segments_expired(monkeypatch):
     x = tokens(4100, 2, 4, seed=87)
     dO, dhT = cotangents(4100, 4, 1)
