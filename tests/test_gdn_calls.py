@@ -219,6 +219,30 @@ def test_two_graphs_of_calls():
             assert all(torch.equal(y, z) for y, z in zip(w, r))
 
 
+def test_segments_in_a_graph():
+    """Calls in segments, captured and replayed with other inputs in the same places."""
+    x, y = (batch(on_gpu(tokens(4100, 2, 4, seed=s))) for s in (89, 90))
+    dO, dhT = (t.cuda() for t in cotangents(4100, 4, 1))
+    dO = dO[None]
+
+    def both(z):
+        o, S = kda.gdn_chunk_fwd(*z)
+        return [o, S, *kda.gdn_chunk_bwd(*z, None, dO, dhT)]
+
+    want = [both(z) for z in (x, y)]
+    held = [t.clone() for t in x]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = both(held)
+    for z, w in ((y, want[1]), (x, want[0]), (x, want[0])):
+        for a, b in zip(held, z):
+            a.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    assert kda.device_status() == kda.KDA_OK
+
+
 def test_state_in_place_and_on_a_side_stream():
     x, h0 = tokens(130, 2, 6, seed=76), torch.randn(1, 6, D, D)
     ro, rS = reference(x, [130], h0)
