@@ -498,15 +498,16 @@ def _check_tokens(t, name, lead, heads, d, dev):
         return heads * d
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError("%s: a token's heads must be dense, got strides %s" % (name, st))
-    step, n = 0, 1                                   # from the last token axis with more than one entry
+    step, n = None, 1                                # from the last token axis with more than one entry
     for size, s in zip(t.shape[-3::-1], st[-3::-1]):
         if size > 1:
-            if step and s != step * n:
-                raise ValueError("%s: the tokens must be equally spaced, got strides %s" % (name, st))
-            if not step:
+            if step is None:
                 step = s
+            elif s != step * n:
+                raise ValueError("%s: the tokens must be equally spaced, got strides %s" % (name, st))
             n *= size
-    step = step or heads * d
+    if step is None:
+        return heads * d
     if step % 8 != 0 or step < heads * d:
         raise ValueError("%s: the token stride must be a multiple of 8 and at least %d, got %d" % (name, heads * d, step))
     return step

@@ -144,6 +144,36 @@ def test_refusals_of_the_binding():
         kda.gdn_decode_step(*[t[0] for t in x], torch.zeros(4, 4, D, D))
 
 
+BROADCAST = [((1, 1, 2, D), (1, 4096, 2, D)), ((1, 2, D), (64, 2, D)), ((1, 1, 2, D), (8, 1, 2, D)),
+             ((3, 1, 2, D), (3, 5, 2, D)), ((1, 5, 2, D), (3, 5, 2, D)), ((2, 1, 4, 1, 2, D), (2, 3, 4, 1, 2, D)),
+             ((D,), (5, 1, D))]
+
+
+@pytest.mark.parametrize("shape, wide", BROADCAST, ids=str)
+def test_broadcast_tokens_are_refused(shape, wide):
+    """A token axis of stride 0 names the same values again: the kernels, which step from token to token, would
+    read behind the tensor."""
+    kda._types()
+    x = torch.zeros(shape, dtype=torch.bfloat16).expand(wide)
+    with pytest.raises(ValueError, match="token"):
+        kda._check_tokens(x, "q", x.shape[:-2], *x.shape[-2:], x.device)
+    y = x.contiguous()
+    assert kda._check_tokens(y, "q", y.shape[:-2], *y.shape[-2:], y.device) == y.shape[-2] * D
+
+
+def test_token_strides():
+    """The stride of slices of a wider tensor; axes of one entry do not matter; uneven ones are refused."""
+    kda._types()
+    wide = torch.zeros(3, 5, 8, D, dtype=torch.bfloat16)
+    of = lambda t: kda._check_tokens(t, "q", t.shape[:-2], *t.shape[-2:], t.device)
+    assert of(wide[:, :, 2:4]) == 8 * D and of(wide[:1, :, 2:4]) == 8 * D and of(wide[:, :1, :4]) == 5 * 8 * D
+    assert of(wide[1:2, 2:3, :4]) == 4 * D and of(wide[:, ::2, :4][:1]) == 16 * D
+    assert of(wide[:1, :1, :4].expand(1, 1, 4, D)) == 4 * D
+    for bad in (wide[:, :4, :4], wide[:, :, ::2], wide.transpose(0, 1)[..., :4, :], wide[..., :64]):
+        with pytest.raises(ValueError):
+            of(bad)
+
+
 # ------------------------------------------------------------ chunked forward --
 
 SHAPES = [(1,), (2, 1), (15,), (16, 17), (63, 64, 65), (127, 0, 128, 129), (0, 5, 0), (200, 1, 1, 333)]
