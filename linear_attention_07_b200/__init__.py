@@ -664,11 +664,25 @@ _PTRS = [ctypes.c_void_p * n for n in range(ACT8_MAX_TENSORS + 1)]
 _SIZES = [ctypes.c_int64 * n for n in range(ACT8_MAX_TENSORS + 1)]
 
 
+def _act8_rows(t, name, dev):
+    """(rows, channels of a row, elements from row to row) of a bf16 tensor; the
+    last two axes make one row where they are dense."""
+    shape = t.shape
+    if len(shape) < 1 or shape[-1] % 32 != 0:
+        raise ValueError("%s: the last axis must be a multiple of 32, got shape %s" % (name, tuple(shape)))
+    if len(shape) < 3 or (shape[-2] > 1 and t.stride(-2) != shape[-1]):
+        t = t.unsqueeze(-2)
+    heads, d = t.shape[-2:]
+    stride = _check_tokens(t, name, t.shape[:-2], heads, d, dev)
+    return t.numel() // (heads * d) if heads * d else 0, heads * d, stride
+
+
 def act_pack8(*tensors):
     """The 8-bit form (Packed8) of each of up to four bf16 tensors, in one
     launch (kda_act_pack8).  The last axis must be a multiple of 32; the
-    tensors may be slices of wider ones as long as their rows are equally
-    spaced.  One tensor gives a Packed8, several a tuple of them."""
+    tensors may be slices of wider ones as long as their rows (all axes but the
+    last, or but the last two where these are dense) are equally spaced, a
+    multiple of 8 elements apart.  One tensor gives a Packed8, several a tuple of them."""
     torch = _types()
     n = len(tensors)
     if not 1 <= n <= ACT8_MAX_TENSORS:
@@ -677,13 +691,10 @@ def act_pack8(*tensors):
     rows, cols, strides, out = [], [], [], []
     for i, t in enumerate(tensors):
         shape = t.shape
-        if len(shape) < 1 or shape[-1] % 32 != 0:
-            raise ValueError("tensor %d: the last axis must be a multiple of 32, got shape %s" % (i, tuple(shape)))
-        x = t if len(shape) >= 3 else t.unsqueeze(-2)            # [..., heads, channels]
-        heads, d = x.shape[-2:]
-        strides.append(_check_tokens(x, "tensor %d" % i, x.shape[:-2], heads, d, dev))
-        cols.append(heads * d)
-        rows.append(t.numel() // (heads * d) if heads * d else 0)
+        r, c, stride = _act8_rows(t, "tensor %d" % i, dev)
+        rows.append(r)
+        cols.append(c)
+        strides.append(stride)
         out.append(Packed8(t.new_empty(shape, dtype=torch.float8_e4m3fn),
                            t.new_empty((*shape[:-1], shape[-1] // 32), dtype=torch.uint8)))
     _call("kda_act_pack8", dev, n, _PTRS[n](*[t.data_ptr() for t in tensors]), _PTRS[n](*[p.data.data_ptr() for p in out]),

@@ -61,6 +61,35 @@ def test_refusals():
     assert lib.kda_launch_count() == n0
 
 
+ROWS = [((2, 50, 1024), (slice(None), slice(None), slice(0, 256)), (100, 256, 1024)),      # [B, T, d] of a projection
+        ((2, 50, 8, 128), (slice(None), slice(None), slice(2, 6)), (100, 512, 1024)),       # whole heads
+        ((2, 50, 8, 128), (slice(None), slice(None), slice(None), slice(0, 64)), (800, 64, 128)),   # part of every head
+        ((50, 1024), (slice(None), slice(256, 512)), (50, 256, 1024)),
+        ((4, 50, 1024), (slice(None, None, 2), slice(0, 1), slice(0, 32)), (2, 32, 102400)),
+        ((3, 4, 64), (slice(None),), (3, 256, 256)), ((96,), (slice(32, 64),), (1, 32, 32)), ((0, 4, 128), (slice(None),), (0, 512, 512))]
+
+
+@pytest.mark.parametrize("shape, part, want", ROWS, ids=str)
+def test_rows_of_slices(shape, part, want):
+    """(rows, channels, stride) of a slice: the last axis is split from the ones before it wherever these are equally spaced."""
+    kda._types()
+    x = torch.zeros(shape, dtype=torch.bfloat16)[part]
+    assert kda._act8_rows(x, "x", x.device) == want
+
+
+def test_rows_that_are_refused():
+    kda._types()
+    wide = torch.zeros(2, 50, 8, 128, dtype=torch.bfloat16)
+    for bad in (wide[:, :40, :, :64], wide[..., ::2], wide[:, ::3],
+                wide[:1, :1, :1].expand(1, 5, 1, 128), wide[0, 0, 0, :64].expand(3, 64), wide.transpose(1, 2)):
+        with pytest.raises(ValueError):
+            kda._act8_rows(bad, "x", bad.device)
+    with pytest.raises(ValueError, match="32"):
+        kda._act8_rows(wide[..., :48], "x", wide.device)
+    with pytest.raises(TypeError):
+        kda._act8_rows(wide.float(), "x", wide.device)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(32,), (1, 32), (3, 96), (7, 5, 64), (2, 77, 3, 128), (1000, 1, 128), (0, 4, 128)], ids=str)
 def test_shapes(shape):
@@ -131,3 +160,10 @@ def test_refusals_of_the_binding():
         kda.act_pack8(x.to(torch.bfloat16)[:, ::2])
     with pytest.raises(TypeError):
         kda.act_unpack8(kda.Packed8(x.to(torch.bfloat16), torch.zeros(4, 2, dtype=torch.uint8, device="cuda")))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape, part, rows", ROWS, ids=str)
+def test_slices(shape, part, rows):
+    x = torch.randn(shape, device="cuda").to(torch.bfloat16)[part]
+    check(x, kda.act_pack8(x))
