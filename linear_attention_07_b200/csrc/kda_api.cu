@@ -430,7 +430,8 @@ static int act8_any(int count, const void* const* src, void* const* dst, void* c
     for (int i = 0; i < count; ++i) {
         if (rows[i] < 0 || cols[i] < 0 || cols[i] % 32 != 0) return KDA_ERR_INVALID_ARG;
         if (cols[i] >= (int64_t)1 << 31 || rows[i] >= (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
-        if (rows[i] * (cols[i] / 16) > (int64_t)0x7fffffff * 256) return KDA_ERR_UNSUPPORTED;   // the grid's x
+        // the grid's x; a quotient, as the product may pass 64 bits
+        if (cols[i] > 0 && rows[i] > (int64_t)0x7fffffff * 256 / (cols[i] / 16)) return KDA_ERR_UNSUPPORTED;
         if (rows[i] * cols[i] == 0) continue;
         if (strides && (strides[i] % 8 != 0 || strides[i] < cols[i] || strides[i] >= (int64_t)1 << 40))
             return KDA_ERR_INVALID_ARG;

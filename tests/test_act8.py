@@ -61,6 +61,18 @@ def test_refusals():
     assert lib.kda_launch_count() == n0
 
 
+def test_sizes_past_64_bits_are_refused():
+    """rows * cols past 2^63: neither taken for nothing to do nor for few rows."""
+    lib = kda.load_library()
+    n0 = lib.kda_launch_count()
+    P, I = ctypes.c_void_p, ctypes.c_int64
+    for rows, cols in ((1 << 39, 1 << 30), (1 << 38, 1 << 30), ((1 << 38) + 1, 1 << 30), ((1 << 40) - 1, (1 << 31) - 32), (1 << 35, 1 << 10)):
+        args = (1, (P * 1)(0x10000), (P * 1)(0x20000), (P * 1)(0x30000), (I * 1)(rows), (I * 1)(cols))
+        assert lib.kda_act_pack8(*args, (I * 1)(cols), None) == kda.KDA_ERR_UNSUPPORTED, (rows, cols)
+        assert lib.kda_act_unpack8(*args, None) == kda.KDA_ERR_UNSUPPORTED, (rows, cols)
+    assert lib.kda_launch_count() == n0
+
+
 ROWS = [((2, 50, 1024), (slice(None), slice(None), slice(0, 256)), (100, 256, 1024)),      # [B, T, d] of a projection
         ((2, 50, 8, 128), (slice(None), slice(None), slice(2, 6)), (100, 512, 1024)),       # whole heads
         ((2, 50, 8, 128), (slice(None), slice(None), slice(None), slice(0, 64)), (800, 64, 128)),   # part of every head
