@@ -337,9 +337,11 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  *   cu_seqlens (device int32 [N + 1]): T tokens in all, sequence n has the
  *     tokens [cu_seqlens[n], cu_seqlens[n + 1]).  Sequences may be empty.
  *     Tokens before the first and behind the last are not touched: their o
- *     rows keep what they held.  Ends outside [0, T] are cut to it and a
- *     range that does not increase is empty (no fault, whatever the array
- *     holds); ranges must not overlap.
+ *     rows keep what they held.  The offsets must not decrease.  They are on
+ *     the device and so not refused: an offset counts as the largest up to it,
+ *     cut to [0, T], so that a sequence that would begin before the one in
+ *     front of it ends loses what lies before that end (no fault, no token
+ *     taken twice, whatever the array holds).
  *   o  : bf16 [tokens][HV][d_v], dense
  *   h0 : state rows to start from, or NULL for zero
  *   hT : state rows to write the last states to, or NULL; may equal h0
@@ -355,7 +357,7 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * fp32 sums: hT is accurate to about 1e-5 of its norm.  Supported: d_k == d_v
  * == 128.  Stream-ordered workspace of 66,560 bytes per value head and
  * 64-token chunk (at most tokens / 64 + N chunks), with segments up to half as
- * much again; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
+ * much again, and 4 bytes per offset; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
  * the prefill (kda_device_status).
  */
 int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -377,7 +379,7 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * atomics: the same inputs give the same bits.  Three launches (one more with
  * cu_seqlens, two more where long sequences of few heads run in segments);
  * stream-ordered workspace of 263,168 bytes per value head and 64-token chunk,
- * with segments up to a fifth more (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
+ * with segments up to a fifth more, and 4 bytes per offset (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
  * the forward.  Supported: d_k == d_v == 128.
  *
  * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits

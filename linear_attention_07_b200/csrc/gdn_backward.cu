@@ -1096,6 +1096,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     const size_t kept = (size_t)heads * D * D, mids = kept * (heads > 0 ? between : 0);
     size_t bytes = units * (REC_BYTES + 4 * (size_t)PLANE + 4 * (size_t)UPLANE) + (4 * kept + (a.fwd_parts ? 3 : 6) * mids) * sizeof(float);
     if (scales) bytes += 2 * qk_bytes + u_bytes;
+    if (cu) bytes += ((size_t)N + 1) * sizeof(int);
     uint8_t* ws = nullptr;
     keep_pool_memory();
     e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes, stream);
@@ -1126,6 +1127,8 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         q_stride = k_stride = (int64_t)HK * D;
         v_stride = (int64_t)HV * D;
     }
+    const Seqs given = a.seqs;
+    if (cu && N > 0) a.seqs.cu = reinterpret_cast<const int*>(take(((size_t)N + 1) * sizeof(int)));
     a.h0 = h0;
     a.dhT = dhT;
     a.dh0 = dh0;
@@ -1157,17 +1160,18 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         (!make_token_map(&maps.q, q, tokens, (int64_t)HK * D, q_stride) || !make_token_map(&maps.k, k, tokens, (int64_t)HK * D, k_stride) ||
          !make_token_map(&mv, v, tokens, row, v_stride) || !make_token_map(&maps.dO, dO, tokens, row, row)))
         e = cudaErrorInvalidValue;
+    if (e == cudaSuccess && N > 0)
+        e = prep_launch(maps.q, maps.k, g, beta, given, cu ? const_cast<int*>(a.seqs.cu) : nullptr, const_cast<uint8_t*>(a.rec),
+                        scale, HK, HV, gate_f32, true, stream);
     if (e == cudaSuccess && cu) {
         const int64_t rows[5] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D, HV, HV};
         Outside z = {};
         void* out[5] = {dq, dk, dv, dg, dbeta};
         for (int i = 0; i < 5; ++i) z.p[i] = (__nv_bfloat16*)out[i], z.row[i] = rows[i];
-        outside_kernel<<<64, 256, 0, stream>>>(z, cu, N, tokens);
+        outside_kernel<<<64, 256, 0, stream>>>(z, a.seqs.cu, N, tokens);
         note_launches(1);
         e = cudaGetLastError();
     }
-    if (e == cudaSuccess && N > 0)
-        e = prep_launch(maps.q, maps.k, g, beta, a.seqs, const_cast<uint8_t*>(a.rec), scale, HK, HV, gate_f32, true, stream);
     auto chains = [&](int pass, int64_t blocks) {
         a.pass = pass;
         chains_kernel<<<(unsigned)blocks, NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);

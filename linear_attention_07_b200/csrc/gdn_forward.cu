@@ -533,7 +533,8 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
         const int64_t heads = (int64_t)a.n_long * HV, state = (int64_t)D * D, between = a.segments - 2;
         const size_t rec_bytes = (size_t)slot_count(a.seqs) * HV * REC_BYTES;
         const size_t states = heads > 0 ? (size_t)(heads * (2 + 3 * between) * state) : 0;
-        e = cudaMallocAsync(reinterpret_cast<void**>(&rec), rec_bytes + states * sizeof(float), stream);
+        const size_t offsets = cu ? ((size_t)N + 1) * sizeof(int) : 0;
+        e = cudaMallocAsync(reinterpret_cast<void**>(&rec), rec_bytes + states * sizeof(float) + offsets, stream);
         if (e != cudaSuccess) return e;
         if (states) {
             a.end0 = reinterpret_cast<float*>(rec + rec_bytes);
@@ -542,7 +543,9 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
             a.N = a.M + heads * between * state;
             a.start = a.N + heads * between * state;
         }
-        e = prep_launch(mq, mk, g, beta, a.seqs, rec, scale, HK, HV, gate_f32, false, stream);
+        int* kept = cu ? reinterpret_cast<int*>(rec + rec_bytes + states * sizeof(float)) : nullptr;
+        e = prep_launch(mq, mk, g, beta, a.seqs, kept, rec, scale, HK, HV, gate_f32, false, stream);
+        a.seqs.cu = kept;
     }
     a.rec = rec;
     auto launch = [&](int pass, int64_t blocks) {

@@ -145,7 +145,8 @@ __device__ __forceinline__ void join(const float* x00, float* a10, int ar, const
 
 __global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
-            const void* __restrict__ beta, const Seqs seqs, uint8_t* __restrict__ rec_all, float scale, int HK, int HV,
+            const void* __restrict__ beta, const Seqs seqs, int* __restrict__ offsets, uint8_t* __restrict__ rec_all,
+            float scale, int HK, int HV,
             bool gate_f32, bool backward, uint64_t wait_ns)
 {
     using namespace prep;
@@ -164,6 +165,13 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     const int64_t slot = blockIdx.x / HV;             // heads next to one another: they share K and Q in L2
     const int hv = (int)(blockIdx.x % HV), hk = hv / (HV / HK);
     int n, chunk, begin, end;
+    if (warp == 3 && offsets && blockIdx.x < (unsigned)seqs.n_seq) {         // there are as many slots as sequences
+        n = (int)blockIdx.x;
+        begin = offset_of(seqs, n);
+        if (lane == 0) offsets[n] = begin;
+        if (lane == 0 && n + 1 == seqs.n_seq) offsets[n + 1] = max(begin, cut_offset(seqs, seqs.cu[n + 1]));
+    }
+    __syncwarp();
     if (!slot_chunk(seqs, slot, n, chunk, begin, end)) return;
     const int t0 = begin + chunk * C, nv = min(C, end - t0);
     uint8_t* rec = rec_all + (slot * HV + hv) * REC_BYTES;
@@ -440,14 +448,14 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
 static DeviceFlags g_prep_attr_done;
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream)
+                        int* offsets, uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream)
 {
     const cudaError_t e = once_per_device(g_prep_attr_done, [](int) {
         return cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep::SMEM);
     });
     if (e != cudaSuccess) return e;
     prep_kernel<<<(unsigned)(slot_count(seqs) * HV), prep::NT, prep::SMEM, stream>>>(
-        mq, mk, g, beta, seqs, rec, scale, HK, HV, gate_f32, backward, bounded_wait_limit_ns());
+        mq, mk, g, beta, seqs, offsets, rec, scale, HK, HV, gate_f32, backward, bounded_wait_limit_ns());
     note_launches(1);
     return cudaGetLastError();
 }

@@ -340,3 +340,70 @@ def test_strides_past_32_bits():
         assert torch.equal(a, b)
     for a, b in zip(kda.act_pack8(*far), kda.act_pack8(*near[:3])):
         assert torch.equal(a.data.view(torch.uint8), b.data.view(torch.uint8)) and torch.equal(a.scales, b.scales)
+
+
+def random_offsets(N, T, seed, ordered=False):
+    cu = torch.randint(-100, T + 100, (N + 1,), generator=torch.Generator().manual_seed(seed))
+    return (cu.sort()[0] if ordered else cu).tolist()
+
+
+# an empty range in front of one that begins earlier, above and below 32 sequences; long ones in segments; all of nothing
+BACK = {"empty before an earlier one": (256, [200, 20, 60]),
+        "two in the wrong order": (300, [200, 300, 0, 100]),
+        "one end too far": (500, [0, 100, 1 << 30, 200, 400]),
+        "random": (700, random_offsets(20, 700, 1)),
+        "random, more than 32": (700, random_offsets(70, 700, 2)),
+        "one goes back, more than 32": (2000, sorted(range(0, 2000, 50)) + [300, 1950, 2000]),
+        "segments": (6000, [0, 2500, 100, 6000]),
+        "below zero": (100, [-5, -(1 << 31), -7])}
+
+
+@pytest.mark.parametrize("name", list(BACK))
+def test_offsets_that_go_back(name):
+    """An offset counts as the largest up to it, inside the tokens: bit for bit what the offsets written so give, with
+    nothing left of the call before, whose workspace this one takes."""
+    T, cu = BACK[name]
+    N, HK, HV = len(cu) - 1, 1, 2
+    kept = torch.tensor(cu).clamp(0, T).cummax(0)[0].int()
+    cu = torch.tensor(cu, dtype=torch.int32)
+    other, x = (batch(on_gpu(tokens(T, HK, HV, seed=s))) for s in (91, 92))
+    h0 = torch.randn(N, HV, D, D, generator=torch.Generator().manual_seed(93)).cuda()
+    dO, dhT = cotangents(T, HV, N)
+    dO, dhT = dO[None].cuda(), dhT.cuda()
+
+    def both(y, offsets):
+        o = torch.full((1, T, HV, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        _, S = kda.gdn_chunk_fwd(*y, h0, cu_seqlens=offsets.cuda(), o=o)
+        back = kda.gdn_chunk_bwd(*y, h0, dO, dhT, cu_seqlens=offsets.cuda())
+        packed = kda.gdn_chunk_bwd(*kda.act_pack8(*y[:3]), *y[3:], h0, dO, dhT, cu_seqlens=offsets.cuda())
+        return [o, S, *back, *packed]
+
+    both(other, cu_of([T // N] * N))
+    got = both(x, cu)
+    both(other, cu_of([T // N] * N))
+    for a, b in zip(got, both(x, kept)):
+        assert torch.equal(a, b)
+    first, last = int(kept[0]), int(kept[-1])
+    for t, outside in zip(got[:1] + got[2:7], [7, 0, 0, 0, 0, 0]):
+        assert (t[0, :first] == outside).all() and (t[0, last:] == outside).all()
+    for n in range(N):
+        if kept[n] == kept[n + 1]:
+            assert torch.equal(got[1][n], h0[n]) and torch.equal(got[7][n], dhT[n])
+    assert kda.device_status() == kda.KDA_OK
+
+
+def test_many_sequences():
+    """More sequences than a warp has lanes, more than its square, empty ones among them."""
+    for N, seed in ((33, 1), (130, 2), (1100, 3)):
+        lens = torch.randint(0, 5, (N,), generator=torch.Generator().manual_seed(seed)).tolist()
+        lens[N // 2] = 150
+        T = sum(lens) + 7
+        x = tokens(T, 1, 2, seed=94 + seed)
+        ro, rS = reference(x, lens, begin=3)
+        dO, dhT = cotangents(T, 2, N)
+        cu = cu_of(lens, 3).cuda()
+        o = torch.zeros(1, T, 2, D, dtype=torch.bfloat16, device="cuda")
+        _, S = kda.gdn_chunk_fwd(*batch(on_gpu(x)), cu_seqlens=cu, o=o)
+        assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= TOL_S
+        check(kda.gdn_chunk_bwd(*batch(on_gpu(x)), None, dO[None].cuda(), dhT.cuda(), cu_seqlens=cu),
+              gradients(x, lens, dO, None, dhT, begin=3))
