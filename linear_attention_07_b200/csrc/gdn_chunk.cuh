@@ -65,58 +65,36 @@ __device__ __forceinline__ int64_t first_slot(const Seqs& s, int n)
     return (int64_t)(a / C) + n;
 }
 
-// Sequence and chunk of a slot; false if the slot belongs to none.  Called by
-// whole warps.  The sequence is the last n with offset(n) / 64 + n <= slot, which
-// increases with n.  The offsets are the caller's here, so what counts is the
-// largest up to n (offset_of).  Up to 32 sequences: one trip to memory.  More: a
-// search that takes the offsets as they are, 32 sequences at once and a trip for
-// each factor of 32, whose result is checked against all offsets before it; only
-// where they turn out to go back, 32 sequences after the other.
+// Chunk of a slot in sequence n; false if it has none there.
+__device__ __forceinline__ bool chunk_of(int64_t slot, int n, int begin, int end, int& chunk)
+{
+    const int64_t c = slot - ((int64_t)(begin / C) + n);
+    chunk = (int)c;
+    return c >= 0 && c * C < end - begin;
+}
+
+// The last sequence n with first_slot(n) <= slot, or 0; by whole warps.  32
+// sequences are looked at at once, a trip to memory for each factor of 32 in
+// their number.
+__device__ __forceinline__ int find_sequence(const Seqs& s, int64_t slot)
+{
+    int lo = 0;
+    for (int count = s.n_seq; count > 1;) {
+        const int step = (count + 31) / 32, at = (int)(threadIdx.x & 31) * step;
+        const bool before = at < count && first_slot(s, lo + at) <= slot;
+        const int last = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0) * step;
+        lo += last;
+        count = min(step, count - last);
+    }
+    return lo;
+}
+
+// Sequence and chunk of a slot; false if the slot belongs to none.  By whole warps.
 __device__ __forceinline__ bool slot_chunk(const Seqs& s, int64_t slot, int& n, int& chunk, int& begin, int& end)
 {
-    const int lane = (int)(threadIdx.x & 31);
-    if (!s.cu || s.n_seq > 32) {
-        int lo = 0;
-        for (int count = s.n_seq; count > 1;) {
-            const int step = (count + 31) / 32, at = lane * step;
-            const bool before = at < count && first_slot(s, lo + at) <= slot;
-            const int last = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0) * step;
-            lo += last;
-            count = min(step, count - last);
-        }
-        n = lo;
-        if (s.cu) {
-            begin = offset_of(s, n);
-            end = max(begin, cut_offset(s, s.cu[n + 1]));
-        } else {
-            seq_range(s, n, begin, end);
-        }
-    }
-    if (s.cu && (s.n_seq <= 32 || (n > 0 && begin / C + n > slot) || (n + 1 < s.n_seq && end / C + n + 1 <= slot))) {
-        n = 0;
-        begin = 0;
-        for (int first = 0, most = 0; first < s.n_seq; first += 32) {
-            const int i = first + lane;
-            int m = i < s.n_seq ? cut_offset(s, s.cu[i]) : 0;
-            m = max(m, most);
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) m = max(m, __shfl_sync(0xffffffffu, m, max(lane - off, 0)));
-            const int count = __popc(__ballot_sync(0xffffffffu, i < s.n_seq && m / C + i <= slot));
-            if (count > 0) {
-                n = first + count - 1;
-                begin = __shfl_sync(0xffffffffu, m, count - 1);
-            } else if (first == 0) {                  // before the first sequence
-                begin = __shfl_sync(0xffffffffu, m, 0);
-            }
-            if (count < 32) break;
-            most = __shfl_sync(0xffffffffu, m, 31);
-        }
-        end = max(begin, cut_offset(s, s.cu[n + 1]));
-    }
-    const int64_t c = slot - ((int64_t)(begin / C) + n);
-    if (c < 0 || c * C >= end - begin) return false;
-    chunk = (int)c;
-    return true;
+    n = find_sequence(s, slot);
+    seq_range(s, n, begin, end);
+    return chunk_of(slot, n, begin, end, chunk);
 }
 
 __device__ __forceinline__ int chunk_count(const Seqs& s, int n)

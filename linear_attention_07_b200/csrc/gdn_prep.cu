@@ -141,6 +141,58 @@ __device__ __forceinline__ void join(const float* x00, float* a10, int ar, const
     put<MT>(a10, ar, c, lane, -1.f, d);
     __syncthreads();
 }
+
+// slot_chunk by the caller's offsets, which may go back (offset_of).  As they
+// hardly ever do, the sequence is looked for as if they did not, and the result
+// checked: of fewer than 32 sequences all offsets are looked at anyway, of more
+// what is found is compared with all before it.  Where it does not hold, all
+// sequences in turn, 32 at a time.
+struct Found {
+    int n, begin, end;
+};
+__device__ __noinline__ Found walk_sequences(const int* cu, int n_seq, int tokens, int slot)
+{
+    const int lane = (int)(threadIdx.x & 31);
+    Found f = {0, 0, 0};
+    for (int first = 0, most = 0; first < n_seq; first += 32) {
+        const int i = first + lane, left = n_seq - first;
+        int m = lane < left ? max(most, min(cu[i], tokens)) : most;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) m = max(m, __shfl_sync(0xffffffffu, m, max(lane - off, 0)));
+        const int e = lane < left ? max(m, min(cu[i + 1], tokens)) : m;
+        const int count = __popc(__ballot_sync(0xffffffffu, lane < left && m / C + i <= slot));
+        if (count > 0 || first == 0) {                // none of the first: in front of all sequences
+            f.n = first + max(count - 1, 0);
+            f.begin = __shfl_sync(0xffffffffu, m, max(count - 1, 0));
+            f.end = __shfl_sync(0xffffffffu, e, max(count - 1, 0));
+        }
+        if (count < 32) break;
+        most = __shfl_sync(0xffffffffu, m, 31);
+    }
+    return f;
+}
+__device__ __forceinline__ bool given_slot_chunk(const Seqs& s, int slot, int& n, int& chunk, int& begin, int& end)
+{
+    const int lane = (int)(threadIdx.x & 31);
+    bool right = true;
+    if (s.cu && s.n_seq > 1 && s.n_seq < 32) {        // a lane for each offset
+        const int v = lane <= s.n_seq ? s.cu[lane] : 0x7fffffff, b = cut_offset(s, v);
+        right = __all_sync(0xffffffffu, v <= __shfl_down_sync(0xffffffffu, v, 1));
+        n = max(__popc(__ballot_sync(0xffffffffu, lane < s.n_seq && b / C + lane <= slot)) - 1, 0);
+        begin = __shfl_sync(0xffffffffu, b, n);
+        end = __shfl_sync(0xffffffffu, b, n + 1);
+    } else {
+        n = find_sequence(s, slot);
+        seq_range(s, n, begin, end);
+        if (s.cu && s.n_seq > 1)
+            right = offset_of(s, n) == begin && (n == 0 || begin / C + n <= slot) && (n + 1 == s.n_seq || end / C + n + 1 > slot);
+    }
+    if (!right) {
+        const Found f = walk_sequences(s.cu, s.n_seq, (int)s.tokens, slot);
+        n = f.n, begin = f.begin, end = f.end;
+    }
+    return chunk_of(slot, n, begin, end, chunk);
+}
 }  // namespace prep
 
 __global__ void __launch_bounds__(prep::NT, 6)
@@ -172,7 +224,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         if (lane == 0 && n + 1 == seqs.n_seq) offsets[n + 1] = max(begin, cut_offset(seqs, seqs.cu[n + 1]));
     }
     __syncwarp();
-    if (!slot_chunk(seqs, slot, n, chunk, begin, end)) return;
+    if (!given_slot_chunk(seqs, (int)slot, n, chunk, begin, end)) return;
     const int t0 = begin + chunk * C, nv = min(C, end - t0);
     uint8_t* rec = rec_all + (slot * HV + hv) * REC_BYTES;
     const uint32_t tile = smem_u32(sm), full = smem_u32(&bars[0]), done = smem_u32(&bars[1]);
