@@ -40,7 +40,7 @@ constexpr uint32_t REC_WL = REC_WH + 2 * BOX;        // and the rest
 constexpr uint32_t REC_TH = REC_WL + 2 * BOX;        // T, likewise   [64 x 64]
 constexpr uint32_t REC_TL = REC_TH + BOX;
 constexpr uint32_t REC_NGAM = REC_TL + BOX;          // -gam_r   [64] fp32
-constexpr uint32_t REC_ETA = REC_NGAM + C * 4;       // eta_r
+constexpr uint32_t REC_ETA = REC_NGAM + C * 4;       // eta_r (forward: times ETA_SCALE, and P divided by it)
 constexpr uint32_t REC_GQ = REC_ETA + C * 4;         // scale gam_r
 constexpr uint32_t REC_BETA = REC_GQ + C * 4;        // beta_r (0 behind the sequence)
 constexpr uint32_t REC_PH = REC_BETA + C * 4;        // P, likewise
@@ -53,8 +53,13 @@ static_assert(REC_BYTES == 66560 && REC_W_BYTES % 1024 == 0, "record");
 
 // The forward multiplies P with eta U, which it has as an operand anyway, so
 // there P's columns are divided by eta.  eta is held above 2^-100 for that: a
-// token whose write has decayed further leaves 2^-100 of it in the state.
+// token whose write has decayed further leaves 2^-100 of it in the state.  So
+// that eta U stays in bf16's range with such an eta too (values below 1e-6 lost
+// digits in chunks that decay far), the forward's eta is 2^50 times as large and
+// P / eta that much smaller; K^T (eta U) is divided by it.  U may be between 2^-60
+// (where both planes of eta U are still normal numbers) and 2^77.
 constexpr float ETA_FLOOR_LOG2 = -100.f;
+constexpr float ETA_SCALE = 0x1p50f, ETA_UNSCALE = 0x1p-50f;
 
 __host__ __device__ inline int64_t slot_count(const Seqs& s) { return s.tokens / C + s.n_seq; }
 

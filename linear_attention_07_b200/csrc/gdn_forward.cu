@@ -243,7 +243,8 @@ forward_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    const float2 y = fma2(make_float2(last, last), make_float2(S[b][i], S[b][i + 1]), make_float2(x[i], x[i + 1]));
+                    const float2 d = mul2(make_float2(x[i], x[i + 1]), make_float2(ETA_UNSCALE, ETA_UNSCALE));
+                    const float2 y = fma2(make_float2(last, last), make_float2(S[b][i], S[b][i + 1]), d);
                     S[b][i] = y.x;
                     S[b][i + 1] = y.y;
                 }

@@ -310,7 +310,7 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     float* x11 = reinterpret_cast<float*>(sm + B11);
     {   // thread: one row of [K K^T; Q K^T]; warps 0-1 make A, warps 2-3 P
         const int r = tid % C;
-        const float gh = sGh[r], gl = sGl[r], f = warp < 2 ? sB[r] : scale;
+        const float gh = sGh[r], gl = sGl[r], f = warp < 2 ? sB[r] : backward ? scale : scale * ETA_UNSCALE;
         const float* from_h = warp < 2 ? sGh : sCh;
         const float* from_l = warp < 2 ? sGl : sCl;
         const int last = warp < 2 ? r - 1 : r;        // the row's last column
@@ -384,7 +384,8 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         const float gh = sGh[r], gl = sGl[r], gam = exp2f(gh + gl);
         const float eta = (sGh[C - 1] - gh) + (sGl[C - 1] - gl);
         reinterpret_cast<float*>(rec + REC_NGAM)[r] = -gam;
-        reinterpret_cast<float*>(rec + REC_ETA)[r] = exp2f(backward || eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
+        // powers of two after the exponentials, so that these keep their digits
+        reinterpret_cast<float*>(rec + REC_ETA)[r] = backward ? exp2f(eta) : ETA_SCALE * exp2f(eta > ETA_FLOOR_LOG2 ? eta : ETA_FLOOR_LOG2);
         reinterpret_cast<float*>(rec + REC_GQ)[r] = scale * gam;
         reinterpret_cast<float*>(rec + REC_BETA)[r] = sB[r];
         sNG[r] = -gam;

@@ -225,6 +225,34 @@ def test_forward_decays(decay, beta):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("decay", ["trained", "none", "strong", "far", "reset"])
+def test_forward_is_linear_in_the_values(decay):
+    """o and hT are linear in (v, h0), however small or large these are: powers of two scale every bit of them. 2^-30 and
+    2^30 leave every number that counts (down to 2^-60 of the largest) a normal one, so no rounding changes."""
+    lens = [150, 65, 1, 64]
+    x = tokens(sum(lens), 2, 4, seed=16, decay=decay)
+    ref = list(x)
+    ref[3] = torch.clamp(x[3], min=-1e4)
+    h = torch.randn(4, 4, D, D, generator=torch.Generator().manual_seed(6))
+    for h0 in (None, h):
+        results = []
+        for e in (0, -30, 30):
+            f = 2.0 ** e
+            y = on_gpu(x)
+            y[2].copy_(y[2] * f)
+            o, S = kda.gdn_chunk_fwd(*batch(y), None if h0 is None else (h0 * f).cuda(), cu_seqlens=cu_of(lens).cuda())
+            results.append((o.double() / f, S.double() / f))
+        ro, rS = reference(ref, lens, h0)
+        for o, S in results:
+            assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= TOL_S
+            for a, b in ((o, results[0][0]), (S, results[0][1])):
+                top = b.abs().max()
+                counts = b.abs() >= top * 2.0 ** -60
+                assert torch.equal(a[counts], b[counts])
+                assert bool((a[~counts].abs() <= top * 2.0 ** -59).all())
+
+
+@pytest.mark.gpu
 def test_forward_repeated_keys():
     """The same key at every token: A is dense, and powers of A would lose every digit."""
     x = tokens(256, 1, 2, seed=12, decay="none", beta=0.9, repeat=True)
