@@ -313,7 +313,7 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  * with a scalar log-decay g_t per token and head in the place of KDA's one
  * per channel, and no lower bound on it (-inf resets the state; values below
  * -104, whose exp is zero in fp32, act as -104).  g <= 0 is a precondition,
- * not checked (a chunk that grows by e^40 and more loses its outputs).  Conventions shared by the
+ * not checked.  Conventions shared by the
  * kda_gdn_* calls, beside those at the top:
  *   - HV value heads (v, g, beta, o, states) of which HV / HK consecutive
  *     ones share a query/key head: HV must be a multiple of HK.

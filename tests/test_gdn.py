@@ -3,13 +3,12 @@ oracle, which takes the decay per channel (the same value in every channel).
 
 Tolerances.  bf16 outputs: rounding to nearest is off by at most 2^-8 of the
 value, uniformly spread over that range by 2^-8 / sqrt(3) in the root mean
-square; o takes three such roundings (U and P inside a chunk, o itself), in
-the 2-norm sqrt(3) * 2^-8 / sqrt(3) = 2^-8 (TOL_O).  A gradient takes up to
-nine (TOL_GRAD = 3 * 2^-8 / sqrt(3) each three in quadrature, below).  fp32
-states: operands enter as pairs of bf16, off by at most 2^-16; a chunk's state
-takes K S, X R (two operands and the dropped lo lo product) and K^T U, five
-such errors, so 5 * 2^-16 bounds the 2-norm for one chunk, and since a chunk's
-own error shrinks with the state it is part of, for all (TOL_S).  The single
+square.  TOL_O = 2^-8 leaves room for three such roundings (U and P inside a
+chunk, o itself) in quadrature; the kernels have the last one only, and what
+their pairs of bf16 keep is held in test_gdn_digits.py.  fp32 states: operands
+enter as pairs of bf16, off by at most 2^-16; 5 * 2^-16 is five such errors at
+once, for every chunk, since a chunk's own error shrinks with the state it is
+part of (TOL_S).  The single
 step is fp32 throughout: sums of 128 terms, 128 * 2^-24 (TOL_STEP).
 """
 import numpy as np

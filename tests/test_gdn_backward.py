@@ -4,11 +4,10 @@
 head are the sums over its value heads).
 
 Tolerances.  One rounding to bf16 is off by 2^-8 at most, 2^-8 / sqrt(3) in
-the root mean square.  A gradient's term is a product of two rounded operands,
-at most one of them from a rounded product itself, and the sum is rounded
-again: four roundings in quadrature, 2 * 2^-8 / sqrt(3) (TOL_GRAD).  dg is a
-sum over up to 64 tokens of terms that each carry such an error: sqrt(64) of
-one (TOL_DG).  dh0 is fp32 through pairs of bf16, as the forward's state.
+the root mean square.  These bounds leave room for four of them in quadrature,
+2 * 2^-8 / sqrt(3) (TOL_GRAD), and for dg, a sum over up to 64 tokens, sqrt(64)
+as much (TOL_DG); the kernels round to bf16 once, at the end, and what their
+pairs of bf16 keep is held in test_gdn_digits.py.  dh0 is fp32 through pairs of bf16, as the forward's state.
 """
 import numpy as np
 import pytest
@@ -138,6 +137,29 @@ def test_decays(decay):
     dO, dhT = cotangents(200, 2, 1)
     h0 = torch.randn(1, 2, D, D, generator=torch.Generator().manual_seed(4)) * 0.1
     check(run(x, [200], dO, h0, dhT), reference(ref, [200], dO, h0, dhT))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("decay", ["trained", "strong", "far", "reset"])
+def test_linear_in_values_and_cotangents(decay):
+    """Gradients of powers of two times (v, h0) or (dO, dhT): dq, dk, dg and dbeta take both factors, dv and dh0 the
+    cotangents' only, and no bit changes (numbers 2^-60 below the largest aside)."""
+    lens = [150, 65, 1, 64]
+    T = sum(lens)
+    x = tokens(T, 2, 4, seed=17, decay=decay)
+    dO, dhT = cotangents(T, 4, len(lens))
+    h0 = torch.randn(len(lens), 4, D, D, generator=torch.Generator().manual_seed(7))
+    want = [t.double() for t in run(x, lens, dO, h0, dhT)]
+    for ev, eo in ((-30, 0), (30, 0), (0, -30), (0, 30)):
+        fv, fo = 2.0 ** ev, 2.0 ** eo
+        y = list(on_gpu(x))
+        y[2].copy_(y[2] * fv)
+        got = kda.gdn_chunk_bwd(*batch(y), (h0 * fv).cuda(), (dO * fo)[None].cuda(), (dhT * fo).cuda(), cu_seqlens=cu_of(lens).cuda())
+        for name, a, b in zip(("dq", "dk", "dv", "dg", "dbeta", "dh0"), got, want):
+            a = a.double() / (fo if name in ("dv", "dh0") else fv * fo)
+            counts = b.abs() >= b.abs().max() * 2.0 ** -60
+            assert torch.equal(a[counts], b[counts]), (name, ev, eo)
+    assert kda.device_status() == kda.KDA_OK
 
 
 @pytest.mark.gpu
