@@ -322,7 +322,8 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  *     from one token to the next (multiples of 8, at least HK * d_k or
  *     HV * d_v), so the three may be slices of one projection's output.
  *     q, k and v are read only.
- *   - g, beta: [HV] per token, dense; fp32 if gate_f32 is not 0, else bf16.
+ *   - g, beta: [HV] per token, dense; both bf16 if gate_f32 is 0, g fp32 and
+ *     beta bf16 if it is KDA_GATE_F32_BETA_BF16, both fp32 for other values.
  *   - states: fp32 [rows][HV][d_k][d_v], the layout of the kda_* states.
  *   - slots (optional, device int32 [N]): the state row of each sequence or
  *     request in a pool of n_slots rows; rows of a call must be distinct (two
@@ -330,6 +331,8 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  *     A value outside [0, n_slots) is a padded entry: it has no state.
  *     slots NULL: row n, and n_slots is not read.
  */
+
+#define KDA_GATE_F32_BETA_BF16 2
 
 /*
  * kda_gdn_chunk_fwd -- chunked forward (prefill, training) over N sequences.

@@ -444,6 +444,8 @@ def chunk_bwd_raw(q_raw, k_raw, v, z, beta, h0, dO, dhT=None, *, want_dh0=True):
 
 
 # ------------------------------------- one decay per head (gated delta rule) --
+GATE_F32_BETA_BF16 = 2
+
 # These calls are made once per layer and token, so their checks are written to
 # cost little: one comparison of type, shape and device per tensor, the reason
 # looked for only when it fails.
@@ -514,11 +516,14 @@ def _check_tokens(t, name, lead, heads, d, dev):
 
 
 def _check_gates(g, beta, shape, dev):
-    """Addresses of g and beta and whether they are fp32."""
-    kind = g.dtype
+    """Addresses of g and beta and the C calls' gate_f32: both bf16, both fp32, or g fp32 and beta bf16."""
+    kind, other = g.dtype, beta.dtype
     if kind is not _F32 and kind is not _BF16:
         raise TypeError("g must be torch.float32 or torch.bfloat16, got %s" % kind)
-    return _dense(g, "g", kind, shape, dev), _dense(beta, "beta", kind, shape, dev), 1 if kind is _F32 else 0
+    if other is not kind and (kind is _BF16 or other is not _BF16):
+        raise TypeError("beta must be %s%s, got %s" % (kind, " or torch.bfloat16" if kind is _F32 else "", other))
+    return (_dense(g, "g", kind, shape, dev), _dense(beta, "beta", other, shape, dev),
+            0 if kind is _BF16 else 1 if other is _F32 else GATE_F32_BETA_BF16)
 
 
 def _gdn_sequences(B, T, cu_seqlens, dev):
@@ -539,9 +544,10 @@ def gdn_chunk_fwd(q, k, v, g, beta, h0=None, *, scale=1.0, cu_seqlens=None, slot
     (kda_gdn_chunk_fwd), bf16 in and out, fp32 state.
 
     q, k: [B, T, HK, 128]; v: [B, T, HV, 128] (bf16; slices of one wider tensor
-    are taken as they are); g, beta: [B, T, HV], fp32 or bf16.  With cu_seqlens
-    (int32 [N + 1], on the device) B is 1 and sequence n has the tokens
-    [cu_seqlens[n], cu_seqlens[n + 1]); else N = B.
+    are taken as they are); g, beta: [B, T, HV], fp32 or bf16, or an fp32 g with
+    a bf16 beta.  With cu_seqlens (int32 [N + 1], not decreasing, on the device)
+    B is 1 and sequence n has the tokens [cu_seqlens[n], cu_seqlens[n + 1]); else
+    N = B.
 
     h0: [N, HV, 128, 128] fp32 or None; hT may be passed as h0.  With slots
     (int32 [N], on the device) h0 is a pool [rows, HV, 128, 128]: sequence n
@@ -624,7 +630,8 @@ def gdn_decode_step(q, k, v, g, beta, state, *, scale=1.0, slots=None, o=None):
     (kda_gdn_decode_step); `state` is updated in place.
 
     q, k: [N, HK, dk]; v: [N, HV, dv] (bf16; slices of one wider tensor are
-    taken as they are); g, beta: [N, HV], fp32 or bf16; state: fp32
+    taken as they are); g, beta: [N, HV], fp32 or bf16, or an fp32 g with a bf16
+    beta; state: fp32
     [N, HV, dk, dv], or a pool [rows, HV, dk, dv] with slots [N] (int32, on the
     device) naming each request's row; a slot outside the pool marks a padded
     request (o = 0, no state).  Returns o [N, HV, dv] bf16."""

@@ -605,7 +605,7 @@ struct LocalArgs {
     __nv_bfloat16 *dq, *dk, *dv, *dg, *dbeta;
     float scale;
     int HK, HV;
-    bool gate_f32;
+    int f32_gates;
     uint64_t wait_ns;
 };
 struct LocalMaps {
@@ -808,7 +808,7 @@ local_kernel(const __grid_constant__ LocalMaps maps, const __grid_constant__ Loc
             double x[2];
             for (int i = 0; i < 2; ++i) {
                 const int rr = 2 * lane + i;
-                x[i] = rr < nv ? (double)cut_decay(gate(p.g, (int64_t)(t0 + rr) * p.HV + hv, p.gate_f32)) : 0.0;
+                x[i] = rr < nv ? (double)cut_decay(gate(p.g, (int64_t)(t0 + rr) * p.HV + hv, p.f32_gates & G_F32)) : 0.0;
             }
             double sum = x[0] + x[1];
 #pragma unroll
@@ -1066,7 +1066,7 @@ cudaError_t act8_launch(int count, const void* const* src, void* const* dst, voi
 cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
                                 const void* beta, const float* h0, const void* dO, const float* dhT, void* dq, void* dk,
                                 void* dv, void* dg, void* dbeta, float* dh0, const int* cu, float scale, int N, int T,
-                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32,
+                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, int f32_gates,
                                 cudaStream_t stream)
 {
     using namespace gdn;
@@ -1151,7 +1151,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
     l.scale = scale;
     l.HK = HK;
     l.HV = HV;
-    l.gate_f32 = gate_f32;
+    l.f32_gates = f32_gates;
     l.wait_ns = a.wait_ns;
     LocalMaps maps;
     CUtensorMap mv;
@@ -1162,7 +1162,7 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         e = cudaErrorInvalidValue;
     if (e == cudaSuccess && N > 0)
         e = prep_launch(maps.q, maps.k, g, beta, given, cu ? const_cast<int*>(a.seqs.cu) : nullptr, const_cast<uint8_t*>(a.rec),
-                        scale, HK, HV, gate_f32, true, stream);
+                        scale, HK, HV, f32_gates, true, stream);
     if (e == cudaSuccess && cu) {
         const int64_t rows[5] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D, HV, HV};
         Outside z = {};

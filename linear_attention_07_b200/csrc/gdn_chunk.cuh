@@ -335,7 +335,7 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
 
 // offsets: where the sequences' offsets go ([n_seq + 1]) that the kernels behind it take for cu; null without cu.
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        int* offsets, uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream);
+                        int* offsets, uint8_t* rec, float scale, int HK, int HV, int f32_gates, bool backward, cudaStream_t stream);
 
 }  // namespace gdn
 }  // namespace kda

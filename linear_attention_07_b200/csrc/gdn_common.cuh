@@ -56,7 +56,8 @@ __device__ __forceinline__ int state_row(const Seqs& s, int n)
     return r >= 0 && r < s.n_slots ? r : -1;
 }
 
-// Gates are fp32 or bf16.
+// Gates are fp32 or bf16; which of them are fp32 goes by these bits.
+constexpr int G_F32 = 1, BETA_F32 = 2;
 __device__ __forceinline__ float gate(const void* p, int64_t i, bool f32)
 {
     return f32 ? reinterpret_cast<const float*>(p)[i]

@@ -499,7 +499,7 @@ static void choose_segments(fw::Args& a, int64_t heads, bool ragged)
 cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
                                float scale, int N, int T, int HK, int HV, int64_t q_stride, int64_t k_stride,
-                               int64_t v_stride, bool gate_f32, cudaStream_t stream)
+                               int64_t v_stride, int f32_gates, cudaStream_t stream)
 {
     using namespace gdn;
     fw::Args a = {};
@@ -545,7 +545,7 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
             a.start = a.N + heads * between * state;
         }
         int* kept = cu ? reinterpret_cast<int*>(rec + rec_bytes + states * sizeof(float)) : nullptr;
-        e = prep_launch(mq, mk, g, beta, a.seqs, kept, rec, scale, HK, HV, gate_f32, false, stream);
+        e = prep_launch(mq, mk, g, beta, a.seqs, kept, rec, scale, HK, HV, f32_gates, false, stream);
         a.seqs.cu = kept;
     }
     a.rec = rec;

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, int* __restrict__ offsets, uint8_t* __restrict__ rec_all,
             float scale, int HK, int HV,
-            bool gate_f32, bool backward, uint64_t wait_ns)
+            int f32_gates, bool backward, uint64_t wait_ns)
 {
     using namespace prep;
     using namespace tc;
@@ -273,12 +273,14 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         const int64_t at = (int64_t)(t0 + 2 * lane) * HV + hv;
         const bool real[2] = {2 * lane < nv, 2 * lane + 1 < nv};
         float gi[2] = {0.f, 0.f}, bi[2] = {0.f, 0.f};
-        auto load = [&](bool f32) {                   // all loads at once, whatever the type
+        auto load = [&](bool g_f32, bool beta_f32) {  // all loads at once, whatever the types
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (real[i]) gi[i] = gate(g, at + i * HV, f32), bi[i] = gate(beta, at + i * HV, f32);
+                if (real[i]) gi[i] = gate(g, at + i * HV, g_f32), bi[i] = gate(beta, at + i * HV, beta_f32);
         };
-        if (gate_f32) load(true); else load(false);
+        if (f32_gates == 0) load(false, false);
+        else if (f32_gates == G_F32) load(true, false);
+        else load(true, true);
         const double x0 = (double)cut_decay(gi[0]), x1 = (double)cut_decay(gi[1]);
         double sum = x0 + x1;
 #pragma unroll
@@ -501,14 +503,14 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
 static DeviceFlags g_prep_attr_done;
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
-                        int* offsets, uint8_t* rec, float scale, int HK, int HV, bool gate_f32, bool backward, cudaStream_t stream)
+                        int* offsets, uint8_t* rec, float scale, int HK, int HV, int f32_gates, bool backward, cudaStream_t stream)
 {
     const cudaError_t e = once_per_device(g_prep_attr_done, [](int) {
         return cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep::SMEM);
     });
     if (e != cudaSuccess) return e;
     prep_kernel<<<(unsigned)(slot_count(seqs) * HV), prep::NT, prep::SMEM, stream>>>(
-        mq, mk, g, beta, seqs, offsets, rec, scale, HK, HV, gate_f32, backward, bounded_wait_limit_ns());
+        mq, mk, g, beta, seqs, offsets, rec, scale, HK, HV, f32_gates, backward, bounded_wait_limit_ns());
     note_launches(1);
     return cudaGetLastError();
 }

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(STEP_NT)
 step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k,
             const __nv_bfloat16* __restrict__ v, const void* __restrict__ g, const void* __restrict__ beta,
             float* __restrict__ state, __nv_bfloat16* __restrict__ o, const int* __restrict__ slots, int n_slots,
-            float scale, int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32)
+            float scale, int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, int f32_gates)
 {
     using M = StepMap<DK, DV>;
     constexpr int CG = M::CG, RSTEP = M::RSTEP, ROWS = M::ROWS;
@@ -61,7 +61,7 @@ step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
     }
     const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(v + n * v_stride + (int64_t)hv * DV + 4 * cg);
     const float2 v01 = __bfloat1622float2(v2[0]), v23 = __bfloat1622float2(v2[1]);
-    const float a = expf(gate(g, n * HV + hv, gate_f32)), b = gate(beta, n * HV + hv, gate_f32);
+    const float a = expf(gate(g, n * HV + hv, f32_gates & G_F32)), b = gate(beta, n * HV + hv, f32_gates & BETA_F32);
     __syncthreads();
     if (tid < 32) {
         float acc = 0.f;
@@ -114,14 +114,14 @@ step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 
 cudaError_t gdn_step_launch(const void* q, const void* k, const void* v, const void* g, const void* beta, float* state,
                             void* o, const int* slots, int n_slots, float scale, int N, int HK, int HV, int dk, int dv,
-                            int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32, cudaStream_t stream)
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int f32_gates, cudaStream_t stream)
 {
     using namespace gdn;
     using bf = __nv_bfloat16;
 #define GDN_STEP(DK_, DV_)                                                                                      \
     step_kernel<DK_, DV_><<<dim3((unsigned)N, (unsigned)HV), STEP_NT, 0, stream>>>(                              \
         (const bf*)q, (const bf*)k, (const bf*)v, g, beta, state, (bf*)o, slots, n_slots, scale, HK, HV,         \
-        q_stride, k_stride, v_stride, gate_f32)
+        q_stride, k_stride, v_stride, f32_gates)
 #define GDN_STEP_DV(DK_) \
     if (dv == 128) GDN_STEP(DK_, 128); else if (dv == 64) GDN_STEP(DK_, 64); else GDN_STEP(DK_, 32)
     if (dk == 128) { GDN_STEP_DV(128); }

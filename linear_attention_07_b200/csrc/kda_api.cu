@@ -2,7 +2,7 @@
 // Every argument error is detected here, before any launch.
 #include <atomic>
 
-#include "kda_common.cuh"
+#include "gdn_common.cuh"
 
 namespace kda {
 
@@ -71,15 +71,15 @@ cudaError_t prefill_serial_launch(const void* q, const void* k, const void* v,
 
 cudaError_t gdn_step_launch(const void* q, const void* k, const void* v, const void* g, const void* beta, float* state,
                             void* o, const int* slots, int n_slots, float scale, int N, int HK, int HV, int dk, int dv,
-                            int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32, cudaStream_t stream);
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int f32_gates, cudaStream_t stream);
 cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, const void* g, const void* beta,
                                const float* h0, void* o, float* hT, const int* cu, const int* slots, int n_slots,
                                float scale, int N, int T, int HK, int HV, int64_t q_stride, int64_t k_stride,
-                               int64_t v_stride, bool gate_f32, cudaStream_t stream);
+                               int64_t v_stride, int f32_gates, cudaStream_t stream);
 cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
                                 const void* beta, const float* h0, const void* dO, const float* dhT, void* dq, void* dk,
                                 void* dv, void* dg, void* dbeta, float* dh0, const int* cu, float scale, int N, int T,
-                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, bool gate_f32,
+                                int HK, int HV, int64_t q_stride, int64_t k_stride, int64_t v_stride, int f32_gates,
                                 cudaStream_t stream);
 int gdn_prep_status(cudaStream_t stream);
 int gdn_backward_status(cudaStream_t stream);
@@ -150,6 +150,16 @@ static int check_gdn_tokens(const void* cu, const void* slots, int n_slots, int 
 static bool elem_ok(const void* p, unsigned bytes)
 {
     return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+// Which gates are fp32, from a call's gate_f32.
+static int f32_gates(int gate_f32)
+{
+    return gate_f32 == 0 ? 0 : gate_f32 == KDA_GATE_F32_BETA_BF16 ? gdn::G_F32 : gdn::G_F32 | gdn::BETA_F32;
+}
+static bool gates_ok(const void* g, const void* beta, int gate_f32)
+{
+    const int f32 = f32_gates(gate_f32);
+    return elem_ok(g, f32 & gdn::G_F32 ? 4 : 2) && elem_ok(beta, f32 & gdn::BETA_F32 ? 4 : 2);
 }
 
 }  // namespace kda
@@ -346,11 +356,10 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
     if (T == 0 && hT == nullptr) return KDA_OK;
     if (T > 0) {
         if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(o)) return KDA_ERR_INVALID_ARG;
-        const unsigned ge = gate_f32 ? 4 : 2;
-        if (!elem_ok(g, ge) || !elem_ok(beta, ge)) return KDA_ERR_INVALID_ARG;
+        if (!gates_ok(g, beta, gate_f32)) return KDA_ERR_INVALID_ARG;
     }
     return status_of(gdn_forward_launch(q, k, v, g, beta, h0, o, hT, cu_seqlens, slots, n_slots, scale, N, T, HK, HV,
-                                        q_stride, k_stride, v_stride, gate_f32 != 0, (cudaStream_t)stream));
+                                        q_stride, k_stride, v_stride, f32_gates(gate_f32), (cudaStream_t)stream));
 }
 
 static int gdn_chunk_bwd_any(const void* q, const void* k, const void* v, const void* const* scales, const void* g,
@@ -370,12 +379,11 @@ static int gdn_chunk_bwd_any(const void* q, const void* k, const void* v, const 
     if (T > 0) {
         if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(dO) || !ptr_ok(dq) || !ptr_ok(dk) || !ptr_ok(dv))
             return KDA_ERR_INVALID_ARG;
-        const unsigned ge = gate_f32 ? 4 : 2;
-        if (!elem_ok(g, ge) || !elem_ok(beta, ge) || !elem_ok(dg, 2) || !elem_ok(dbeta, 2)) return KDA_ERR_INVALID_ARG;
+        if (!gates_ok(g, beta, gate_f32) || !elem_ok(dg, 2) || !elem_ok(dbeta, 2)) return KDA_ERR_INVALID_ARG;
         if (scales && (!scales[0] || !scales[1] || !scales[2])) return KDA_ERR_INVALID_ARG;
     }
     return status_of(gdn_backward_launch(q, k, v, scales, g, beta, h0, dO, dhT, dq, dk, dv, dg, dbeta, dh0, cu_seqlens,
-                                         scale, N, T, HK, HV, q_stride, k_stride, v_stride, gate_f32 != 0,
+                                         scale, N, T, HK, HV, q_stride, k_stride, v_stride, f32_gates(gate_f32),
                                          (cudaStream_t)stream));
 }
 
@@ -416,10 +424,9 @@ int kda_gdn_decode_step(const void* q, const void* k, const void* v, const void*
     if (st != KDA_OK) return st;
     if ((int64_t)N * HV == 0) return KDA_OK;
     if (!ptr_ok(q) || !ptr_ok(k) || !ptr_ok(v) || !ptr_ok(state) || !ptr_ok(o)) return KDA_ERR_INVALID_ARG;
-    const unsigned ge = gate_f32 ? 4 : 2;
-    if (!elem_ok(g, ge) || !elem_ok(beta, ge) || (slots && !elem_ok(slots, 4))) return KDA_ERR_INVALID_ARG;
+    if (!gates_ok(g, beta, gate_f32) || (slots && !elem_ok(slots, 4))) return KDA_ERR_INVALID_ARG;
     return status_of(gdn_step_launch(q, k, v, g, beta, state, o, slots, slots ? n_slots : N, scale, N, HK, HV, d_k, d_v,
-                                     q_stride, k_stride, v_stride, gate_f32 != 0, (cudaStream_t)stream));
+                                     q_stride, k_stride, v_stride, f32_gates(gate_f32), (cudaStream_t)stream));
 }
 
 static int act8_any(int count, const void* const* src, void* const* dst, void* const* scales, const int64_t* rows,
@@ -492,6 +499,6 @@ int kda_prefill_path(int B, int T, int H)
     return prefill_path_of(B, T, H);
 }
 
-int kda_version(void) { return (1 << 16) | 0; }
+int kda_version(void) { return (1 << 16) | 1; }
 
 }  // extern "C"

@@ -143,6 +143,33 @@ def test_refusals_of_the_binding():
         kda.gdn_decode_step(*[t[0] for t in x], torch.zeros(4, 4, D, D))
 
 
+def test_gate_types():
+    """Both fp32, both bf16, or an fp32 decay with a bf16 write strength."""
+    kda._types()
+    f, b = torch.zeros(2, 4), torch.zeros(2, 4, dtype=torch.bfloat16)
+    of = lambda g, beta: kda._check_gates(g, beta, (2, 4), g.device)[2]
+    assert (of(b, b), of(f, f), of(f, b)) == (0, 1, kda.GATE_F32_BETA_BF16)
+    for g, beta in ((b, f), (f.double(), f), (f, f.double()), (f.half(), b), (b, b.half()), (f, b.half()), (f.int(), f)):
+        with pytest.raises(TypeError):
+            of(g, beta)
+    for g, beta in ((f, b[:1]), (f[:, ::2], b), (f, b.t())):
+        with pytest.raises(ValueError):
+            of(g, beta)
+    import ctypes
+    lib, A = kda.load_library(), ctypes.c_void_p(0x10000)
+    n0 = lib.kda_launch_count()
+    for gate, g, beta in ((2, 0x10002, 0x10000), (2, 0x10000, 0x10001), (2, 0x10000, 0), (2, 0, 0x10000), (1, 0x10000, 0x10002),
+                          (3, 0x10000, 0x10002), (0, 0x10001, 0x10000)):
+        P = ctypes.c_void_p
+        assert lib.kda_gdn_chunk_fwd(A, A, A, P(g), P(beta), None, A, None, None, None, 0, 1.0, 1, 64, 2, 4, 128, 128, 256, 256,
+                                     512, gate, None) == kda.KDA_ERR_INVALID_ARG
+        assert lib.kda_gdn_decode_step(A, A, A, P(g), P(beta), A, A, None, 0, 1.0, 1, 2, 4, 128, 128, 256, 256, 512, gate,
+                                       None) == kda.KDA_ERR_INVALID_ARG
+        assert lib.kda_gdn_chunk_bwd(A, A, A, P(g), P(beta), None, A, None, A, A, A, A, A, A, None, 1.0, 1, 64, 2, 4, 128, 128,
+                                     256, 256, 512, gate, None) == kda.KDA_ERR_INVALID_ARG
+    assert lib.kda_launch_count() == n0
+
+
 BROADCAST = [((1, 1, 2, D), (1, 4096, 2, D)), ((1, 2, D), (64, 2, D)), ((1, 1, 2, D), (8, 1, 2, D)),
              ((3, 1, 2, D), (3, 5, 2, D)), ((1, 5, 2, D), (3, 5, 2, D)), ((2, 1, 4, 1, 2, D), (2, 3, 4, 1, 2, D)),
              ((D,), (5, 1, D))]

@@ -407,3 +407,26 @@ def test_many_sequences():
         assert rel(o[0], ro) <= TOL_O and rel(S, rS) <= TOL_S
         check(kda.gdn_chunk_bwd(*batch(on_gpu(x)), None, dO[None].cuda(), dhT.cuda(), cu_seqlens=cu),
               gradients(x, lens, dO, None, dhT, begin=3))
+
+
+def test_fp32_decay_with_bf16_write_strength():
+    """Bit for bit what both in fp32 give, the write strength's values being the same."""
+    x, h0 = tokens(300, 2, 4, seed=98), torch.randn(3, 4, D, D, generator=torch.Generator().manual_seed(99)).cuda()
+    q, k, v, g, b = batch(on_gpu(x))
+    b = b.to(torch.bfloat16)
+    cu = cu_of([100, 7, 193]).cuda()
+    dO, dhT = cotangents(300, 4, 3)
+    dO, dhT = dO[None].cuda(), dhT.cuda()
+
+    def calls(beta):
+        S = h0.clone()
+        step = kda.gdn_decode_step(*(t[0, :3] for t in (q, k, v, g, beta)), S)
+        return [*kda.gdn_chunk_fwd(q, k, v, g, beta, h0, cu_seqlens=cu), step, S,
+                *kda.gdn_chunk_bwd(q, k, v, g, beta, h0, dO, dhT, cu_seqlens=cu),
+                *kda.gdn_chunk_bwd(*kda.act_pack8(q, k, v), g, beta, h0, dO, dhT, cu_seqlens=cu)]
+
+    for a, w in zip(calls(b), calls(b.float())):
+        assert a.dtype == w.dtype and torch.equal(a, w)
+    with pytest.raises(TypeError):
+        kda.gdn_chunk_fwd(q, k, v, g.to(torch.bfloat16), b.float(), cu_seqlens=cu)
+    assert kda.device_status() == kda.KDA_OK
