@@ -18,7 +18,9 @@ void note_launches(int n);
 // Kernel attributes (the dynamic shared-memory limit) and memory-pool
 // settings apply to one device only, so one-time setup is kept per device
 // ordinal.  The setup calls are idempotent: two host threads that race on a
-// device's first call may both run them, which is harmless.
+// device's first call may both run them, which is harmless.  They are no part
+// of what a stream may be capturing meanwhile, and some would end the capture:
+// the thread's capture mode is relaxed for them.
 constexpr int MAX_DEVICES = 64;
 using DeviceFlags = std::atomic<bool>[MAX_DEVICES];
 
@@ -32,7 +34,11 @@ cudaError_t once_per_device(DeviceFlags& done, F&& setup)
     if (e != cudaSuccess) return e;
     const bool tracked = dev >= 0 && dev < MAX_DEVICES;
     if (tracked && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
     e = setup(dev);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (e == cudaSuccess && tracked) done[dev].store(true, std::memory_order_release);
     return e;
 }

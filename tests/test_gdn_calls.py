@@ -430,3 +430,79 @@ def test_fp32_decay_with_bf16_write_strength():
     with pytest.raises(TypeError):
         kda.gdn_chunk_fwd(q, k, v, g.to(torch.bfloat16), b.float(), cu_seqlens=cu)
     assert kda.device_status() == kda.KDA_OK
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import linear_attention_07_b200 as kda
+from test_gdn import batch, on_gpu, tokens
+from test_gdn_backward import cotangents
+x = batch(on_gpu(tokens(2200, 2, 4, seed=100)))
+dO, dhT = (t.cuda() for t in cotangents(2200, 4, 1))
+S = torch.zeros(1, 4, 128, 128, device="cuda")
+def calls():
+    o, h = kda.gdn_chunk_fwd(*x)
+    packed = kda.act_pack8(*x[:3])
+    return [o, h, *kda.gdn_chunk_bwd(*packed, *x[3:], None, dO[None], dhT), kda.gdn_decode_step(*(t[0, :1] for t in x), S)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+torch.cuda.synchronize()
+S.zero_()
+assert all(torch.equal(a, b) for a, b in zip(got, calls()))
+assert kda.device_status() == kda.KDA_OK
+print("captured first")
+"""
+
+
+def test_first_call_of_a_process_is_captured():
+    """What a call sets up once per device may happen inside a capture."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stderr
+
+
+def test_calls_from_threads():
+    """Calls from several host threads, each on a stream of its own."""
+    import threading
+    xs = [batch(on_gpu(tokens(T, 2, 4, seed=101 + T))) for T in (100, 700, 2300)]
+    dOs = [cotangents(x[0].shape[1], 4, 1) for x in xs]
+    dOs = [(a[None].cuda(), b.cuda()) for a, b in dOs]
+
+    def calls(i):
+        x, (dO, dhT) = xs[i], dOs[i]
+        o, S = kda.gdn_chunk_fwd(*x)
+        packed = kda.act_pack8(*x[:3])
+        return [o, S, *kda.gdn_chunk_bwd(*x, None, dO, dhT), *kda.gdn_chunk_bwd(*packed, *x[3:], None, dO, dhT),
+                *(kda.act_unpack8(p) for p in packed)]
+
+    want = [calls(i) for i in range(3)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def thread(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(6):
+                    got = calls(i)
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[i])):
+                        wrong.append(i)
+        except Exception as e:
+            wrong.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+    assert kda.device_status() == kda.KDA_OK
