@@ -28,10 +28,10 @@ void keep_pool_memory()
 {
     once_per_device(g_pool_done, [](int dev) {
         cudaMemPool_t pool;
-        if (cudaDeviceGetDefaultMemPool(&pool, dev) == cudaSuccess) {
-            uint64_t keep = UINT64_MAX;
-            cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
-        }
+        uint64_t keep = UINT64_MAX;
+        if (cudaDeviceGetDefaultMemPool(&pool, dev) != cudaSuccess ||
+            cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep) != cudaSuccess)
+            cudaGetLastError();
         return cudaSuccess;   // a pool that keeps nothing only costs speed
     });
 }
@@ -103,6 +103,7 @@ static bool sizes_ok(int64_t a, int64_t b, int64_t c, int64_t d)
 static int status_of(cudaError_t e)
 {
     if (e == cudaSuccess) return KDA_OK;
+    cudaGetLastError();      // reported here: the next call's check of its launches must not find it
     return e == cudaErrorMemoryAllocation ? KDA_ERR_NO_MEMORY : KDA_ERR_CUDA;
 }
 
@@ -479,7 +480,10 @@ int kda_device_status(kda_stream_t stream)
     for (auto* part : {prefill_device_status, bwd_device_status, gdn_prep_status, gdn_forward_status,
                        gdn_backward_status}) {
         const int s = part((cudaStream_t)stream);     // each reads and clears its own word
-        if (s == KDA_ERR_CUDA) return s;
+        if (s == KDA_ERR_CUDA) {
+            cudaGetLastError();
+            return s;
+        }
         if (s != KDA_OK) st = s;
     }
     return st;

@@ -506,3 +506,47 @@ def test_calls_from_threads():
         t.join()
     assert not wrong, wrong
     assert kda.device_status() == kda.KDA_OK
+
+
+NO_MEMORY = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import linear_attention_07_b200 as kda
+T, HK, HV = 16384, 1, 64
+q, k = (torch.randn(1, T, HK, 128, device="cuda").to(torch.bfloat16) for _ in range(2))
+v = torch.randn(1, T, HV, 128, device="cuda").to(torch.bfloat16)
+g, b = -torch.rand(1, T, HV, device="cuda"), torch.rand(1, T, HV, device="cuda")
+o, S = torch.empty_like(v), torch.zeros(1, HV, 128, 128, device="cuda")
+kda.act_pack8(k)
+torch.cuda.empty_cache()
+free, _ = torch.cuda.mem_get_info()
+held = torch.empty(free - (700 << 20), dtype=torch.uint8, device="cuda")      # of 1.09 GB of workspace
+for _ in range(2):
+    try:
+        kda.gdn_chunk_fwd(q, k, v, g, b, o=o, hT=S)
+        raise SystemExit("there was memory")
+    except kda.KdaError as e:
+        assert e.status == kda.KDA_ERR_NO_MEMORY, e
+    assert not S.any()
+    kda.act_pack8(k)                    # not blamed for it
+    kda.gdn_decode_step(*(t[0, :1] for t in (q, k, v, g, b)), S)
+    S.zero_()
+del held
+torch.cuda.empty_cache()
+kda.gdn_chunk_fwd(q, k, v, g, b, o=o, hT=S)
+torch.cuda.synchronize()
+assert S.any() and kda.device_status() == kda.KDA_OK
+print("said so")
+"""
+
+
+def test_no_memory_for_the_workspace():
+    """KDA_ERR_NO_MEMORY, nothing written, and the calls behind it go on."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = NO_MEMORY.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "said so" in r.stdout, r.stderr
