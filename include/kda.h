@@ -28,12 +28,16 @@
  * Conventions shared by every entry point:
  *   - All tensor pointers are DEVICE pointers, owned by the caller, 16-byte
  *     aligned, densely packed in the row-major layouts given per function.
- *     No entry point keeps a pointer after it returns.  Only the bf16
- *     prefill calls kda_chunk_fwd, kda_chunk_fwd_raw and kda_chunk_fwd_states
- *     take memory of their own, and only on the segment-scan path (see
- *     kda_chunk_fwd): stream-ordered workspace (cudaMallocAsync /
- *     cudaFreeAsync on `stream`).  kda_chunk_fwd_noalloc is kda_chunk_fwd
- *     without any allocation.
+ *     No entry point keeps a pointer after it returns.  Memory of their own
+ *     is taken by the bf16 prefill calls kda_chunk_fwd, kda_chunk_fwd_raw and
+ *     kda_chunk_fwd_states, only on the segment-scan path (see kda_chunk_fwd;
+ *     kda_chunk_fwd_noalloc is kda_chunk_fwd without any allocation), by
+ *     kda_chunk_bwd and kda_chunk_bwd_raw, and by the kda_gdn_chunk_* calls:
+ *     stream-ordered workspace (cudaMallocAsync /
+ *     cudaFreeAsync on `stream`), of the size that each states.  It comes from
+ *     the device's default memory pool, which keeps what it has got for the
+ *     calls behind (the first such call sets its release threshold), out of
+ *     reach of other allocators: cudaMemPoolTrimTo gives it back.
  *   - Calls are asynchronous on `stream` (0 = legacy default stream) and do
  *     no host synchronisation.  Asynchronous device errors surface at the
  *     caller's next synchronisation, as for any CUDA launch.
@@ -45,7 +49,7 @@
  *     library's global state is a launch counter (atomic), one-time set-up
  *     per device (kernel shared-memory limits, the SM count, the memory
  *     pool's release threshold; idempotent, done by the first call on each
- *     device), one bounded-wait error word per device (kda_device_status)
+ *     device), the bounded waits' error words per device (kda_device_status)
  *     and the scratch array of kda_chunk_fwd_noalloc, whose segment-scan
  *     calls must be ordered with one another (see there).
  */
@@ -352,17 +356,21 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  *   slots name the rows of both h0 and hT.  A padded sequence starts from
  *   zero and keeps no state; an empty one copies its h0 row (or zeros).
  * Tokens behind a sequence's end inside its last 64-token chunk count as zero
- * whatever they hold.  Two launches: every chunk's state-free part for all
+ * whatever they hold.  A NaN or an infinity in a token of a sequence makes o NaN
+ * from the start of the token's 64-token chunk on, and hT, in the value heads
+ * that it enters; other sequences stay as they are.  Two launches: every chunk's state-free part for all
  * chunks at once, then one CTA per sequence and value head along the chunks.
  * Long sequences of few heads (32 chunks on average, at least three CTAs per
  * sequence and head at once) are cut into segments instead, joined as
  * kda_state_chain joins them: four launches.  K, Q and V enter
  * the products as bf16, the state and what is computed as pairs of bf16 with
- * fp32 sums: hT is accurate to about 1e-5 of its norm.  Supported: d_k == d_v
- * == 128.  Stream-ordered workspace of 66,560 bytes per value head and
+ * fp32 sums: hT is accurate to 6e-6 of its norm (measured, unit-norm keys of
+ * which none repeats; 3e-5 where all are the same and are overwritten), single
+ * entries to 1e-4 of the root mean square.  The digits do not depend on the
+ * size of v and h0 (2^-30 to 2^30 times the usual).  Supported: d_k == d_v == 128.  Stream-ordered workspace of 66,560 bytes per value head and
  * 64-token chunk (at most tokens / 64 + N chunks), with segments up to half as
- * much again, and 4 bytes per offset; KDA_ERR_NO_MEMORY if it cannot be had.  Bounded waits as in
- * the prefill (kda_device_status).
+ * much again, and 4 bytes per offset; KDA_ERR_NO_MEMORY if it cannot be had.
+ * Bounded waits as in the prefill (kda_device_status).
  */
 int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                       const float* h0, void* o, float* hT, const int32_t* cu_seqlens, const int32_t* slots,
@@ -383,13 +391,17 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * atomics: the same inputs give the same bits.  Three launches (one more with
  * cu_seqlens, two more where long sequences of few heads run in segments);
  * stream-ordered workspace of 263,168 bytes per value head and 64-token chunk,
- * with segments up to a fifth more, and 4 bytes per offset (KDA_ERR_NO_MEMORY if it cannot be had).  Bounded waits as in
- * the forward.  Supported: d_k == d_v == 128.
+ * with segments up to a fifth more, and 4 bytes per offset (KDA_ERR_NO_MEMORY
+ * if it cannot be had).  Bounded waits as in the forward.  dg and dbeta are bf16
+ * whatever the gates are, rounded once from fp32.  A NaN or an infinity in a
+ * token may make the gradients of its whole chunk NaN, beside those that depend
+ * on it.  Supported: d_k == d_v == 128.
  *
  * kda_gdn_chunk_bwd_packed8 -- the same from q, k and v in 8 bits
  * (kda_act_pack8, dense [tokens][HK or HV][128] and [..][4] scales): the
  * gradients at the values that the 8-bit forms stand for.  They are expanded
- * into the workspace (2 more bytes per value).
+ * into the workspace first (one more launch, 2 more bytes per value): what the
+ * 8-bit forms save is memory between the passes, not during this one.
  */
 int kda_gdn_chunk_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
                       const float* h0, const void* dO, const float* dhT, void* dq, void* dk, void* dv,
@@ -440,8 +452,8 @@ int kda_act_unpack8(int count, const void* const* data, const void* const* scale
 /*
  * kda_device_status -- KDA_OK, or KDA_ERR_TIMEOUT if a kernel of this
  * library gave up on a bounded device-side wait since the last call (every
- * wait between the roles of a prefill kernel, and the backward's waits for
- * its tensor-core products, give up after 2 s).  The kernel then winds down
+ * wait between the roles of a prefill or kda_gdn_chunk_* kernel, and the
+ * backward's waits for its tensor-core products, give up after 2 s).  The kernel then winds down
  * and fills the o rows and hT of the affected heads (backward: the dq, dk,
  * dv, dg and dbeta rows of the affected chunk) with NaN (intermediate
  * states, if asked for, are undefined), so a partial result never passes

@@ -1039,11 +1039,16 @@ static DeviceFlags g_back_attr_done;
 // Segments of a call's long sequences, as in the forward: the first launch has
 // 3 segments - 4 CTAs per sequence and value head, or 4 for three segments with
 // the forward chain in two parts.  Whole call, one sequence, in one piece and so,
-// us: 8192 tokens 926 -> 833 at 32 heads (in parts), 840 -> 719 at 24, 644 -> 344
-// at 8, 530 -> 184 at 1 (6 segments 234, 8 203, 16 183, 24 205); 2048 tokens 274
-// -> 279 at 32 heads, 258 -> 247 at 24, 183 -> 136 at 8; 1024 tokens 159 -> 172,
-// 159 -> 169 and 111 -> 109: in one piece below 32 chunks on average, in parts
-// below 40 unless a batch is ragged, whose longest sequence has more.
+// us: 8192 tokens 1009 -> 850 at 32 heads (in parts), 861 -> 724 at 24, 644 ->
+// 334 at 8, 534 -> 186 at 1 (6 segments 234, 8 203, 16 183, 24 205); 2560 tokens
+// 357 -> 339 at 32 heads; 2048 tokens 274 -> 279 at 32 heads, 255 -> 242 at 24,
+// 182 -> 138 at 8; 1024 tokens 159 -> 172, 159 -> 169 and 111 -> 109: in one piece
+// below 32 chunks on average, one sequence of 30 heads and more below 40.  Several
+// with cu_seqlens go in parts from 32 on, though only the device has their
+// lengths: sequences of 16 heads with 4000 + 96 tokens 439 -> 368, 3000 + 1096
+// 367 -> 324, 2500 + 2100 343 -> 314, 2048 + 2048 298 -> 287, but 2300 + 1796 317
+// -> 347, and of 10 heads with 2000 + 1900 + 2244 298 -> 346: one a little
+// below 32 chunks runs in one piece, and what is left of the long one after it.
 static void choose_segments(bk::Args& a, int64_t heads, bool ragged)
 {
     if (heads == 0) return;

@@ -103,7 +103,6 @@ struct Args {
     float *end0, *before_last, *M, *N, *start;
     int pass, segments, min_chunks, n_long;          // at most n_long sequences are in segments
     int HK, HV;
-    float scale;
     uint64_t wait_ns;
 };
 
@@ -476,9 +475,9 @@ static DeviceFlags g_fwd_attr_done;
 // first launch one wave; and at most the square root of the sequences' average
 // of chunks, as a segment costs about 4 us (its transition is joined to the
 // others in turn) and a chunk 2.5 us.  Whole call, one sequence, in one piece
-// and so, us: 8192 tokens 404 -> 313 at 32 heads, 345 -> 152 at 8, 324 -> 129 at
-// 1 (8 segments 136, 16 139); 32768 tokens of 1 head 1233 -> 240; 2048 tokens
-// 117 -> 110 at 32 heads, 101 -> 83 at 8; 1024 tokens 68 -> 74 and 63 -> 67: in
+// and so, us: 8192 tokens 401 -> 318 at 32 heads, 343 -> 153 at 8, 322 -> 128 at
+// 1 (8 segments 136, 16 139); 32768 tokens of 1 head 1231 -> 240; 2048 tokens
+// 117 -> 111 at 32 heads, 100 -> 83 at 8; 1024 tokens 68 -> 74 and 63 -> 67: in
 // one piece below 32 chunks on average (lengths are on the device).  With
 // more heads a batch's longest sequences gained nothing so, even where they
 // took most of the call (16 prompts x 16 heads with one of 4096 tokens, the next
@@ -514,7 +513,6 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
     a.o = (__nv_bfloat16*)o;
     a.HK = HK;
     a.HV = HV;
-    a.scale = scale;
     a.wait_ns = bounded_wait_limit_ns();
     cudaError_t e = once_per_device(g_fwd_attr_done, [](int) {
         return cudaFuncSetAttribute(forward_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fw::SMEM);
