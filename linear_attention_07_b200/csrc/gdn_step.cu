@@ -61,7 +61,13 @@ step_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
     }
     const __nv_bfloat162* v2 = reinterpret_cast<const __nv_bfloat162*>(v + n * v_stride + (int64_t)hv * DV + 4 * cg);
     const float2 v01 = __bfloat1622float2(v2[0]), v23 = __bfloat1622float2(v2[1]);
-    const float a = expf(gate(g, n * HV + hv, f32_gates & G_F32)), b = gate(beta, n * HV + hv, f32_gates & BETA_F32);
+    // one branch per pair of types, so that both loads go out together
+    const int64_t at = n * HV + hv;
+    float a, b;
+    if (f32_gates == 0) a = gate(g, at, false), b = gate(beta, at, false);
+    else if (f32_gates == G_F32) a = gate(g, at, true), b = gate(beta, at, false);
+    else a = gate(g, at, true), b = gate(beta, at, true);
+    a = expf(a);
     __syncthreads();
     if (tid < 32) {
         float acc = 0.f;
