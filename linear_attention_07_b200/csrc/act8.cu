@@ -15,9 +15,9 @@
 // UNITS times 8 channels, all loads first, so that a warp's accesses are whole
 // lines on both sides (16 bytes a lane of bf16, 8 of e4m3) and four lanes share
 // a block; one launch takes up to four tensors, whose rows may be slices of
-// wider rows.  134 M values (16384 tokens of 64 x 128): packed in 75 us, 5.4
-// TB/s, where issuing the conversions is as long as the loads; unpacked in 59 us
-// (67 in a run of calls), 6.9 TB/s, part of it from L2.  With 16 channels a
+// wider rows.  134 M values (16384 tokens of 64 x 128): packed in 73 us, 5.6
+// TB/s, where issuing the conversions is as long as the loads; unpacked in 57 us
+// (67 in a run of calls), 7.1 TB/s, part of it from L2.  With 16 channels a
 // thread, 32 bytes apart, it was 81 and 82 us.
 #include "kda_common.cuh"
 

@@ -30,9 +30,9 @@
 // single rounding would show in dg and dbeta, which are few numbers each from
 // a long sum.
 //
-// 8192 tokens x 32 heads (16 query/key heads): chains 433 us (210 + 9 + 214; in
+// 8192 tokens x 32 heads (16 query/key heads): chains 435 us (215 + 9 + 211; in
 // one piece 560: 3.3 us a forward chunk, 4.2 us a reverse one, which has 96 KB
-// to store, and an SM stores about 32 bytes a cycle), local 338 us (10 us per value head: the pair products and the states'
+// to store, and an SM stores about 32 bytes a cycle), local 342 us (10 us per value head: the pair products and the states'
 // read shared memory at its rate, 128 bytes a cycle, for 7,000 of 18,000 cycles,
 // and the sums over the results take the rest).  The local kernel with one role
 // that did everything in turn took 410 us; with 16 computing warps of 16 columns

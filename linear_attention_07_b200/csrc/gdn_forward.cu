@@ -35,7 +35,7 @@
 // A chunk takes 2.5 us (about 4,500 cycles; 2.8 us when more than half of the
 // SMs run one, 2.2 us without outputs), whatever its head: a chain of two
 // products of 0.4 us each, four passes between tensor memory and registers and
-// the splits.  4 x 16384 tokens x 32 heads: 750 us on 128 SMs.  History of a
+// the splits.  4 x 16384 tokens x 32 heads: 742 us on 128 SMs.  History of a
 // chunk at 8192 tokens x 32 heads: 3.4 us with three products in turn (T R after
 // V - K S), 3.3 with stages freed late, 2.6 with W formed before.
 #include <algorithm>

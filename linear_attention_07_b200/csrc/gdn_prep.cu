@@ -12,7 +12,7 @@
 // fp32 accuracy (three tf32 products each): with fp32 FMAs those read shared
 // memory once per multiply, which bound the kernel.
 //
-// 84 us for 8192 tokens x 32 heads, 618 us for 4 x 16384 x 32 (a record of
+// 85 us for 8192 tokens x 32 heads, 611 us for 4 x 16384 x 32 (a record of
 // 66,560 bytes each: 3.7 TB/s).  Bound by a CTA's 15 us of dependent phases
 // against six CTAs per SM: issue slots are half full, shared memory's port as
 // much, no phase above 15 % of the time.  Four CTAs of 52 KB took 818 us; with
