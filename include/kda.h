@@ -356,20 +356,22 @@ int kda_verify_fwd(const void* q, const void* k, const void* v, const void* g,
  *   slots name the rows of both h0 and hT.  A padded sequence starts from
  *   zero and keeps no state; an empty one copies its h0 row (or zeros).
  * Tokens behind a sequence's end inside its last 64-token chunk count as zero
- * whatever they hold.  A NaN or an infinity in a token of a sequence makes o NaN
- * from the start of the token's 64-token chunk on, and hT, in the value heads
- * that it enters; other sequences stay as they are.  Two launches: every chunk's state-free part for all
- * chunks at once, then one CTA per sequence and value head along the chunks.
- * Long sequences of few heads (32 chunks on average, at least three CTAs per
- * sequence and head at once) are cut into segments instead, joined as
- * kda_state_chain joins them: four launches.  K, Q and V enter
- * the products as bf16, the state and what is computed as pairs of bf16 with
- * fp32 sums: hT is accurate to 6e-6 of its norm (measured, unit-norm keys of
+ * whatever they hold.  A NaN or an infinity in a token of a sequence may make o
+ * NaN from the start of the token's 64-token chunk on, and hT, in the value heads
+ * that it enters; other sequences stay as they are.  Two launches: every chunk's
+ * state-free part for all chunks at once, then one CTA per sequence and value
+ * head along the chunks.  Long sequences of few heads (32 chunks on average, at
+ * least three CTAs per sequence and head at once) are cut into segments instead,
+ * joined as kda_state_chain joins them: four launches.  cu_seqlens of 32
+ * sequences and more take one more, which puts the offsets in order.  K, Q and V
+ * enter the products as bf16, the state and what is computed as pairs of bf16
+ * with fp32 sums: hT is accurate to 6e-6 of its norm (measured, unit-norm keys of
  * which none repeats; 3e-5 where all are the same and are overwritten), single
  * entries to 1e-4 of the root mean square.  The digits do not depend on the
- * size of v and h0 (2^-30 to 2^30 times the usual).  Supported: d_k == d_v == 128.  Stream-ordered workspace of 66,560 bytes per value head and
- * 64-token chunk (at most tokens / 64 + N chunks), with segments up to half as
- * much again, and 4 bytes per offset; KDA_ERR_NO_MEMORY if it cannot be had.
+ * size of v and h0 (2^-30 to 2^30 times the usual).  Supported: d_k == d_v ==
+ * 128.  Stream-ordered workspace of 66,560 bytes per value head and 64-token
+ * chunk (at most tokens / 64 + N chunks), with segments up to half as much again,
+ * and 4 bytes per offset; KDA_ERR_NO_MEMORY if it cannot be had.
  * Bounded waits as in the prefill (kda_device_status).
  */
 int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta,
@@ -389,7 +391,8 @@ int kda_gdn_chunk_fwd(const void* q, const void* k, const void* v, const void* g
  * Tokens before the first sequence and behind the last get zero gradients.  A
  * write strength smaller than 2^-30 counts as 2^-30 (with its sign).  No
  * atomics: the same inputs give the same bits.  Three launches (one more with
- * cu_seqlens, two more where long sequences of few heads run in segments);
+ * cu_seqlens, another with those of 32 sequences and more, two more where long
+ * sequences of few heads run in segments);
  * stream-ordered workspace of 263,168 bytes per value head and 64-token chunk,
  * with segments up to a fifth more, and 4 bytes per offset (KDA_ERR_NO_MEMORY
  * if it cannot be had).  Bounded waits as in the forward.  dg and dbeta are bf16

@@ -1024,7 +1024,9 @@ struct Outside {
 };
 __global__ void outside_kernel(const Outside z, const int* __restrict__ cu, int n_seq, int64_t tokens)
 {
-    const int64_t a = min((int64_t)max(cu[0], 0), tokens), b = min(max((int64_t)cu[n_seq], a), tokens);
+    const int lane = (int)(threadIdx.x & 31);         // fewer than 32 sequences: in any order; else in order
+    const int most = __reduce_max_sync(0xffffffffu, n_seq >= 32 ? cu[n_seq] : lane <= n_seq ? cu[lane] : 0);
+    const int64_t a = min((int64_t)max(cu[0], 0), tokens), b = min(max((int64_t)most, a), tokens);
     const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
     for (int i = 0; i < 5; ++i) {
         for (int64_t e = at; e < a * z.row[i]; e += step) z.p[i][e] = __float2bfloat16_rn(0.f);
@@ -1132,8 +1134,9 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         q_stride = k_stride = (int64_t)HK * D;
         v_stride = (int64_t)HV * D;
     }
-    const Seqs given = a.seqs;
-    if (cu && N > 0) a.seqs.cu = reinterpret_cast<const int*>(take(((size_t)N + 1) * sizeof(int)));
+    Seqs given = a.seqs;
+    int* offsets = cu && N > 0 ? reinterpret_cast<int*>(take(((size_t)N + 1) * sizeof(int))) : nullptr;
+    if (offsets) a.seqs.cu = offsets;
     a.h0 = h0;
     a.dhT = dhT;
     a.dh0 = dh0;
@@ -1165,18 +1168,19 @@ cudaError_t gdn_backward_launch(const void* q, const void* k, const void* v, con
         (!make_token_map(&maps.q, q, tokens, (int64_t)HK * D, q_stride) || !make_token_map(&maps.k, k, tokens, (int64_t)HK * D, k_stride) ||
          !make_token_map(&mv, v, tokens, row, v_stride) || !make_token_map(&maps.dO, dO, tokens, row, row)))
         e = cudaErrorInvalidValue;
-    if (e == cudaSuccess && N > 0)
-        e = prep_launch(maps.q, maps.k, g, beta, given, cu ? const_cast<int*>(a.seqs.cu) : nullptr, const_cast<uint8_t*>(a.rec),
-                        scale, HK, HV, f32_gates, true, stream);
+    if (e == cudaSuccess && offsets) e = order_launch(given, offsets, stream);
     if (e == cudaSuccess && cu) {
         const int64_t rows[5] = {(int64_t)HK * D, (int64_t)HK * D, (int64_t)HV * D, HV, HV};
         Outside z = {};
         void* out[5] = {dq, dk, dv, dg, dbeta};
         for (int i = 0; i < 5; ++i) z.p[i] = (__nv_bfloat16*)out[i], z.row[i] = rows[i];
-        outside_kernel<<<64, 256, 0, stream>>>(z, a.seqs.cu, N, tokens);
+        outside_kernel<<<64, 256, 0, stream>>>(z, given.cu, N, tokens);
         note_launches(1);
         e = cudaGetLastError();
     }
+    if (e == cudaSuccess && N > 0)
+        e = prep_launch(maps.q, maps.k, g, beta, given, offsets, const_cast<uint8_t*>(a.rec),
+                        scale, HK, HV, f32_gates, true, stream);
     auto chains = [&](int pass, int64_t blocks) {
         a.pass = pass;
         chains_kernel<<<(unsigned)blocks, NT, SMEM, stream>>>(maps.q, maps.k, mv, maps.dO, a);

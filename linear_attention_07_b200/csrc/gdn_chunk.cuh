@@ -333,7 +333,9 @@ __device__ __forceinline__ void tma_store_2d(const void* map, int x, int y, uint
 // without (stores).
 bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t cols, int64_t stride, bool store = false);
 
-// offsets: where the sequences' offsets go ([n_seq + 1]) that the kernels behind it take for cu; null without cu.
+// offsets: where the sequences' offsets go in order ([n_seq + 1]), which the kernels behind the prep take for cu; null
+// without cu.  order_launch puts those of 32 sequences or more there and into seqs (one launch), prep_launch fewer.
+cudaError_t order_launch(Seqs& seqs, int* offsets, cudaStream_t stream);
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
                         int* offsets, uint8_t* rec, float scale, int HK, int HV, int f32_gates, bool backward, cudaStream_t stream);
 

@@ -21,22 +21,14 @@ struct Seqs {
 
 // The caller's offsets may hold anything.  Offset n counts as the largest of
 // cu[0 .. n], cut to [0, tokens]: ranges neither overlap nor go back, whatever
-// the array holds.  The prep kernel leaves the offsets so for the kernels
-// behind it.
+// the array holds.  prep_launch leaves the offsets so for the kernels behind
+// it.
 __device__ __forceinline__ int cut_offset(const Seqs& s, int v)
 {
     return v < 0 ? 0 : v > s.tokens ? (int)s.tokens : v;
 }
-// By whole warps.
-__device__ __forceinline__ int offset_of(const Seqs& s, int n)
-{
-    int m = 0;
-#pragma unroll 8
-    for (int i = (int)(threadIdx.x & 31); i <= n; i += 32) m = max(m, s.cu[i]);
-    return cut_offset(s, __reduce_max_sync(0xffffffffu, m));
-}
 
-// Token range of sequence n, by offsets that the prep kernel left (or of a call without tokens).
+// Token range of sequence n, by offsets that are in order.
 __device__ __forceinline__ void seq_range(const Seqs& s, int n, int& begin, int& end)
 {
     if (s.cu) {

@@ -542,9 +542,10 @@ cudaError_t gdn_forward_launch(const void* q, const void* k, const void* v, cons
             a.N = a.M + heads * between * state;
             a.start = a.N + heads * between * state;
         }
-        int* kept = cu ? reinterpret_cast<int*>(rec + rec_bytes + states * sizeof(float)) : nullptr;
-        e = prep_launch(mq, mk, g, beta, a.seqs, kept, rec, scale, HK, HV, f32_gates, false, stream);
-        a.seqs.cu = kept;
+        int* in_order = cu ? reinterpret_cast<int*>(rec + rec_bytes + states * sizeof(float)) : nullptr;
+        if (cu) e = order_launch(a.seqs, in_order, stream);
+        if (e == cudaSuccess) e = prep_launch(mq, mk, g, beta, a.seqs, in_order, rec, scale, HK, HV, f32_gates, false, stream);
+        a.seqs.cu = in_order;
     }
     a.rec = rec;
     auto launch = [&](int pass, int64_t blocks) {

@@ -142,58 +142,50 @@ __device__ __forceinline__ void join(const float* x00, float* a10, int ar, const
     __syncthreads();
 }
 
-// slot_chunk by the caller's offsets, which may go back (offset_of).  As they
-// hardly ever do, the sequence is looked for as if they did not, and the result
-// checked: of fewer than 32 sequences all offsets are looked at anyway, of more
-// what is found is compared with all before it.  Where it does not hold, all
-// sequences in turn, 32 at a time.
-struct Found {
-    int n, begin, end;
-};
-__device__ __noinline__ Found walk_sequences(const int* cu, int n_seq, int tokens, int slot)
-{
-    const int lane = (int)(threadIdx.x & 31);
-    Found f = {0, 0, 0};
-    for (int first = 0, most = 0; first < n_seq; first += 32) {
-        const int i = first + lane, left = n_seq - first;
-        int m = lane < left ? max(most, min(cu[i], tokens)) : most;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) m = max(m, __shfl_sync(0xffffffffu, m, max(lane - off, 0)));
-        const int e = lane < left ? max(m, min(cu[i + 1], tokens)) : m;
-        const int count = __popc(__ballot_sync(0xffffffffu, lane < left && m / C + i <= slot));
-        if (count > 0 || first == 0) {                // none of the first: in front of all sequences
-            f.n = first + max(count - 1, 0);
-            f.begin = __shfl_sync(0xffffffffu, m, max(count - 1, 0));
-            f.end = __shfl_sync(0xffffffffu, e, max(count - 1, 0));
-        }
-        if (count < 32) break;
-        most = __shfl_sync(0xffffffffu, m, 31);
-    }
-    return f;
-}
+// slot_chunk by the caller's offsets of fewer than 32 sequences, which may go
+// back: offset n is the largest up to n.  A lane has each of them, so that they
+// are put in order only where they are not.  (For more, order_kernel does it: to
+// look at all offsets in every CTA made calls of 100 and 1000 sequences 4 % longer.)
 __device__ __forceinline__ bool given_slot_chunk(const Seqs& s, int slot, int& n, int& chunk, int& begin, int& end)
 {
-    const int lane = (int)(threadIdx.x & 31);
-    bool right = true;
-    if (s.cu && s.n_seq > 1 && s.n_seq < 32) {        // a lane for each offset
-        const int v = lane <= s.n_seq ? s.cu[lane] : 0x7fffffff, b = cut_offset(s, v);
-        right = __all_sync(0xffffffffu, v <= __shfl_down_sync(0xffffffffu, v, 1));
-        n = max(__popc(__ballot_sync(0xffffffffu, lane < s.n_seq && b / C + lane <= slot)) - 1, 0);
-        begin = __shfl_sync(0xffffffffu, b, n);
-        end = __shfl_sync(0xffffffffu, b, n + 1);
+    if (s.n_seq == 1) {
+        n = 0;
+        seq_range(s, 0, begin, end);
     } else {
-        n = find_sequence(s, slot);
-        seq_range(s, n, begin, end);
-        if (s.cu && s.n_seq > 1)
-            right = offset_of(s, n) == begin && (n == 0 || begin / C + n <= slot) && (n + 1 == s.n_seq || end / C + n + 1 > slot);
-    }
-    if (!right) {
-        const Found f = walk_sequences(s.cu, s.n_seq, (int)s.tokens, slot);
-        n = f.n, begin = f.begin, end = f.end;
+        const int lane = (int)(threadIdx.x & 31);
+        int v = cut_offset(s, lane <= s.n_seq ? s.cu[lane] : 0x7fffffff);
+        if (!__all_sync(0xffffffffu, v <= __shfl_down_sync(0xffffffffu, v, 1)))
+#pragma unroll 1
+            for (int off = 1; off < 32; off <<= 1) v = max(v, __shfl_sync(0xffffffffu, v, max(lane - off, 0)));
+        n = max(__popc(__ballot_sync(0xffffffffu, lane < s.n_seq && v / C + lane <= slot)) - 1, 0);
+        begin = __shfl_sync(0xffffffffu, v, n);
+        end = __shfl_sync(0xffffffffu, v, n + 1);
     }
     return chunk_of(slot, n, begin, end, chunk);
 }
 }  // namespace prep
+
+// The caller's offsets in order: offset n is the largest of cu[0 .. n], cut to [0, tokens].  One CTA: 3 us up to 1000
+// sequences, 14 us for 16000.
+constexpr int ORDER_NT = 1024;
+__global__ void __launch_bounds__(ORDER_NT) order_kernel(const Seqs s, int* __restrict__ offsets)
+{
+    __shared__ int most[2][ORDER_NT / 32];            // of each warp; two sets in turn: one barrier a pass
+    const int lane = (int)(threadIdx.x & 31), warp = (int)(threadIdx.x >> 5);
+    int before = 0;
+    for (int first = 0, set = 0; first <= s.n_seq; first += ORDER_NT, set ^= 1) {
+        const int i = first + (int)threadIdx.x;
+        int v = i <= s.n_seq ? cut_offset(s, s.cu[i]) : 0;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) v = max(v, __shfl_sync(0xffffffffu, v, max(lane - off, 0)));
+        if (lane == 31) most[set][warp] = v;
+        __syncthreads();
+        const int w = most[set][lane];
+        v = max(v, max(before, __reduce_max_sync(0xffffffffu, lane < warp ? w : 0)));
+        if (i <= s.n_seq) offsets[i] = v;
+        before = max(before, __reduce_max_sync(0xffffffffu, w));
+    }
+}
 
 __global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
@@ -217,14 +209,12 @@ prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     const int64_t slot = blockIdx.x / HV;             // heads next to one another: they share K and Q in L2
     const int hv = (int)(blockIdx.x % HV), hk = hv / (HV / HK);
     int n, chunk, begin, end;
-    if (warp == 3 && offsets && blockIdx.x < (unsigned)seqs.n_seq) {         // there are as many slots as sequences
-        n = (int)blockIdx.x;
-        begin = offset_of(seqs, n);
-        if (lane == 0) offsets[n] = begin;
-        if (lane == 0 && n + 1 == seqs.n_seq) offsets[n + 1] = max(begin, cut_offset(seqs, seqs.cu[n + 1]));
+    const bool has_tokens = offsets ? given_slot_chunk(seqs, (int)slot, n, chunk, begin, end) : slot_chunk(seqs, slot, n, chunk, begin, end);
+    if (offsets && hv == 0 && tid == 0 && slot == begin / C + n) {           // every sequence has this slot, if an empty one
+        offsets[n] = begin;
+        if (n + 1 == seqs.n_seq) offsets[n + 1] = end;
     }
-    __syncwarp();
-    if (!given_slot_chunk(seqs, (int)slot, n, chunk, begin, end)) return;
+    if (!has_tokens) return;
     const int t0 = begin + chunk * C, nv = min(C, end - t0);
     uint8_t* rec = rec_all + (slot * HV + hv) * REC_BYTES;
     const uint32_t tile = smem_u32(sm), full = smem_u32(&bars[0]), done = smem_u32(&bars[1]);
@@ -500,6 +490,15 @@ bool make_token_map(CUtensorMap* map, const void* base, int64_t tokens, int64_t 
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaError_t order_launch(Seqs& seqs, int* offsets, cudaStream_t stream)
+{
+    if (seqs.n_seq < 32) return cudaSuccess;
+    order_kernel<<<1, ORDER_NT, 0, stream>>>(seqs, offsets);
+    note_launches(1);
+    seqs.cu = offsets;
+    return cudaGetLastError();
+}
+
 static DeviceFlags g_prep_attr_done;
 
 cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void* g, const void* beta, const Seqs& seqs,
@@ -509,6 +508,7 @@ cudaError_t prep_launch(const CUtensorMap& mq, const CUtensorMap& mk, const void
         return cudaFuncSetAttribute(prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prep::SMEM);
     });
     if (e != cudaSuccess) return e;
+    if (seqs.cu == offsets) offsets = nullptr;        // in order already
     prep_kernel<<<(unsigned)(slot_count(seqs) * HV), prep::NT, prep::SMEM, stream>>>(
         mq, mk, g, beta, seqs, offsets, rec, scale, HK, HV, f32_gates, backward, bounded_wait_limit_ns());
     note_launches(1);
