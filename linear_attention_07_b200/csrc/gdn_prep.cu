@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(ORDER_NT) order_kernel(const Seqs s, int* __re
 __global__ void __launch_bounds__(prep::NT, 6)
 prep_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const void* __restrict__ g,
             const void* __restrict__ beta, const Seqs seqs, int* __restrict__ offsets, uint8_t* __restrict__ rec_all,
-            float scale, int HK, int HV,
-            int f32_gates, bool backward, uint64_t wait_ns)
+            float scale, int HK, int HV, int f32_gates, bool backward, uint64_t wait_ns)
 {
     using namespace prep;
     using namespace tc;
